@@ -15,6 +15,9 @@
  *             fsdp_adamw_pack_groups, fsdp_amax_groups,
  *             fsdp_pack_allgather_fp8_groups, fsdp_step_group_set
  *             AdamW, amax and copy-ins of many groups, one launch each
+ *   Muon      fsdp_muon_momentum, fsdp_muon_reduce_momentum,
+ *             fsdp_muon_update
+ *             the step of matrix parameters by an orthogonalised momentum
  *
  * and around them: the reduce-scatter copy-in (fsdp_pack_reduce_scatter),
  * fp32 contributions (fsdp_reduce_shard_f32), the FP8 E4M3 all-gather
@@ -530,6 +533,65 @@ fsdp_status fsdp_step_group_set(const fsdp_group_set *set,
                                 const fsdp_adamw_hparams_t *hp, int64_t step,
                                 uint32_t flags, int32_t timed_kernel,
                                 void *const *timing_events, void *stream);
+
+/* ---- Muon: the step of matrix parameters --------------------------------- */
+
+/* Muon moves a matrix by its orthogonalised momentum.  On Shard(0) shards the
+ * step is: momentum and the copy-in of its bf16 update, an all-gather of the
+ * updates (and fsdp_unpack_allgather into full matrices), orthogonalisation
+ * of the full matrices, and the update of the fp32 master shards with their
+ * copy-in.  A plan over the group's matrices runs it; norms, biases and
+ * embeddings stay with AdamW on a plan of their own (both bind the shards
+ * that the group's reduction wrote).  The momentum is the plan's exp_avg;
+ * exp_avg_sq is not used.  [ST] fully_shard paragraph (the optimizer works on
+ * the shards). */
+typedef struct fsdp_muon_hparams_t {
+    double lr;            /* fsdp_muon_update                                    */
+    double momentum;      /* mu, in [0, 1): the two momentum calls               */
+    double weight_decay;  /* decoupled, fsdp_muon_update                         */
+    int32_t nesterov;     /* 0 or 1: the two momentum calls                      */
+    int32_t reserved;     /* 0                                                   */
+} fsdp_muon_hparams_t;
+
+/* Momentum on the bound shards and the copy-in of the update.  Per valid
+ * element, each operation one fp32 rounding (1 - mu rounded once from fp64):
+ *     m = mu*m + (1-mu)*g;   u = nesterov ? mu*m + (1-mu)*g : m
+ * m (exp_avg) in place, ag_in[shard_offset + i] = bf16(u) to nearest even, 0
+ * in the piece's padding and any alignment gap.  m must be zero before the
+ * first step.
+ *   ag_in  [S] bf16, may be row `rank` of the all-gather buffer; must not
+ *          overlap the bound shards
+ * Needs FSDP_ROLE_GRAD | FSDP_ROLE_EXP_AVG.
+ * Errors: FSDP_E_INVAL (null ag_in with S > 0, null hparams, momentum outside
+ *         [0, 1), overlap), FSDP_E_ALIGN, FSDP_E_STATE, FSDP_E_HIP. */
+fsdp_status fsdp_muon_momentum(const fsdp_plan *plan, uint16_t *ag_in,
+                               const fsdp_muon_hparams_t *hp, void *stream);
+
+/* fsdp_reduce_shard and fsdp_muon_momentum in one pass: the gradient is the
+ * mean of the N rows of rs_in and is not stored.  Bit-identical to the two
+ * calls.
+ *   rs_in  [N, S] bf16 contributions, as for fsdp_reduce_shard
+ *   ag_in  [S] bf16; must not overlap rs_in or the bound shards
+ * Needs FSDP_ROLE_EXP_AVG.  Errors: as fsdp_muon_momentum. */
+fsdp_status fsdp_muon_reduce_momentum(const fsdp_plan *plan, const uint16_t *rs_in,
+                                      uint16_t *ag_in, const fsdp_muon_hparams_t *hp,
+                                      void *stream);
+
+/* Update of the master shards by the orthogonalised updates, and the copy-in
+ * of the new master.  Per valid element of parameter i, each operation one
+ * fp32 rounding (1 - lr*wd and lr rounded once from fp64):
+ *     p = p*(1 - lr*wd) - (lr*scales[i])*o
+ *   upd     [S] bf16 segment of updates o (each matrix orthogonalised on one
+ *           rank and its rows sent back); or NULL: o is this rank's rows of
+ *           the bound full tensors (every rank orthogonalised every matrix)
+ *   ag_in   [S] bf16 copy-in as fsdp_pack_allgather writes it, or NULL for
+ *           none; must not overlap upd, scales or the bound tensors
+ *   scales  device array of n_params fp32 factors, or NULL for 1
+ * Needs FSDP_ROLE_MASTER, and FSDP_ROLE_FULL where upd is NULL.
+ * Errors: FSDP_E_INVAL (null hparams, lr or weight_decay not finite, overlap),
+ *         FSDP_E_ALIGN, FSDP_E_STATE, FSDP_E_HIP. */
+fsdp_status fsdp_muon_update(const fsdp_plan *plan, const uint16_t *upd, uint16_t *ag_in,
+                             const float *scales, const fsdp_muon_hparams_t *hp, void *stream);
 
 /* ---- CPU offload --------------------------------------------------------- */
 

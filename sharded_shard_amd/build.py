@@ -32,21 +32,25 @@ SOURCES = [
     ("capi.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
     ("host_adamw.cpp", ["-x", "c++", "-ffp-contract=off", "-fno-fast-math", "-pthread"]),
     ("reshard.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
+    ("muon.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
     ("copy.hip", ["-x", "hip"] + DEVICE),
     ("pack.hip", ["-x", "hip"] + DEVICE),
     ("reduce.hip", ["-x", "hip"] + DEVICE),
     ("step.hip", ["-x", "hip"] + DEVICE),
+    ("muon.hip", ["-x", "hip"] + DEVICE),
 ]
+# the kernels of the sharded step, which the committed traffic counters cover
+STEP_KERNEL_SOURCES = ["copy.hip", "pack.hip", "reduce.hip", "step.hip"]
 KERNEL_SOURCES = [n for n, _ in SOURCES if n.endswith(".hip")]
 
 
 def kernel_sources_sha256() -> str:
-    """sha256 over the device sources (every .hip file and the headers they
-    include), in name order: identifies the kernels a measurement was taken
-    on."""
+    """sha256 over the sharded step's device sources (its .hip files and the
+    headers they include), in name order: identifies the kernels a measurement
+    was taken on."""
     import hashlib
     h = hashlib.sha256()
-    for name in sorted(KERNEL_SOURCES + ["device.hpp", "rows.hpp", "launch.hpp", "plan.hpp"]):
+    for name in sorted(STEP_KERNEL_SOURCES + ["device.hpp", "rows.hpp", "launch.hpp", "plan.hpp"]):
         h.update(name.encode() + b"\0")
         with open(os.path.join(SRC, name), "rb") as f:
             h.update(f.read())

@@ -74,6 +74,11 @@ class AdamwHparams(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
 
 
+class MuonHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("nesterov", _i32), ("reserved", _i32)]
+
+
 class FsdpError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} [{status}]")
@@ -143,6 +148,9 @@ _SIGS = {
     "fsdp_adamw_pack_groups": (_i32, [_P, ctypes.POINTER(AdamwHparams), _i64, _P, _P]),
     "fsdp_step_group_set": (_i32, [_P, _PP, _P, _PP, ctypes.POINTER(AdamwHparams), _i64,
                                    ctypes.c_uint32, _i32, _PP, _P]),
+    "fsdp_muon_momentum": (_i32, [_P, _P, ctypes.POINTER(MuonHparams), _P]),
+    "fsdp_muon_reduce_momentum": (_i32, [_P, _P, _P, ctypes.POINTER(MuonHparams), _P]),
+    "fsdp_muon_update": (_i32, [_P, _P, _P, _P, ctypes.POINTER(MuonHparams), _P]),
     "fsdp_check_stream": (_i32, [_P]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -623,6 +631,42 @@ class StepGroupSetCall:
         _check(lib.fsdp_step_group_set(self._set, self._rs, self._arena, self._ag_out,
                                        ctypes.byref(self._hp), step, self.flags, timed_kernel,
                                        ev, self._stream), "fsdp_step_group_set")
+
+
+# ---- Muon ---------------------------------------------------------------------------
+
+def fsdp_muon_momentum(plan, ag_in, momentum: float, nesterov: bool = True, stream=None) -> None:
+    hp = MuonHparams(0.0, momentum, 0.0, 1 if nesterov else 0, 0)
+    d = _dims(plan)
+    a = _dev(ag_in, 2 * d[1], "ag_in") if d else addr(ag_in)
+    _check(lib.fsdp_muon_momentum(plan, a, ctypes.byref(hp), stream_handle(stream)),
+           "fsdp_muon_momentum")
+
+
+def fsdp_muon_reduce_momentum(plan, rs_in, ag_in, momentum: float, nesterov: bool = True,
+                              stream=None) -> None:
+    hp = MuonHparams(0.0, momentum, 0.0, 1 if nesterov else 0, 0)
+    d = _dims(plan)
+    r = _dev(rs_in, 2 * d[0] * d[1], "rs_in") if d else addr(rs_in)
+    a = _dev(ag_in, 2 * d[1], "ag_in") if d else addr(ag_in)
+    _check(lib.fsdp_muon_reduce_momentum(plan, r, a, ctypes.byref(hp), stream_handle(stream)),
+           "fsdp_muon_reduce_momentum")
+
+
+def fsdp_muon_update(plan, upd, ag_in, lr: float, weight_decay: float, scales=None,
+                     stream=None) -> None:
+    """upd: the [S] segment of orthogonalised updates, or None for this rank's
+    rows of the bound full tensors; ag_in: the copy-in segment or None; scales:
+    n_params fp32 or None."""
+    hp = MuonHparams(lr, 0.0, weight_decay, 0, 0)
+    d = _dims(plan)
+    if d:
+        u, a = _dev(upd, 2 * d[1], "upd"), _dev(ag_in, 2 * d[1], "ag_in")
+        sc = _dev(scales, 4 * d[2], "scales")
+    else:
+        u, a, sc = addr(upd), addr(ag_in), addr(scales)
+    _check(lib.fsdp_muon_update(plan, u, a, sc, ctypes.byref(hp), stream_handle(stream)),
+           "fsdp_muon_update")
 
 
 def fsdp_check_stream(stream=None) -> None:

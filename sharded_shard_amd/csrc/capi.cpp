@@ -18,25 +18,7 @@
 
 #include "../../include/fsdp_shard.h"
 #include "launch.hpp"
-#include "plan.hpp"
-
-
-struct fsdp_plan {
-    fsdp::Layout L;
-    std::vector<fsdp::DevEntry> host_entries;
-    int32_t bound = 0;
-    int device = -1;
-    bool tiles_uploaded = false;  // the tile tables below hold the plan's tiles
-    char *dmem = nullptr;  // one device block: entries, then the tile tables
-    fsdp::DevEntry *d_entries = nullptr;
-    fsdp::PackTile *d_pack = nullptr;
-    fsdp::PackTile *d_rspack = nullptr;
-    fsdp::UnpackTile *d_unpack = nullptr;
-    fsdp::ReduceTile *d_reduce = nullptr;
-    fsdp::EwTile *d_adamw = nullptr;
-    fsdp::EwTile *d_full = nullptr;
-};
-
+#include "state.hpp"
 // Bound plans whose AdamW and copy-in run as one launch each: the plans'
 // entry records concatenated (group g's entries from ent_off[g]) and their
 // AdamW and copy-in tiles re-indexed into that table and into one copy-in
@@ -125,11 +107,13 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     if (p->dmem != nullptr && dev != p->device)
         return fail(FSDP_E_STATE, c + ": plan already bound on another device");
     const size_t n = p->L.entries.size();
+    std::vector<int64_t> own;
+    for (const fsdp_shard_entry_t &t : p->L.entries) own.push_back(t.row_begin * t.cols);
     struct Table {
         void **dst;
         const void *src;
         size_t bytes;
-    } tabs[7] = {
+    } tabs[8] = {
         {reinterpret_cast<void **>(&p->d_entries), nullptr, n * sizeof(fsdp::DevEntry)},
         {reinterpret_cast<void **>(&p->d_pack), p->L.pack.data(),
          p->L.pack.size() * sizeof(fsdp::PackTile)},
@@ -143,6 +127,7 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
          p->L.adamw.size() * sizeof(fsdp::EwTile)},
         {reinterpret_cast<void **>(&p->d_full), p->L.full.data(),
          p->L.full.size() * sizeof(fsdp::EwTile)},
+        {reinterpret_cast<void **>(&p->d_own), own.data(), own.size() * sizeof(int64_t)},
     };
     const bool first = p->dmem == nullptr;
     if (first) {
@@ -166,7 +151,7 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     // (hot calls then fail with FSDP_E_STATE) rather than half-updated.
     const int32_t prev = p->bound;
     p->bound = 0;
-    const int n_tabs = p->tiles_uploaded ? 1 : 7;
+    const int n_tabs = p->tiles_uploaded ? 1 : 8;
     for (int k = 0; k < n_tabs; ++k) {
         if (tabs[k].bytes == 0) continue;
         const void *src = k == 0 ? static_cast<const void *>(ents.data()) : tabs[k].src;
@@ -187,6 +172,10 @@ namespace fsdp {
 // Error reporting and AdamW scalars shared with the other translation units.
 fsdp_status set_error(fsdp_status s, const std::string &msg) { return fail(s, msg); }
 fsdp_status set_hip_error(hipError_t e, const char *what) { return hip_fail(e, what); }
+fsdp_status check_roles(const fsdp_plan *p, int32_t roles, const char *call) {
+    return need_roles(p, roles, call);
+}
+fsdp_status check_plan_device(const fsdp_plan *p) { return check_device(p); }
 
 // Fault injection, to test how callers see a failed launch without breaking a
 // kernel.  With FSDP_FAULT=launch in the environment every library launch
@@ -552,6 +541,12 @@ fsdp_status launched(hipError_t e, const char *call) {
 }
 
 }  // namespace
+
+namespace fsdp {
+fsdp_status check_segment(const fsdp_plan *p, const void *buf, const char *call, const char *name) {
+    return check_buf(p, buf, call, name);
+}
+}  // namespace fsdp
 
 extern "C" {
 

@@ -42,7 +42,12 @@ class ShardedGroup:
     def __init__(self, shapes: Sequence[Sequence[int]], world: int, rank: int,
                  align_elems: int = 1, device: str = "cuda",
                  full_arena: Optional[torch.Tensor] = None, bind: bool = True,
-                 stream=None):
+                 stream=None, optimizer: str = "adamw"):
+        """optimizer: "adamw", or "muon" for a group of matrices, whose momentum
+        is ``m_flat`` and which has no ``v_flat``."""
+        if optimizer not in ("adamw", "muon"):
+            raise ValueError(f"optimizer must be 'adamw' or 'muon', not {optimizer!r}")
+        self.optimizer = optimizer
         self.shapes = [tuple(int(d) for d in s) for s in shapes]
         rc = [split_shape(s) for s in self.shapes]
         self.rows = [r for r, _ in rc]
@@ -83,7 +88,8 @@ class ShardedGroup:
 
     def allocate(self, full: bool = True) -> None:
         mk = lambda: torch.zeros(self.shard_space, dtype=torch.float32, device=self.device)
-        self.master_flat, self.grad_flat, self.m_flat, self.v_flat = mk(), mk(), mk(), mk()
+        self.master_flat, self.grad_flat, self.m_flat = mk(), mk(), mk()
+        self.v_flat = mk() if self.optimizer == "adamw" else None
         if full and self.full_flat is None:
             self.full_flat = torch.zeros(self.full_space, dtype=torch.int16, device=self.device)
         if self.full_flat is not None and self.full_flat.numel() < self.full_space:
@@ -98,6 +104,8 @@ class ShardedGroup:
         return self.full_flat[o:o + self.rows[i] * self.cols[i]].view(self.rows[i], self.cols[i])
 
     def _ptrs(self, flat):
+        if flat is None:
+            return None
         return [self.shard_view(flat, i).data_ptr() if self.entries[i].valid_numel else 0
                 for i in range(len(self.entries))]
 
@@ -198,6 +206,21 @@ class ShardedGroup:
         """Fused reduce -> AdamW -> pack (bit-identical to the three calls)."""
         capi.fsdp_step_shard(self.plan, rs_in, ag_in, lr, beta1, beta2, eps, weight_decay, step,
                              capi.FSDP_STEP_WRITE_GRAD if write_grad else 0, stream)
+
+    def muon_momentum(self, ag_in, momentum: float, nesterov: bool = True, stream=None) -> None:
+        """m = mu m + (1-mu) grad, and the bf16 update into ``ag_in`` [S]."""
+        capi.fsdp_muon_momentum(self.plan, ag_in, momentum, nesterov, stream)
+
+    def muon_reduce_momentum(self, rs_in, ag_in, momentum: float, nesterov: bool = True,
+                             stream=None) -> None:
+        """``muon_momentum`` of the mean of ``rs_in``'s N rows, in one pass."""
+        capi.fsdp_muon_reduce_momentum(self.plan, rs_in, ag_in, momentum, nesterov, stream)
+
+    def muon_update(self, upd, ag_in, lr: float, weight_decay: float, scales=None,
+                    stream=None) -> None:
+        """Master update by the orthogonalised ``upd`` [S] (None: this rank's rows
+        of the full tensors) and its bf16 copy-in into ``ag_in`` (None: none)."""
+        capi.fsdp_muon_update(self.plan, upd, ag_in, lr, weight_decay, scales, stream)
 
     def close(self) -> None:
         if self.plan is not None:
