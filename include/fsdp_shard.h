@@ -16,7 +16,7 @@
  *             fsdp_pack_allgather_fp8_groups, fsdp_step_group_set
  *             AdamW, amax and copy-ins of many groups, one launch each
  *   Muon      fsdp_muon_momentum, fsdp_muon_reduce_momentum,
- *             fsdp_muon_update
+ *             fsdp_ortho_execute, fsdp_muon_update
  *             the step of matrix parameters by an orthogonalised momentum
  *
  * and around them: the reduce-scatter copy-in (fsdp_pack_reduce_scatter),
@@ -592,6 +592,69 @@ fsdp_status fsdp_muon_reduce_momentum(const fsdp_plan *plan, const uint16_t *rs_
  *         FSDP_E_ALIGN, FSDP_E_STATE, FSDP_E_HIP. */
 fsdp_status fsdp_muon_update(const fsdp_plan *plan, const uint16_t *upd, uint16_t *ag_in,
                              const float *scales, const fsdp_muon_hparams_t *hp, void *stream);
+
+/* Orthogonalisation of full matrices by Newton-Schulz products.  For each
+ * matrix U [rows, cols] (X = U, or U^T where rows > cols, so that X X^T is on
+ * the smaller side):
+ *     X = U / (|U|_F + eps)
+ *     for each step's (a, b, c):  A = X X^T;  X = a X + (b A + c A A) X
+ *     out = bf16(X)
+ * which maps every singular value s to a s + b s^3 + c s^5, step by step, and
+ * leaves the singular vectors.  The norm is summed in fp64.  The products take
+ * fp16 operands (scaled by powers of two) and add in fp32, the term a X takes X
+ * to 22 bits: the result is within about 2e-3 of the exact iterate before its
+ * rounding to bf16 (relative, in the 2-norm, for the default coefficients).  A
+ * matrix that holds a NaN or an infinity becomes NaN throughout; one of zeros
+ * stays zero (with eps > 0).  Results do not depend on the other matrices of
+ * the plan.
+ *
+ * A plan covers many matrices of any shapes (their products share launches);
+ * binding names their memory; executing enqueues the products. */
+typedef struct fsdp_ortho_plan fsdp_ortho_plan;
+
+/* Host only.
+ *   rows, cols  host arrays of n_mats; 0 is an empty matrix; the longer side at
+ *               most 2^20, the shorter 2^16
+ *   coeffs      host array of 3 * n_steps: a, b, c of each step; n_steps in
+ *               [1, 64].  Starting from singular values in [0, 1], no step may
+ *               take one past 4, nor |b s^2 + c s^4| past 16 (the range of the
+ *               scaled products)
+ *   eps         finite, >= 0
+ * Errors: FSDP_E_INVAL, FSDP_E_UNSUPPORTED (sides, n_steps, the range of the
+ *         coefficients), FSDP_E_NOMEM. */
+fsdp_status fsdp_ortho_plan_create(const int64_t *rows, const int64_t *cols, int32_t n_mats,
+                                   const double *coeffs, int32_t n_steps, double eps,
+                                   fsdp_ortho_plan **out);
+
+/* The number of matrices, and the bytes of workspace an execution needs. */
+fsdp_status fsdp_ortho_plan_info(const fsdp_ortho_plan *plan, int32_t *n_mats,
+                                 int64_t *workspace_bytes);
+
+/* in, out: host arrays of n_mats device pointers to contiguous [rows, cols]
+ * matrices (any pointer where the matrix is empty): in bf16 or fp32
+ * (FSDP_DTYPE_*), out bf16, each aligned to its element.  An output may share
+ * memory with its own input, and with nothing else of the plan.  Uploads the
+ * plan's tables on `stream` and waits for it, and for the device before it
+ * replaces them.  A rejected call keeps the previous binding; a HIP failure
+ * during the upload leaves the plan unbound.
+ * Errors: FSDP_E_INVAL (null pointer of a non-empty matrix, overlap),
+ *         FSDP_E_UNSUPPORTED (dtype), FSDP_E_ALIGN, FSDP_E_STATE (bound on
+ *         another device), FSDP_E_NOMEM, FSDP_E_HIP. */
+fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *plan, const void *const *in, uint16_t *const *out,
+                            int32_t in_dtype, void *stream);
+
+/* Enqueue the orthogonalisation of every matrix of the plan.
+ *   workspace  device memory, 256-byte aligned, of at least the plan's
+ *              workspace bytes; its contents need not be kept between calls.
+ *              Executions that share a workspace must follow one another
+ *              (one stream, or events between them)
+ * Errors: FSDP_E_INVAL (null plan; null, small or overlapping workspace),
+ *         FSDP_E_ALIGN, FSDP_E_STATE (not bound, another device), FSDP_E_HIP. */
+fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *plan, void *workspace,
+                               int64_t workspace_bytes, void *stream);
+
+/* Waits for the device and frees the plan's tables; NULL is ignored. */
+void fsdp_ortho_plan_destroy(fsdp_ortho_plan *plan);
 
 /* ---- CPU offload --------------------------------------------------------- */
 

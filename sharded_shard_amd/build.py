@@ -33,11 +33,13 @@ SOURCES = [
     ("host_adamw.cpp", ["-x", "c++", "-ffp-contract=off", "-fno-fast-math", "-pthread"]),
     ("reshard.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
     ("muon.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
+    ("ortho.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
     ("copy.hip", ["-x", "hip"] + DEVICE),
     ("pack.hip", ["-x", "hip"] + DEVICE),
     ("reduce.hip", ["-x", "hip"] + DEVICE),
     ("step.hip", ["-x", "hip"] + DEVICE),
     ("muon.hip", ["-x", "hip"] + DEVICE),
+    ("ortho.hip", ["-x", "hip"] + DEVICE),
 ]
 # the kernels of the sharded step, which the committed traffic counters cover
 STEP_KERNEL_SOURCES = ["copy.hip", "pack.hip", "reduce.hip", "step.hip"]

@@ -151,6 +151,13 @@ _SIGS = {
     "fsdp_muon_momentum": (_i32, [_P, _P, ctypes.POINTER(MuonHparams), _P]),
     "fsdp_muon_reduce_momentum": (_i32, [_P, _P, _P, ctypes.POINTER(MuonHparams), _P]),
     "fsdp_muon_update": (_i32, [_P, _P, _P, _P, ctypes.POINTER(MuonHparams), _P]),
+    "fsdp_ortho_plan_create": (_i32, [ctypes.POINTER(_i64), ctypes.POINTER(_i64), _i32,
+                                      ctypes.POINTER(ctypes.c_double), _i32, ctypes.c_double,
+                                      ctypes.POINTER(_P)]),
+    "fsdp_ortho_plan_info": (_i32, [_P, ctypes.POINTER(_i32), ctypes.POINTER(_i64)]),
+    "fsdp_ortho_bind": (_i32, [_P, _PP, _PP, _i32, _P]),
+    "fsdp_ortho_execute": (_i32, [_P, _P, _i64, _P]),
+    "fsdp_ortho_plan_destroy": (None, [_P]),
     "fsdp_check_stream": (_i32, [_P]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -667,6 +674,48 @@ def fsdp_muon_update(plan, upd, ag_in, lr: float, weight_decay: float, scales=No
         u, a, sc = addr(upd), addr(ag_in), addr(scales)
     _check(lib.fsdp_muon_update(plan, u, a, sc, ctypes.byref(hp), stream_handle(stream)),
            "fsdp_muon_update")
+
+
+def fsdp_ortho_plan_create(rows, cols, coeffs, eps: float = 1e-7):
+    """coeffs: one (a, b, c) per step.  Returns an opaque plan handle."""
+    n = len(rows)
+    if len(cols) != n:
+        raise ValueError("rows and cols differ in length")
+    flat = [float(x) for abc in coeffs for x in abc]
+    if len(flat) != 3 * len(coeffs):
+        raise ValueError("coeffs: three numbers per step")
+    out = _P()
+    _check(lib.fsdp_ortho_plan_create((_i64 * max(1, n))(*rows), (_i64 * max(1, n))(*cols), n,
+                                      (ctypes.c_double * max(1, len(flat)))(*flat), len(coeffs),
+                                      eps, ctypes.byref(out)), "fsdp_ortho_plan_create")
+    return out
+
+
+def fsdp_ortho_plan_info(plan):
+    """(n_mats, workspace_bytes) of a plan."""
+    n, b = _i32(), _i64()
+    _check(lib.fsdp_ortho_plan_info(plan, ctypes.byref(n), ctypes.byref(b)),
+           "fsdp_ortho_plan_info")
+    return n.value, b.value
+
+
+def fsdp_ortho_bind(plan, ins, outs, in_dtype: int = FSDP_DTYPE_BF16, stream=None) -> None:
+    """ins, outs: one tensor or address per matrix."""
+    _check(lib.fsdp_ortho_bind(plan, _ptr_array(ins), _ptr_array(outs), in_dtype,
+                               stream_handle(stream)), "fsdp_ortho_bind")
+
+
+def fsdp_ortho_execute(plan, workspace, workspace_bytes=None, stream=None) -> None:
+    """workspace: a tensor, or an address of workspace_bytes bytes."""
+    if hasattr(workspace, "data_ptr"):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace = _dev(workspace, 0, "workspace")
+    _check(lib.fsdp_ortho_execute(plan, addr(workspace), int(workspace_bytes or 0),
+                                  stream_handle(stream)), "fsdp_ortho_execute")
+
+
+def fsdp_ortho_plan_destroy(plan) -> None:
+    lib.fsdp_ortho_plan_destroy(plan)
 
 
 def fsdp_check_stream(stream=None) -> None:

@@ -1,0 +1,356 @@
+// Orthogonalisation plans: layout of the workspace, work tiles, argument
+// checks and the launches of an execution.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <string>
+#include <vector>
+
+#include "../../include/fsdp_shard.h"
+#include "ortho.hpp"
+#include "state.hpp"
+
+struct fsdp_ortho_plan {
+    std::vector<fsdp::OrthoMat> mats;       // matrices with elements; in, out set by bind
+    std::vector<int32_t> index;             // their places in the caller's list
+    std::vector<fsdp::OrthoCoef> coef;
+    std::vector<fsdp::OrthoTile> norm, init, sym, apply;
+    int32_t n_mats = 0, growth = 0;
+    double eps = 0.0;
+    int64_t ws_bytes = 0;
+    bool bound = false, f32 = false;
+    int device = -1;
+    char *dmem = nullptr;                   // mats, then the tile tables
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;  // bytes of the bound matrices
+};
+
+namespace {
+
+using fsdp::set_error;
+
+// Singular values that the scaled fp16 products hold: X within 4, B within 16.
+constexpr double kMaxSigma = 4.0, kMaxB = 16.0;
+constexpr int64_t kMaxSide = 1 << 20, kMaxMin = 1 << 16;
+
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+
+// Largest |f| of f(s) = a s + b s^3 + c s^5 over [0, top], of |b s^2 + c s^4|,
+// and of |f(s) / s|, from the ends and the places where a derivative is 0.
+void extremes(double a, double b, double c, double top, double *f, double *g, double *q) {
+    std::vector<double> t = {0.0, top * top};      // values of s^2
+    if (c != 0.0) {
+        t.push_back(-b / (2.0 * c));
+        const double d = 9.0 * b * b - 20.0 * a * c;
+        if (d >= 0.0) {
+            t.push_back((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+            t.push_back((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+        }
+    } else if (b != 0.0) {
+        t.push_back(-a / (3.0 * b));
+    }
+    *f = *g = *q = 0.0;
+    for (double s2 : t) {
+        if (!(s2 >= 0.0 && s2 <= top * top)) continue;
+        const double r = a + s2 * (b + s2 * c);
+        *f = std::max(*f, std::fabs(std::sqrt(s2) * r));
+        *g = std::max(*g, std::fabs(s2 * (b + s2 * c)));
+        *q = std::max(*q, std::fabs(r));
+    }
+}
+
+fsdp_status check_coeffs(const double *coeffs, int32_t n_steps, fsdp_ortho_plan *p) {
+    double top = 1.0, growth = 0.0;
+    for (int32_t k = 0; k < n_steps; ++k) {
+        const double a = coeffs[3 * k], b = coeffs[3 * k + 1], c = coeffs[3 * k + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+            return set_error(FSDP_E_INVAL, "fsdp_ortho_plan_create: coefficient of step " +
+                                               std::to_string(k) + " is not finite");
+        double f, g, q;
+        extremes(a, b, c, top * 1.02, &f, &g, &q);
+        if (!(f <= kMaxSigma) || !(g <= kMaxB))
+            return set_error(FSDP_E_UNSUPPORTED,
+                             "fsdp_ortho_plan_create: the coefficients of step " +
+                                 std::to_string(k) +
+                                 " take a singular value past 4 or b s^2 + c s^4 past 16");
+        top = f;
+        growth += std::max(0.0, std::log2(std::max(q, 1e-30)));
+        p->coef.push_back({static_cast<float>(a), static_cast<float>(b), static_cast<float>(c)});
+    }
+    p->growth = static_cast<int32_t>(std::ceil(std::min(growth, 1000.0)));
+    return FSDP_OK;
+}
+
+void layout(fsdp_ortho_plan *p) {
+    int64_t off = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = off;
+        off += round_up(bytes, 256);
+        return at;
+    };
+    for (size_t i = 0; i < p->mats.size(); ++i) {
+        fsdp::OrthoMat &M = p->mats[i];
+        const int64_t x = static_cast<int64_t>(M.np) * M.mp * 2;
+        const int64_t s = static_cast<int64_t>(M.mp) * M.mp * 2;
+        M.t[0] = take(x);
+        M.t[1] = take(x);
+        M.lo = take(x);
+        M.a = take(s);
+        M.b = take(s);
+        const int64_t total = static_cast<int64_t>(M.rows) * M.cols;
+        M.n_parts = static_cast<int32_t>(std::max<int64_t>(
+            1, std::min<int64_t>(fsdp::kOrthoParts, total / fsdp::kOrthoPartMin)));
+        M.parts = take(M.n_parts * 8);
+        M.scal = take(sizeof(fsdp::OrthoScal));
+        const int32_t id = static_cast<int32_t>(i);
+        for (int32_t t = 0; t < M.n_parts; ++t) p->norm.push_back({id, t, 0, 0});
+        for (int32_t j = 0; j < M.np / 64; ++j)
+            for (int32_t k = 0; k < M.mp / 64; ++k) p->init.push_back({id, k, j, 0});
+        for (int32_t a = 0; a < M.mp / 128; ++a)
+            for (int32_t b = 0; b <= a; ++b) p->sym.push_back({id, a, b, 0});
+        for (int32_t j = 0; j < M.np / 128; ++j)
+            for (int32_t a = 0; a < M.mp / 128; ++a) p->apply.push_back({id, a, j, 0});
+    }
+    p->ws_bytes = off;
+}
+
+fsdp_status hip_error(hipError_t e, const char *what) { return fsdp::set_hip_error(e, what); }
+
+}  // namespace
+
+extern "C" {
+
+fsdp_status fsdp_ortho_plan_create(const int64_t *rows, const int64_t *cols, int32_t n_mats,
+                                   const double *coeffs, int32_t n_steps, double eps,
+                                   fsdp_ortho_plan **out) {
+    if (out == nullptr) return set_error(FSDP_E_INVAL, "fsdp_ortho_plan_create: null out");
+    *out = nullptr;
+    if (n_mats < 0 || (n_mats > 0 && (rows == nullptr || cols == nullptr)))
+        return set_error(FSDP_E_INVAL, "fsdp_ortho_plan_create: null rows or cols");
+    if (coeffs == nullptr || n_steps < 1)
+        return set_error(FSDP_E_INVAL, "fsdp_ortho_plan_create: need coefficients of one step or more");
+    if (n_steps > 64)
+        return set_error(FSDP_E_UNSUPPORTED, "fsdp_ortho_plan_create: more than 64 steps");
+    if (!(eps >= 0.0) || !std::isfinite(eps))
+        return set_error(FSDP_E_INVAL, "fsdp_ortho_plan_create: eps must be finite and not negative");
+    fsdp_ortho_plan *p = nullptr;
+    try {
+        p = new fsdp_ortho_plan();
+        p->n_mats = n_mats;
+        p->eps = eps;
+        fsdp_status s = check_coeffs(coeffs, n_steps, p);
+        for (int32_t i = 0; s == FSDP_OK && i < n_mats; ++i) {
+            const std::string which = "fsdp_ortho_plan_create: matrix " + std::to_string(i);
+            if (rows[i] < 0 || cols[i] < 0)
+                s = set_error(FSDP_E_INVAL, which + ": negative rows or cols");
+            else if (std::max(rows[i], cols[i]) > kMaxSide || std::min(rows[i], cols[i]) > kMaxMin)
+                s = set_error(FSDP_E_UNSUPPORTED, which + ": a side is too long");
+            if (s != FSDP_OK || rows[i] == 0 || cols[i] == 0) continue;
+            fsdp::OrthoMat M{};
+            M.rows = static_cast<int32_t>(rows[i]);
+            M.cols = static_cast<int32_t>(cols[i]);
+            M.wide = M.rows <= M.cols ? 1 : 0;
+            M.m = std::min(M.rows, M.cols);
+            M.n = std::max(M.rows, M.cols);
+            M.mp = static_cast<int32_t>(round_up(M.m, fsdp::kOrthoPad));
+            M.np = static_cast<int32_t>(round_up(M.n, fsdp::kOrthoPad));
+            p->mats.push_back(M);
+            p->index.push_back(i);
+        }
+        if (s == FSDP_OK) layout(p);
+        const size_t most = size_t{1} << 30;
+        if (s == FSDP_OK && (p->apply.size() > most || p->init.size() > most))
+            s = set_error(FSDP_E_UNSUPPORTED, "fsdp_ortho_plan_create: too many tiles for one launch");
+        if (s != FSDP_OK) {
+            delete p;
+            return s;
+        }
+        *out = p;
+        return FSDP_OK;
+    } catch (...) {
+        delete p;
+        return set_error(FSDP_E_NOMEM, "fsdp_ortho_plan_create: host allocation failed");
+    }
+}
+
+fsdp_status fsdp_ortho_plan_info(const fsdp_ortho_plan *p, int32_t *n_mats,
+                                 int64_t *workspace_bytes) {
+    if (p == nullptr || n_mats == nullptr || workspace_bytes == nullptr)
+        return set_error(FSDP_E_INVAL, "fsdp_ortho_plan_info: null argument");
+    *n_mats = p->n_mats;
+    *workspace_bytes = p->ws_bytes;
+    return FSDP_OK;
+}
+
+fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *p, const void *const *in, uint16_t *const *out,
+                            int32_t in_dtype, void *stream) try {
+    if (p == nullptr || (p->n_mats > 0 && (in == nullptr || out == nullptr)))
+        return set_error(FSDP_E_INVAL, "fsdp_ortho_bind: null plan or array");
+    if (in_dtype != FSDP_DTYPE_BF16 && in_dtype != FSDP_DTYPE_F32)
+        return set_error(FSDP_E_UNSUPPORTED, "fsdp_ortho_bind: in_dtype must be BF16 or F32");
+    const uintptr_t esize = in_dtype == FSDP_DTYPE_F32 ? 4 : 2;
+    struct Span {
+        uintptr_t lo, hi;
+        bool out;
+        int32_t i;
+    };
+    std::vector<Span> spans;
+    std::vector<fsdp::OrthoMat> mats = p->mats;
+    for (size_t k = 0; k < mats.size(); ++k) {
+        const int32_t i = p->index[k];
+        const std::string which = "fsdp_ortho_bind: matrix " + std::to_string(i);
+        if (in[i] == nullptr || out[i] == nullptr)
+            return set_error(FSDP_E_INVAL, which + ": null pointer");
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]);
+        const uintptr_t b = reinterpret_cast<uintptr_t>(out[i]);
+        if (a % esize != 0 || b % 2 != 0)
+            return set_error(FSDP_E_ALIGN, which + ": pointer misaligned for its type");
+        const uintptr_t n = static_cast<uintptr_t>(mats[k].rows) * static_cast<uintptr_t>(mats[k].cols);
+        spans.push_back({a, a + n * esize, false, i});
+        spans.push_back({b, b + n * 2, true, i});
+        mats[k].in = in[i];
+        mats[k].out = out[i];
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span &x, const Span &y) { return x.lo < y.lo; });
+    // an output may share memory with its own input only: pairs that overlap
+    // are adjacent in reach of the running end
+    for (size_t x = 0; x < spans.size(); ++x)
+        for (size_t y = x + 1; y < spans.size() && spans[y].lo < spans[x].hi; ++y)
+            if ((spans[x].out || spans[y].out) &&
+                !(spans[x].i == spans[y].i && spans[x].out != spans[y].out))
+                return set_error(FSDP_E_INVAL,
+                                 "fsdp_ortho_bind: output memory of matrix " +
+                                     std::to_string(spans[x].out ? spans[x].i : spans[y].i) +
+                                     " overlaps matrix " +
+                                     std::to_string(spans[x].out ? spans[y].i : spans[x].i));
+    std::vector<std::pair<uintptr_t, uintptr_t>> merged;
+    for (const Span &sp : spans)
+        if (!merged.empty() && sp.lo <= merged.back().second)
+            merged.back().second = std::max(merged.back().second, sp.hi);
+        else
+            merged.emplace_back(sp.lo, sp.hi);
+
+    int dev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_error(e, "fsdp_ortho_bind: hipGetDevice");
+    if (p->dmem != nullptr && dev != p->device)
+        return set_error(FSDP_E_STATE, "fsdp_ortho_bind: plan already bound on another device");
+    const struct {
+        const void *src;
+        size_t bytes;
+    } tabs[5] = {{mats.data(), mats.size() * sizeof(fsdp::OrthoMat)},
+                 {p->norm.data(), p->norm.size() * sizeof(fsdp::OrthoTile)},
+                 {p->init.data(), p->init.size() * sizeof(fsdp::OrthoTile)},
+                 {p->sym.data(), p->sym.size() * sizeof(fsdp::OrthoTile)},
+                 {p->apply.data(), p->apply.size() * sizeof(fsdp::OrthoTile)}};
+    if (p->dmem == nullptr) {
+        size_t total = 256;
+        for (const auto &t : tabs) total += round_up(static_cast<int64_t>(t.bytes), 256);
+        void *mem = nullptr;
+        if (hipMalloc(&mem, total) != hipSuccess)
+            return set_error(FSDP_E_NOMEM, "fsdp_ortho_bind: hipMalloc of device tables failed");
+        p->dmem = static_cast<char *>(mem);
+        p->device = dev;
+    }
+    // executions queued on any stream may still read the tables
+    e = hipDeviceSynchronize();
+    if (e != hipSuccess) return hip_error(e, "fsdp_ortho_bind: hipDeviceSynchronize");
+    p->bound = false;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    char *cur = p->dmem;
+    for (const auto &t : tabs) {
+        if (t.bytes > 0 && e == hipSuccess)
+            e = hipMemcpyAsync(cur, t.src, t.bytes, hipMemcpyHostToDevice, st);
+        cur += round_up(static_cast<int64_t>(t.bytes), 256);
+    }
+    if (e == hipSuccess) e = hipStreamSynchronize(st);
+    if (e != hipSuccess) return hip_error(e, "fsdp_ortho_bind: upload");
+    p->mats = std::move(mats);
+    p->spans = std::move(merged);
+    p->f32 = in_dtype == FSDP_DTYPE_F32;
+    p->bound = true;
+    return FSDP_OK;
+} catch (...) {
+    return set_error(FSDP_E_NOMEM, "fsdp_ortho_bind: host allocation failed");
+}
+
+fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *p, void *workspace, int64_t workspace_bytes,
+                               void *stream) try {
+    const char *call = "fsdp_ortho_execute";
+    if (p == nullptr) return set_error(FSDP_E_INVAL, "fsdp_ortho_execute: null plan");
+    if (!p->bound) return set_error(FSDP_E_STATE, "fsdp_ortho_execute: plan not bound");
+    if (p->mats.empty()) return FSDP_OK;
+    if (workspace == nullptr || workspace_bytes < p->ws_bytes)
+        return set_error(FSDP_E_INVAL, "fsdp_ortho_execute: the workspace needs " +
+                                           std::to_string(p->ws_bytes) + " bytes");
+    const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace);
+    if (w0 % 256 != 0)
+        return set_error(FSDP_E_ALIGN, "fsdp_ortho_execute: workspace not 256-byte aligned");
+    const uintptr_t w1 = w0 + static_cast<uintptr_t>(p->ws_bytes);
+    for (const auto &sp : p->spans)
+        if (sp.first < w1 && w0 < sp.second)
+            return set_error(FSDP_E_INVAL, "fsdp_ortho_execute: workspace overlaps a bound matrix");
+    int dev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_error(e, "fsdp_ortho_execute: hipGetDevice");
+    if (dev != p->device)
+        return set_error(FSDP_E_STATE, "fsdp_ortho_execute: current device differs from the bound one");
+
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const char *cur = p->dmem;
+    auto table = [&](size_t bytes) {
+        const char *t = cur;
+        cur += round_up(static_cast<int64_t>(bytes), 256);
+        return t;
+    };
+    auto tiles = [&](const std::vector<fsdp::OrthoTile> &v) {
+        return reinterpret_cast<const fsdp::OrthoTile *>(table(v.size() * sizeof(fsdp::OrthoTile)));
+    };
+    const auto *mats = reinterpret_cast<const fsdp::OrthoMat *>(
+        table(p->mats.size() * sizeof(fsdp::OrthoMat)));
+    const fsdp::OrthoTile *norm = tiles(p->norm), *init = tiles(p->init), *sym = tiles(p->sym),
+                          *apply = tiles(p->apply);
+    auto run = [&](auto &&launch) {
+        if (e == hipSuccess) e = fsdp::injected_fault();
+        if (e == hipSuccess) e = launch();
+    };
+    run([&] {
+        return fsdp::launch_ortho_norm(norm, static_cast<int64_t>(p->norm.size()), mats, workspace,
+                                       p->f32, st);
+    });
+    run([&] {
+        return fsdp::launch_ortho_init(init, static_cast<int64_t>(p->init.size()), mats, workspace,
+                                       p->f32, p->eps, p->growth, st);
+    });
+    const int64_t n_sym = static_cast<int64_t>(p->sym.size());
+    const int64_t n_apply = static_cast<int64_t>(p->apply.size());
+    for (size_t k = 0; k < p->coef.size(); ++k) {
+        const int32_t src = static_cast<int32_t>(k & 1);
+        const bool last = k + 1 == p->coef.size();
+        run([&] { return fsdp::launch_ortho_gram(sym, n_sym, mats, workspace, src, k == 0, st); });
+        run([&] { return fsdp::launch_ortho_poly(sym, n_sym, mats, workspace, p->coef[k], st); });
+        run([&] {
+            return fsdp::launch_ortho_apply(apply, n_apply, mats, workspace, src, k == 0, last,
+                                            p->coef[k], st);
+        });
+    }
+    return e == hipSuccess ? FSDP_OK : hip_error(e, (std::string(call) + ": launch").c_str());
+} catch (...) {
+    return set_error(FSDP_E_NOMEM, "fsdp_ortho_execute: host allocation failed");
+}
+
+void fsdp_ortho_plan_destroy(fsdp_ortho_plan *p) {
+    if (p == nullptr) return;
+    if (p->dmem != nullptr) {
+        int cur = -1;
+        (void)hipGetDevice(&cur);
+        (void)hipSetDevice(p->device);
+        (void)hipDeviceSynchronize();
+        (void)hipFree(p->dmem);
+        if (cur >= 0) (void)hipSetDevice(cur);
+    }
+    delete p;
+}
+
+}  // extern "C"

@@ -38,6 +38,76 @@ def split_shape(shape) -> tuple:
     return int(shape[0]), cols
 
 
+# the quintic step of the Muon optimizer, five times
+NS_COEFFS = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+class Orthogonalizer:
+    """Newton-Schulz orthogonalisation of a list of full matrices, many shapes
+    in one call; ``bind`` names the matrices, ``execute`` enqueues the work.
+
+    The workspace is allocated on first use, or the caller's: several of them
+    may share one whose executions follow each other.
+    """
+
+    def __init__(self, shapes: Sequence[Sequence[int]], coeffs=NS_COEFFS, eps: float = 1e-7):
+        self.plan = None
+        self.shapes = [split_shape(s) for s in shapes]
+        self.plan = capi.fsdp_ortho_plan_create([r for r, _ in self.shapes],
+                                                [c for _, c in self.shapes], coeffs, eps)
+        self.workspace_bytes = capi.fsdp_ortho_plan_info(self.plan)[1]
+        self.workspace = None
+        self._bound = None
+
+    def bind(self, ins, outs=None, stream=None) -> None:
+        """ins: [rows, cols] GPU tensors, all bf16 (or their int16 bits) or all
+        fp32; outs: bf16 (or int16) ones, by default the bf16 inputs themselves."""
+        outs = ins if outs is None else outs
+        if len(ins) != len(self.shapes) or len(outs) != len(self.shapes):
+            raise ValueError("one input and one output per matrix")
+        half = (torch.bfloat16, torch.int16)
+        f32 = any(t.dtype == torch.float32 for t in ins)
+        for what, ts, dtypes in (("input", ins, (torch.float32,) if f32 else half),
+                                 ("output", outs, half)):
+            for i, (t, s) in enumerate(zip(ts, self.shapes)):
+                if t.numel() != s[0] * s[1] or t.dtype not in dtypes:
+                    raise ValueError(f"{what} {i} must hold {s[0]} x {s[1]} elements of "
+                                     f"{' or '.join(str(d) for d in dtypes)}")
+                capi._dev(t, 0, f"{what} {i}")
+        capi.fsdp_ortho_bind(self.plan, list(ins), list(outs),
+                             capi.FSDP_DTYPE_F32 if f32 else capi.FSDP_DTYPE_BF16, stream)
+        self._bound = (list(ins), list(outs))
+
+    def allocate(self, workspace: Optional[torch.Tensor] = None, device: str = "cuda") -> None:
+        if workspace is None:
+            workspace = torch.empty(max(self.workspace_bytes, 1), dtype=torch.uint8, device=device)
+        if workspace.numel() * workspace.element_size() < self.workspace_bytes:
+            raise ValueError(f"workspace holds less than {self.workspace_bytes} bytes")
+        self.workspace = workspace
+
+    def execute(self, stream=None) -> None:
+        if self.workspace is None:
+            self.allocate()
+        capi.fsdp_ortho_execute(self.plan, self.workspace, stream=stream)
+
+    def close(self) -> None:
+        if self.plan is not None:
+            capi.fsdp_ortho_plan_destroy(self.plan)
+            self.plan = None
+
+    def __enter__(self) -> "Orthogonalizer":
+        return self
+
+    def __exit__(self, *exc) -> None:
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
 class ShardedGroup:
     def __init__(self, shapes: Sequence[Sequence[int]], world: int, rank: int,
                  align_elems: int = 1, device: str = "cuda",
@@ -221,6 +291,15 @@ class ShardedGroup:
         """Master update by the orthogonalised ``upd`` [S] (None: this rank's rows
         of the full tensors) and its bf16 copy-in into ``ag_in`` (None: none)."""
         capi.fsdp_muon_update(self.plan, upd, ag_in, lr, weight_decay, scales, stream)
+
+    def orthogonalizer(self, params: Optional[Sequence[int]] = None, coeffs=NS_COEFFS,
+                       eps: float = 1e-7, stream=None) -> Orthogonalizer:
+        """An Orthogonalizer bound, in place, to the full matrices of ``params``
+        (all by default; one rank's share where each rank works on its own)."""
+        idx = range(len(self.shapes)) if params is None else params
+        o = Orthogonalizer([(self.rows[i], self.cols[i]) for i in idx], coeffs, eps)
+        o.bind([self.full_view(i) for i in idx], stream=stream)
+        return o
 
     def close(self) -> None:
         if self.plan is not None:

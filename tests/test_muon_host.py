@@ -121,3 +121,52 @@ def test_muon_binding_rejects_undersized_and_host_tensors():
                 call(make(need))
     finally:
         capi.fsdp_plan_destroy(p)
+
+
+def test_ortho_plan_layout_and_refusals():
+    ns = [(3.4445, -4.7750, 2.0315)] * 5
+    p = capi.fsdp_ortho_plan_create([5, 0, 300], [7, 4, 20], ns)
+    n, ws = capi.fsdp_ortho_plan_info(p)
+    assert n == 3 and ws > 0 and ws % 256 == 0
+    assert _status(lambda: capi.fsdp_ortho_execute(p, 0x1000, ws, stream=0)) == capi.FSDP_E_STATE
+    ptr = [0x10000, 0, 0x20000]
+    out = [0x30000, 0, 0x40000]
+    for ins, outs, dtype, status in (
+            ([0, 0, 0x20000], out, 0, capi.FSDP_E_INVAL),
+            (ptr, [0x30000, 0, 0], 0, capi.FSDP_E_INVAL),
+            (ptr, out, 2, capi.FSDP_E_UNSUPPORTED),
+            ([0x10001, 0, 0x20000], out, 0, capi.FSDP_E_ALIGN),
+            ([0x10002, 0, 0x20000], out, 1, capi.FSDP_E_ALIGN),
+            (ptr, [0x30000, 0, 0x40001], 0, capi.FSDP_E_ALIGN),
+            (ptr, [0x30000, 0, 0x30000 + 2 * 34], 0, capi.FSDP_E_INVAL),
+            (ptr, [0x20000, 0, 0x40000], 0, capi.FSDP_E_INVAL),
+            (ptr, [0x30000, 0, 0x10000 + 2 * 34], 0, capi.FSDP_E_INVAL),
+            ([0x10000, 0, 0x30000], [0x30000 + 5990 * 4, 0, 0x40000], 1, capi.FSDP_E_INVAL)):
+        assert _status(lambda: capi.fsdp_ortho_bind(p, ins, outs, dtype, stream=0)) == status
+    capi.fsdp_ortho_plan_destroy(p)
+    capi.fsdp_ortho_plan_destroy(None)
+    assert capi.fsdp_ortho_plan_info(capi.fsdp_ortho_plan_create([], [], ns))[1] == 0
+    for rows, cols, coeffs, eps, status in (
+            ([-1], [2], ns, 0.0, capi.FSDP_E_INVAL),
+            ([2], [-1], ns, 0.0, capi.FSDP_E_INVAL),
+            ([2], [2], [], 0.0, capi.FSDP_E_INVAL),
+            ([2], [2], ns, -1.0, capi.FSDP_E_INVAL),
+            ([2], [2], ns, float("nan"), capi.FSDP_E_INVAL),
+            ([2], [2], [(float("inf"), 0, 0)], 0.0, capi.FSDP_E_INVAL),
+            ([2], [2], [(float("nan"), 0, 0)], 0.0, capi.FSDP_E_INVAL),
+            ([2], [2], ns * 13, 0.0, capi.FSDP_E_UNSUPPORTED),
+            ([2], [2], [(4.5, 0, 0)], 0.0, capi.FSDP_E_UNSUPPORTED),
+            ([2], [2], [(2.0, 0, 0)] * 3, 0.0, capi.FSDP_E_UNSUPPORTED),
+            ([2], [2], [(30.0, -60.0, 31.0)], 0.0, capi.FSDP_E_UNSUPPORTED),
+            ([(1 << 20) + 1], [2], ns, 0.0, capi.FSDP_E_UNSUPPORTED),
+            ([1 << 17], [1 << 17], ns, 0.0, capi.FSDP_E_UNSUPPORTED)):
+        assert _status(lambda: capi.fsdp_ortho_plan_create(rows, cols, coeffs, eps)) == status
+    for call in (lambda: capi.fsdp_ortho_plan_info(None), lambda: capi.fsdp_ortho_bind(None, [], []),
+                 lambda: capi.fsdp_ortho_bind(None, [], [], stream=0),
+                 lambda: capi.fsdp_ortho_execute(None, 0, 0, stream=0)):
+        with pytest.raises((capi.FsdpError, RuntimeError, AssertionError)):
+            call()
+    with pytest.raises(ValueError):
+        capi.fsdp_ortho_plan_create([1], [1, 2], ns)
+    with pytest.raises(ValueError):
+        capi.fsdp_ortho_plan_create([1], [1], [(1.0, 2.0)])
