@@ -82,6 +82,32 @@ fsdp_status check_coeffs(const double *coeffs, int32_t n_steps, fsdp_ortho_plan 
     return FSDP_OK;
 }
 
+// Tiles of one matrix, kBlockA x kBlockB of them at a time, so that tiles that
+// follow each other share rows of both operands.
+constexpr int32_t kBlockA = 4, kBlockB = 8;
+void blocks(int32_t mat, int32_t na, int32_t nb, bool lower, std::vector<fsdp::OrthoTile> *out) {
+    for (int32_t b0 = 0; b0 < nb; b0 += kBlockB)
+        for (int32_t a0 = 0; a0 < na; a0 += kBlockA)
+            for (int32_t b = b0; b < std::min(b0 + kBlockB, nb); ++b)
+                for (int32_t a = a0; a < std::min(a0 + kBlockA, na); ++a)
+                    if (!lower || b <= a) out->push_back({mat, a, b, 0});
+}
+
+// Workgroups go to the GPU's 8 XCDs in turn and each XCD has an L2 of its own:
+// of every kXcds * kRun tiles in order, each XCD gets kRun that follow each other.
+constexpr size_t kXcds = 8, kRun = 32;
+void spread(std::vector<fsdp::OrthoTile> *tiles) {
+    const std::vector<fsdp::OrthoTile> in = *tiles;
+    size_t done = 0;
+    while (done < in.size()) {
+        const size_t n = std::min(in.size() - done, kXcds * kRun);
+        size_t from = 0;
+        for (size_t x = 0; x < kXcds; ++x)
+            for (size_t k = x; k < n; k += kXcds) (*tiles)[done + k] = in[done + from++];
+        done += n;
+    }
+}
+
 void layout(fsdp_ortho_plan *p) {
     int64_t off = 0;
     auto take = [&](int64_t bytes) {
@@ -107,12 +133,17 @@ void layout(fsdp_ortho_plan *p) {
         for (int32_t t = 0; t < M.n_parts; ++t) p->norm.push_back({id, t, 0, 0});
         for (int32_t j = 0; j < M.np / 64; ++j)
             for (int32_t k = 0; k < M.mp / 64; ++k) p->init.push_back({id, k, j, 0});
-        for (int32_t a = 0; a < M.mp / 128; ++a)
-            for (int32_t b = 0; b <= a; ++b) p->sym.push_back({id, a, b, 0});
-        for (int32_t j = 0; j < M.np / 128; ++j)
-            for (int32_t a = 0; a < M.mp / 128; ++a) p->apply.push_back({id, a, j, 0});
+#ifndef FSDP_ORTHO_BM
+#define FSDP_ORTHO_BM 128
+#define FSDP_ORTHO_BN 128
+#endif
+        const int32_t ta = (M.mp + FSDP_ORTHO_BM - 1) / FSDP_ORTHO_BM;
+        blocks(id, ta, ta, true, &p->sym);
+        blocks(id, ta, (M.np + FSDP_ORTHO_BN - 1) / FSDP_ORTHO_BN, false, &p->apply);
     }
     p->ws_bytes = off;
+    spread(&p->sym);
+    spread(&p->apply);
 }
 
 fsdp_status hip_error(hipError_t e, const char *what) { return fsdp::set_hip_error(e, what); }

@@ -17,9 +17,11 @@
 // which vanish with the singular value, take the high part.  That leaves 3e-4
 // to 2e-3, below the 1.7e-3 of rounding the result to bf16 itself or near it.
 //
-// Layout.  Only X^T is stored, [np][mp].  X = a X + B X is then a product of
-// rows with rows (rows of B, rows of X^T), and A sums over rows of X^T, whose
-// tiles the transposing LDS read turns into operands.
+// Layout.  Only X^T is stored.  X = a X + B X is then a product of rows with
+// rows (rows of B, rows of X^T), and A sums over rows of X^T, whose tiles the
+// transposing LDS read turns into operands.  X^T, A and B lie in panels of 32
+// columns, [columns / 32][rows][32]: the rows of one step of a sum (64 bytes
+// each) follow each other, and so do a 32 x 32 block's in an epilogue.
 #include "ortho.hpp"
 
 #include "device.hpp"
@@ -31,10 +33,12 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) s16x8 lds_s16x8;
 typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
 
 // log2 of the scale of A and B
@@ -43,6 +47,11 @@ constexpr int kLogA = 11;
 constexpr int kLogX = 12;
 
 __device__ __forceinline__ char *at(void *ws, int64_t off) { return static_cast<char *>(ws) + off; }
+
+// Element (row, col) of a matrix in panels of 32 columns with `rows` rows.
+__device__ __forceinline__ int64_t panel_at(int rows, int row, int col) {
+    return (static_cast<int64_t>(col >> 5) * rows + row) * 32 + (col & 31);
+}
 
 // ---------------------------------------------------------------------------
 // norm and start
@@ -139,7 +148,7 @@ __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__r
     for (int y = ty; y < 64; y += kBlock / 64) {
         const float x = M.wide ? buf[tx][y] : buf[y][tx];
         const _Float16 h = static_cast<_Float16>(x);
-        const int64_t o = static_cast<int64_t>(tl.tj * 64 + y) * M.mp + tl.ti * 64 + tx;
+        const int64_t o = panel_at(M.np, tl.tj * 64 + y, tl.ti * 64 + tx);
         hi[o] = h;
         lo[o] = static_cast<_Float16>(x - static_cast<float>(h));
     }
@@ -151,7 +160,8 @@ __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__r
 
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 
-constexpr int kBK = 64;
+// elements of the sum per stage: one panel of columns
+constexpr int kBK = 32;
 
 // A 32 x 32 block's rows come back from the matrix core as four runs of four a
 // lane; with operand row rho holding tile row pi(rho) a lane's values are two
@@ -162,92 +172,138 @@ __device__ __forceinline__ int perm_row(int rho) {
     return 16 * c + 8 * h + 4 * d + e;
 }
 
-// Tiles of rows with 64 halves (128 bytes, eight 16-byte chunks): the chunk
-// sits at its index xor this, so that the eight lanes of one LDS cycle, which
-// read eight rows at the same index, hit different banks.
-__device__ __forceinline__ int swz_row(int row) { return (row & 3) | ((row >> 1) & 4); }
+// Rows of 64 bytes in LDS: a row's 16-byte chunk sits at its index xor this, so
+// that the 16 lanes of one LDS cycle, which read 16 neighbouring rows at the
+// same index, hit all 64 banks (256 bytes: four rows).
+__device__ __forceinline__ int swz_row(int row) { return (row >> 2) & 3; }
 
-// Fills `rows` rows of an LDS tile from a row-major matrix (ld bytes a row,
-// rows past `avail` bytes read zeros): each wave's load writes 1 KB, 8 rows.
-template <int ROWS, int WAVES>
-__device__ __forceinline__ void fill_rows(lds_char *dst, const char *src, uint32_t ld,
-                                          uint32_t avail, uint32_t kbyte, int wave, int lane) {
-    static_assert(ROWS % (8 * WAVES) == 0, "whole loads per wave");
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char *>(src), 0, avail, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < ROWS / 8 / WAVES; ++i) {
-        const int row8 = (i * WAVES + wave) * 8, row = row8 + (lane >> 3);
-        const uint32_t voff = static_cast<uint32_t>(row) * ld +
-                              static_cast<uint32_t>((lane & 7) ^ swz_row(row)) * 16u;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + row8 * 128), 16, voff, kbyte,
-                                                 0, 0);
-    }
+// Rows of a panel into LDS, straight from memory: load u of a tile writes 1 KB,
+// the rows 16 u .. 16 u + 16.  Past nbytes it writes zeros.
+__device__ __forceinline__ void fill_rows(lds_char *dst, const char *src, uint32_t nbytes, int u,
+                                          int lane) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(src), 0, nbytes, 0x00020000);
+    const uint32_t voff = static_cast<uint32_t>((lane >> 2) * 64 +
+                                                ((lane & 3) ^ swz_row(lane >> 2)) * 16);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + u * 1024), 16, voff, u * 1024, 0,
+                                             0);
 }
 
-// Fills a tile of kBK rows of COLS halves (the sum runs over rows).  A
-// 32-byte piece p of row k sits at p xor swz_col(k): a transposing read takes
-// 32 bytes of each of 16 rows at the same p.
-__device__ __forceinline__ int swz_col(int k) { return (k & 3) | ((k >> 1) & 4); }
-
-template <int COLS, int WAVES>
-__device__ __forceinline__ void fill_cols(lds_char *dst, const char *src, uint32_t ld,
-                                          uint32_t avail, uint32_t kbyte, int wave, int lane) {
-    constexpr int kPer = 1024 / (COLS * 2);       // rows per load
-    constexpr int kLanes = 64 / kPer;             // lanes per row
-    static_assert(kBK % (kPer * WAVES) == 0, "whole loads per wave");
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char *>(src), 0, avail, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < kBK / kPer / WAVES; ++i) {
-        const int k0 = (i * WAVES + wave) * kPer, k = k0 + lane / kLanes, c = lane % kLanes;
-        const uint32_t voff = static_cast<uint32_t>(k) * ld +
-                              static_cast<uint32_t>(((c >> 1) ^ swz_col(k)) * 32 + (c & 1) * 16);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + k0 * COLS * 2), 16, voff,
-                                                 kbyte, 0, 0);
-    }
+// The rows [32 s, 32 s + 32) of panels of `panel` bytes each, in LDS one
+// panel's 2 KB after the other; load u: half a panel's.
+__device__ __forceinline__ void fill_cols(lds_char *dst, const char *src, uint32_t nbytes,
+                                          uint32_t panel, int s, int u, int lane) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(src), 0, nbytes, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (lds_void *)(dst + u * 1024), 16, static_cast<uint32_t>(lane) * 16u,
+        static_cast<uint32_t>(u >> 1) * panel + (u & 1) * 1024 + s * 2048, 0, 0);
 }
 
-// Operand of 32 rows and 16 k: this lane's row and its 8 k.
+// Operand of 32 rows and 16 elements of the sum: this lane's row, its 8.
 __device__ __forceinline__ f16x8 read_rows(const lds_char *t, int row, int ks, int lane) {
     const int c = (ks * 2 + (lane >> 5)) ^ swz_row(row);
-    return *(const lds_f16x8 *)(t + row * 128 + c * 16);
+    return *(const lds_f16x8 *)(t + row * 64 + c * 16);
 }
 
-// The same from a tile with the sum over rows.  Lane l of a 16-lane group reads
-// 4 neighbouring columns (8 bytes) of row k0 + (l >> 2); it gets column l of
-// the 16 that lanes 0 to 3 read, of those 4 rows.  col: the first column that
-// this lane reads.
-template <int COLS>
+// Four rows at t, row bytes apart, of 16 columns: lane l of a 16-lane group
+// reads 4 neighbouring columns (8 bytes) of row l >> 2, and gets column l of
+// the 16 that lanes 0 to 3 read, of those 4 rows.  (restrict: with aliasing
+// facts on the read the compiler does not wait for every load to LDS that is
+// under way before it; the borders wait for those that matter.)
+__device__ __forceinline__ s16x4 read_tr(lds_char *__restrict__ t) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)t);
+}
+
+// The operand from a tile with the sum over rows; col: the first column that
+// this lane reads.  No swizzle is needed: the 32 lanes of one LDS cycle read
+// four whole rows of a panel.
 __device__ __forceinline__ f16x8 read_cols(lds_char *t, int col, int ks, int lane) {
-    const int k0 = ks * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3);
+    const int k = ks * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3);
+    lds_char *at = t + (col >> 5) * 2048 + k * 64 + (col & 31) * 2;
     union {
         s16x4 s[2];
         f16x8 v;
     } u;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int k = k0 + 4 * j;
-        u.s[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4 *)(t + k * COLS * 2 + (((col >> 4) ^ swz_col(k)) * 32) + (col & 15) * 2));
-    }
+    u.s[0] = read_tr(at);
+    u.s[1] = read_tr(at + 4 * 64);
     return u.v;
 }
 
-// Bytes of `rows` rows, as far as a buffer range reaches (a tile needs less).
-__device__ __forceinline__ uint32_t bytes_from(int rows, uint32_t ld) {
-    const int64_t b = static_cast<int64_t>(rows) * ld;
-    return b > 0x7FFFFFFF ? 0x7FFFFFFFu : static_cast<uint32_t>(b);
+// x as one fp32 value.  Without this the compiler may take a product and its
+// conversion to fp16 as one operation of one rounding in one place and as two
+// in another, and a high part that is stored then differs, where the two
+// round apart, from the one that the low part was taken against.
+__device__ __forceinline__ float settled(float x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
-template <int KIND, int BM, int BN, int WM, int WN>
+union Half8 {
+    f16x8 f;
+    s16x8 s;
+    u32x4 w;
+};
+
+// A wave's 32 x 32 block turned over: in, this lane's column j = perm_row(lane
+// & 31) with rows 16 c + 8 h .. + 8 in v[c]; out, row turned_row(lane) with
+// columns 16 t + 8 (lane >> 5) .. + 8 in v[t].  st: 2 KB of LDS of the wave's.
+__device__ __forceinline__ int turned_row(int lane) { return lane & 31; }
+__device__ __forceinline__ void turn(lds_char *st, Half8 (&v)[2], int lane) {
+    const int h = lane >> 5, j = perm_row(lane & 31);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) *(lds_s16x8 *)(st + j * 64 + c * 32 + h * 16) = v[c].s;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        lds_char *at = st + (16 * t + 8 * h + ((lane >> 2) & 3)) * 64 + ((lane >> 4) & 1) * 32 +
+                       (lane & 3) * 8;
+        const s16x4 a = read_tr(at), b = read_tr(at + 4 * 64);
+        v[t].s = s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    }
+}
+
+// n of 8 bf16 at p, in one store where they are all there and p allows it.
+__device__ __forceinline__ void store_out(uint16_t *p, const Half8 &v, int n, bool vec) {
+    if (vec && n >= 8) {
+        *reinterpret_cast<u32x4 *>(p) = v.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) p[e] = static_cast<uint16_t>(v.s[e]);
+    }
+}
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+template <int N>
+__device__ __forceinline__ void border() {
+    // vmcnt(N) lgkmcnt(0), then the barrier
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// C = alpha * (sums of P's rows i with Q's rows j), one BM x BN tile a block.
+//
+// NST stages of LDS, of which NST - 1 are on their way while one is read, and
+// two sets of operand registers: while the matrix cores work on one set the
+// other is read, across the stages' borders too.  At a border every wave has
+// its last operands of the old stage in registers (lgkmcnt) and its loads of
+// the next one landed (vmcnt: those after it may be under way); past the barrier the next stage may be read and the old one
+// overwritten.
+template <int KIND, int BM, int BN, int WM, int WN, int NST>
 __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const OrthoTile *__restrict__ tiles, const OrthoMat *__restrict__ mats, void *ws, int32_t src,
     int32_t first, OrthoCoef coef) {
     constexpr int WAVES = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
     constexpr bool kSym = KIND == kGram || KIND == kPoly;
-    constexpr int kStage = (BM + BN) * kBK * 2;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
+    constexpr int kStage = (BM + BN) * kBK * 2, kLoadsP = BM / 16 / WAVES,
+                  kLoadsQ = BN / 16 / WAVES;
+    static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0, "whole loads per wave");
+    static_assert(NST * kStage >= WAVES * 2048 && NST >= 3 && NST <= 4,
+                  "LDS of the epilogue; the shortest sum has four stages");
+    __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
     lds_char *lds = (lds_char *)smem;
 
     const OrthoTile tl = tiles[blockIdx.x];
@@ -256,98 +312,74 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int i0 = tl.ti * BM, j0 = tl.tj * BN;
-
-    // P gives the tile's rows i, Q its columns j
-    const char *P, *Q;
-    uint32_t ldk, availP, availQ, kstep;
-    int K;
-    if constexpr (KIND == kGram) {
-        // rows of X^T are the sum: a stage is kBK of them, columns i0.. and j0..
-        const char *T = at(ws, src ? M.t[1] : M.t[0]);
-        P = T + i0 * 2;
-        Q = T + j0 * 2;
-        ldk = static_cast<uint32_t>(M.mp) * 2;
-        availP = availQ = kBK * ldk;   // at most: the last columns' rows end before it
-        K = M.np;
-        kstep = 0;
-    } else {
-        const char *A = at(ws, KIND == kPoly ? M.a : M.b);
-        ldk = static_cast<uint32_t>(M.mp) * 2;
-        P = A + static_cast<int64_t>(i0) * ldk;
-        Q = KIND == kPoly ? A + static_cast<int64_t>(j0) * ldk
-                          : at(ws, src ? M.t[1] : M.t[0]) + static_cast<int64_t>(j0) * ldk;
-        availP = bytes_from(M.mp - i0, ldk);
-        availQ = bytes_from((KIND == kPoly ? M.mp : M.np) - j0, ldk);
-        K = M.mp;
-        kstep = kBK * 2;
-    }
-
-    f32x16 acc[FM][FN];
-#pragma unroll
-    for (int x = 0; x < FM; ++x)
-#pragma unroll
-        for (int y = 0; y < FN; ++y)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
-
-    auto fill = [&](int s, int buf) {
-        lds_char *b = lds + buf * kStage;
-        if constexpr (KIND == kGram) {
-            const int64_t o = static_cast<int64_t>(s) * kBK * ldk;
-            fill_cols<BM, WAVES>(b, P + o, ldk, availP, 0, wave, lane);
-            fill_cols<BN, WAVES>(b + BM * kBK * 2, Q + o, ldk, availQ, 0, wave, lane);
-        } else {
-            fill_rows<BM, WAVES>(b, P, ldk, availP, s * kstep, wave, lane);
-            fill_rows<BN, WAVES>(b + BM * kBK * 2, Q, ldk, availQ, s * kstep, wave, lane);
-        }
-    };
-
-    const int steps = K / kBK;
+    const int h = lane >> 5;
     // both operands take their rows through the same permutation
     const int prow = perm_row(lane & 31);
     const int pcol = perm_row((lane & 16) | ((lane & 3) << 2));
-    fill(0, 0);
-    for (int s = 0; s < steps; ++s) {
-        // the wave's own loads of stage s have landed; past the barrier so have
-        // the others', and nobody reads the other buffer any more
-        __builtin_amdgcn_s_waitcnt(0x0F70);       // vmcnt(0)
-        __syncthreads();
-        if (s + 1 < steps) fill(s + 1, (s + 1) & 1);
-        lds_char *b = lds + (s & 1) * kStage;
-        lds_char *bp = b, *bq = b + BM * kBK * 2;
-#pragma unroll
-        for (int ks = 0; ks < kBK / 16; ++ks) {
-            f16x8 p[FM], q[FN];
-#pragma unroll
-            for (int x = 0; x < FM; ++x) {
-                const int base = wm * WTM + x * 32;
-                if constexpr (KIND == kGram) p[x] = read_cols<BM>(bp, base + pcol, ks, lane);
-                else p[x] = read_rows(bp, base + prow, ks, lane);
-            }
-#pragma unroll
-            for (int y = 0; y < FN; ++y) {
-                const int base = wn * WTN + y * 32;
-                if constexpr (KIND == kGram) q[y] = read_cols<BN>(bq, base + pcol, ks, lane);
-                else q[y] = read_rows(bq, base + prow, ks, lane);
-            }
-#pragma unroll
-            for (int x = 0; x < FM; ++x)
-#pragma unroll
-                for (int y = 0; y < FN; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p[x], q[y], acc[x][y], 0, 0,
-                                                                       0);
-        }
-    }
-
-    // Epilogue.  Of block (x, y) this lane has column j and, for c = 0, 1, the
-    // rows 16 c + 8 h .. + 8 in acc[8 c .. 8 c + 8).
     const OrthoScal sc = *reinterpret_cast<const OrthoScal *>(at(ws, M.scal));
-    const int h = lane >> 5;
+    const char *T = at(ws, src ? M.t[1] : M.t[0]);
+
+    // load k of this wave's kLoadsP of stage s's rows i, or of its kLoadsQ of the rows j
+    auto fill_p = [&](int s, int buf, int k) {
+        lds_char *b = lds + buf * kStage;
+        const int u = k * WAVES + wave;
+        if constexpr (KIND == kGram) {
+            // rows of X^T are the sum, columns i and j
+            const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
+            const int at = i0 / 32, n = M.mp / 32 - at < BM / 32 ? M.mp / 32 - at : BM / 32;
+            fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
+        } else {
+            const char *A = at(ws, KIND == kPoly ? M.a : M.b);
+            const int n = M.mp - i0 < BM ? M.mp - i0 : BM;
+            fill_rows(b, A + (static_cast<int64_t>(s) * M.mp + i0) * 64, n * 64u, u, lane);
+        }
+    };
+    auto fill_q = [&](int s, int buf, int k) {
+        lds_char *b = lds + buf * kStage + BM * 64;
+        const int u = k * WAVES + wave;
+        if constexpr (KIND == kGram) {
+            const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
+            const int at = j0 / 32, n = M.mp / 32 - at < BN / 32 ? M.mp / 32 - at : BN / 32;
+            fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
+        } else {
+            const char *A = KIND == kPoly ? at(ws, M.a) : T;
+            const int rq = KIND == kPoly ? M.mp : M.np, n = rq - j0 < BN ? rq - j0 : BN;
+            fill_rows(b, A + (static_cast<int64_t>(s) * rq + j0) * 64, n * 64u, u, lane);
+        }
+    };
+    f16x8 p[2][FM], q[2][FN];
+    // operand k of a set, the first product's first: rows i, then j, in turn
+    auto read = [&](int set, int buf, int ks, int k) {
+        lds_char *bp = lds + buf * kStage, *bq = bp + BM * 64;
+        const bool isq = k == 1 || k > FM;
+        const int x = isq ? (k == 1 ? 0 : k - FM) : (k == 0 ? 0 : k - 1);
+        const int base = isq ? wn * WTN + x * 32 : wm * WTM + x * 32;
+        f16x8 v;
+        if constexpr (KIND == kGram) v = read_cols(isq ? bq : bp, base + pcol, ks, lane);
+        else v = read_rows(isq ? bq : bp, base + prow, ks, lane);
+        if (isq) q[set][x] = v;
+        else p[set][x] = v;
+    };
+
+    const int steps = (KIND == kGram ? M.np : M.mp) / kBK;       // four at least
+#pragma unroll
+    for (int s = 0; s < NST - 1; ++s) {
+#pragma unroll
+        for (int k = 0; k < kLoadsP; ++k) fill_p(s, s, k);
+#pragma unroll
+        for (int k = 0; k < kLoadsQ; ++k) fill_q(s, s, k);
+    }
+    f32x16 acc[FM][FN];
     if constexpr (kSym) {
-        _Float16 *C = reinterpret_cast<_Float16 *>(at(ws, KIND == kGram ? M.a : M.b));
-        const _Float16 *A = reinterpret_cast<const _Float16 *>(at(ws, M.a));
-        const float phi = first ? sc.phi0 : sc.phi;
-        const float alpha = KIND == kGram ? ldexpf(phi * phi, kLogA) : ldexpf(coef.c, -kLogA);
+#pragma unroll
+        for (int x = 0; x < FM; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
+    } else {
+        // the sums start from a X, so that its loads overlap the first stages'
+        const float ca = ldexpf(coef.a, kLogA);
 #pragma unroll
         for (int x = 0; x < FM; ++x)
 #pragma unroll
@@ -356,77 +388,146 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                 for (int c = 0; c < 2; ++c) {
                     const int i = i0 + wm * WTM + x * 32 + 16 * c + 8 * h;
                     const int j = j0 + wn * WTN + y * 32 + prow;
-                    if (i >= M.mp || j >= M.mp) continue;
-                    f16x8 v;
-                    f16x8 old;
+                    f16x8 hi{}, lo{};
+                    if (i < M.mp && j < M.np) {
+                        const int64_t o = panel_at(M.np, j, i);
+                        hi = reinterpret_cast<const f16x8 *>(T)[o >> 3];
+                        lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o >> 3];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        acc[x][y][8 * c + e] =
+                            ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e]));
+                }
+    }
+    border<0>();
+#pragma unroll
+    for (int k = 0; k < FM + FN; ++k) read(0, 0, 0, k);
+    // The products of one set; after each, its share of the next set's reads
+    // and of the loads: a wave issues in order, and a burst of loads that the
+    // memory path cannot take at once would hold up its products.
+    auto multiply = [&](int set, auto reads, auto loads, auto &&rd, auto &&ld) {
+        constexpr int n = FM * FN, R = reads.value, L = loads.value;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const int x = k / FN, y = k % FN;
+            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p[set][x], q[set][y], acc[x][y], 0,
+                                                               0, 0);
+            // the reads go first, so that the last have a product or more to land
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r * (n - 1) / (FM + FN) == k) rd(r);
+#pragma unroll
+            for (int l = 0; l < L; ++l)
+                if ((2 * l + 1) * n / (2 * (L > 0 ? L : 1)) == k) ld(l);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // One stage: two sets.  No branch lies between a read of operands and their
+    // use, so that the compiler waits for the older set of reads alone.
+    static_assert(kBK == 32, "a stage is two sets of operands");
+    int buf = 0;
+    auto stage = [&](auto wait, auto more, int s) {
+        constexpr int LP = more.value > 1 ? kLoadsP : 0, LQ = more.value > 1 ? kLoadsQ : 0;
+        constexpr int R = FM + FN;
+        const int last = buf == 0 ? NST - 1 : buf - 1;      // read before the last border
+        multiply(0, Int<R>{}, Int<LP>{}, [&](int k) { read(1, buf, 1, k); },
+                 [&](int k) { fill_p(s + NST - 1, last, k); });
+        buf = buf == NST - 1 ? 0 : buf + 1;
+        if constexpr (more.value > 0) border<wait.value>();
+        multiply(1, Int<(more.value > 0 ? R : 0)>{}, Int<LQ>{}, [&](int k) { read(0, buf, 0, k); },
+                 [&](int k) { fill_q(s + NST - 1, last, k); });
+    };
+    constexpr int kLoads = kLoadsP + kLoadsQ;
+    int s = 0;
+    // loads younger than the next stage's: NST - 3 stages and this one's first
+    for (; s + NST - 1 < steps; ++s) stage(Int<kLoads *(NST - 3) + kLoadsP>{}, Int<2>{}, s);
+    // what is left was filled: NST - 2 stages with a border, and the last one
+    if constexpr (NST > 3) stage(Int<kLoads *(NST - 3)>{}, Int<1>{}, s++);
+    if constexpr (NST > 2) stage(Int<0>{}, Int<1>{}, s++);
+    stage(Int<0>{}, Int<0>{}, s);
+
+    // Epilogue.  Of block (x, y) this lane has column j and, for c = 0, 1, the
+    // rows 16 c + 8 h .. + 8 in acc[8 c .. 8 c + 8).
+    lds_char *st = lds + wave * 2048;
+    if constexpr (kSym || KIND == kLast) border<0>();
+    const float phi = first ? sc.phi0 : sc.phi, rho = first ? sc.rho : 1.0f;
+    const float alpha = KIND == kGram   ? ldexpf(phi * phi, kLogA)
+                        : KIND == kPoly ? ldexpf(coef.c, -kLogA)
+                                        : ldexpf(rho, -kLogA);
+    const bool vec = KIND == kLast && (lo32(M.out) & 15u) == 0 && (M.cols & 7) == 0;
+#pragma unroll
+    for (int x = 0; x < FM; ++x)
+#pragma unroll
+        for (int y = 0; y < FN; ++y) {
+            const int ib = i0 + wm * WTM + x * 32, jb = j0 + wn * WTN + y * 32, j = jb + prow;
+            if (ib >= M.mp || jb >= (kSym ? M.mp : M.np)) continue;
+            Half8 v[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int i = ib + 16 * c + 8 * h;
+                if constexpr (kSym) {
+                    f16x8 *C = reinterpret_cast<f16x8 *>(at(ws, KIND == kGram ? M.a : M.b));
+                    const int64_t o = panel_at(M.mp, j, i) >> 3;
+                    f16x8 old{};
                     if constexpr (KIND == kPoly)
-                        old = *reinterpret_cast<const f16x8 *>(A + static_cast<int64_t>(j) * M.mp + i);
+                        old = reinterpret_cast<const f16x8 *>(at(ws, M.a))[o];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         float t = alpha * acc[x][y][8 * c + e];
                         if constexpr (KIND == kPoly) t = coef.b * static_cast<float>(old[e]) + t;
-                        v[e] = static_cast<_Float16>(t);
+                        v[c].f[e] = static_cast<_Float16>(t);
                     }
-                    // (i, j) and (j, i) are the same value; a diagonal tile has
-                    // both among its own, which must not differ: the lower wins
-                    if (tl.ti != tl.tj) {
-                        *reinterpret_cast<f16x8 *>(C + static_cast<int64_t>(j) * M.mp + i) = v;
+                    C[o] = v[c].f;
+                } else if constexpr (KIND == kApply) {
+                    const int64_t o = panel_at(M.np, j, i) >> 3;
+                    f16x8 vl;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            C[static_cast<int64_t>(i + e) * M.mp + j] = v[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (i + e >= j) {
-                                C[static_cast<int64_t>(i + e) * M.mp + j] = v[e];
-                                C[static_cast<int64_t>(j) * M.mp + i + e] = v[e];
-                            }
+                    for (int e = 0; e < 8; ++e) {
+                        const float t = settled(alpha * acc[x][y][8 * c + e]);
+                        v[c].f[e] = static_cast<_Float16>(t);
+                        vl[e] = static_cast<_Float16>(t - static_cast<float>(v[c].f[e]));
                     }
-                }
-    } else {
-        const _Float16 *T = reinterpret_cast<const _Float16 *>(at(ws, src ? M.t[1] : M.t[0]));
-        _Float16 *T2 = reinterpret_cast<_Float16 *>(at(ws, src ? M.t[0] : M.t[1]));
-        _Float16 *L = reinterpret_cast<_Float16 *>(at(ws, M.lo));
-        const float rho = first ? sc.rho : 1.0f;
-        const float ca = coef.a * rho, cb = ldexpf(rho, -kLogA);
-#pragma unroll
-        for (int x = 0; x < FM; ++x)
-#pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int i = i0 + wm * WTM + x * 32 + 16 * c + 8 * h;
-                    const int j = j0 + wn * WTN + y * 32 + prow;
-                    if (i >= M.mp || j >= M.np) continue;
-                    const int64_t o = static_cast<int64_t>(j) * M.mp + i;
-                    const f16x8 hi = *reinterpret_cast<const f16x8 *>(T + o);
-                    const f16x8 lo = *reinterpret_cast<const f16x8 *>(L + o);
-                    float v[8];
+                    reinterpret_cast<f16x8 *>(at(ws, src ? M.t[0] : M.t[1]))[o] = v[c].f;
+                    reinterpret_cast<f16x8 *>(at(ws, M.lo))[o] = vl;
+                } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[e] = ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e])) +
-                               cb * acc[x][y][8 * c + e];
-                    if constexpr (KIND == kApply) {
-                        f16x8 vh, vl;
+                        v[c].s[e] = static_cast<short>(
+                            bf16_rne(alpha * acc[x][y][8 * c + e] * sc.phi));
+                }
+            }
+            if constexpr (kSym) {
+                // a tile off the diagonal is its mirror image's values too
+                if (tl.ti != tl.tj) {
+                    turn(st, v, lane);
+                    f16x8 *C = reinterpret_cast<f16x8 *>(at(ws, KIND == kGram ? M.a : M.b));
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            vh[e] = static_cast<_Float16>(v[e]);
-                            vl[e] = static_cast<_Float16>(v[e] - static_cast<float>(vh[e]));
-                        }
-                        *reinterpret_cast<f16x8 *>(T2 + o) = vh;
-                        *reinterpret_cast<f16x8 *>(L + o) = vl;
-                    } else {
-                        if (j >= M.n) continue;
+                    for (int t = 0; t < 2; ++t)
+                        C[panel_at(M.mp, ib + turned_row(lane), jb + 16 * t + 8 * h) >> 3] = v[t].f;
+                }
+            } else if constexpr (KIND == kLast) {
+                if (M.wide) {
+                    turn(st, v, lane);
+                    const int i = ib + turned_row(lane);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (i + e >= M.m) continue;
-                            const uint16_t w = static_cast<uint16_t>(bf16_rne(v[e] * sc.phi));
-                            if (M.wide) M.out[static_cast<int64_t>(i + e) * M.cols + j] = w;
-                            else M.out[static_cast<int64_t>(j) * M.cols + i + e] = w;
-                        }
+                    for (int t = 0; t < 2; ++t) {
+                        const int jj = jb + 16 * t + 8 * h;
+                        if (i < M.m && jj < M.n)
+                            store_out(M.out + static_cast<int64_t>(i) * M.cols + jj, v[t],
+                                      M.n - jj, vec);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int i = ib + 16 * c + 8 * h;
+                        if (i < M.m && j < M.n)
+                            store_out(M.out + static_cast<int64_t>(j) * M.cols + i, v[c], M.m - i,
+                                      vec);
                     }
                 }
-    }
+            }
+        }
 }
 
 }  // namespace
@@ -434,6 +535,18 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
+
+#ifndef FSDP_ORTHO_BM
+#define FSDP_ORTHO_BM 128
+#define FSDP_ORTHO_BN 128
+#define FSDP_ORTHO_WM 2
+#define FSDP_ORTHO_WN 2
+#endif
+#ifndef FSDP_ORTHO_NST
+#define FSDP_ORTHO_NST 4
+#endif
+#define TILE_ARGS FSDP_ORTHO_BM, FSDP_ORTHO_BN, FSDP_ORTHO_WM, FSDP_ORTHO_WN, FSDP_ORTHO_NST
+#define TILE_THR (64 * FSDP_ORTHO_WM * FSDP_ORTHO_WN)
 
 hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              bool f32, hipStream_t st) {
@@ -458,7 +571,7 @@ hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *
 hipError_t launch_ortho_gram(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              int32_t src, bool first, hipStream_t st) {
     if (n == 0) return hipSuccess;
-    ortho_product_kernel<kGram, 128, 128, 2, 2><<<static_cast<unsigned>(n), 256, 0, st>>>(
+    ortho_product_kernel<kGram, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
         tiles, mats, ws, src, first, OrthoCoef{});
     return hipGetLastError();
 }
@@ -466,7 +579,7 @@ hipError_t launch_ortho_gram(const OrthoTile *tiles, int64_t n, const OrthoMat *
 hipError_t launch_ortho_poly(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              OrthoCoef c, hipStream_t st) {
     if (n == 0) return hipSuccess;
-    ortho_product_kernel<kPoly, 128, 128, 2, 2><<<static_cast<unsigned>(n), 256, 0, st>>>(
+    ortho_product_kernel<kPoly, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
         tiles, mats, ws, 0, 0, c);
     return hipGetLastError();
 }
@@ -475,10 +588,10 @@ hipError_t launch_ortho_apply(const OrthoTile *tiles, int64_t n, const OrthoMat 
                               int32_t src, bool first, bool last, OrthoCoef c, hipStream_t st) {
     if (n == 0) return hipSuccess;
     if (last)
-        ortho_product_kernel<kLast, 128, 128, 2, 2><<<static_cast<unsigned>(n), 256, 0, st>>>(
+        ortho_product_kernel<kLast, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
             tiles, mats, ws, src, first, c);
     else
-        ortho_product_kernel<kApply, 128, 128, 2, 2><<<static_cast<unsigned>(n), 256, 0, st>>>(
+        ortho_product_kernel<kApply, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
             tiles, mats, ws, src, first, c);
     return hipGetLastError();
 }
