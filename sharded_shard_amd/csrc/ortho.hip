@@ -34,7 +34,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -163,19 +162,17 @@ enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 // elements of the sum per stage: one panel of columns
 constexpr int kBK = 32;
 
-// A 32 x 32 block's rows come back from the matrix core as four runs of four a
-// lane; with operand row rho holding tile row pi(rho) a lane's values are two
-// runs of eight neighbouring rows instead: 16-byte stores.
-//   rho = 8 (2c + d) + 4 h + e  ->  16 c + 8 h + 4 d + e
-__device__ __forceinline__ int perm_row(int rho) {
-    const int e = rho & 3, h = (rho >> 2) & 1, d = (rho >> 3) & 1, c = rho >> 4;
-    return 16 * c + 8 * h + 4 * d + e;
-}
+// Blocks of 32 x 32 are two by two products of 16 x 16 (and 32 of the sum).  Of
+// a product's 16 rows lane l gets back 4 (l >> 4) .. + 4, so the rows of half b
+// of a block are taken in an order that joins the two halves' fours to eight
+// neighbouring rows: 16-byte stores.
+__device__ __forceinline__ int perm_row(int r, int b) { return 8 * (r >> 2) + 4 * b + (r & 3); }
 
-// Rows of 64 bytes in LDS: a row's 16-byte chunk sits at its index xor this, so
-// that the 16 lanes of one LDS cycle, which read 16 neighbouring rows at the
-// same index, hit all 64 banks (256 bytes: four rows).
-__device__ __forceinline__ int swz_row(int row) { return (row >> 2) & 3; }
+// Rows of 64 bytes in LDS: a row's 16-byte chunk sits at its index xor this.  One
+// LDS cycle serves 16 lanes of which half come from the other 16 of each 32
+// (measured by conflicts: quads 0, 2 with 5, 7 and so on), which read the next
+// chunk: with the two 16-row halves apart they hit all 64 banks.
+__device__ __forceinline__ int swz_row(int row) { return ((row >> 4) & 1) << 1; }
 
 // Rows of a panel into LDS, straight from memory: load u of a tile writes 1 KB,
 // the rows 16 u .. 16 u + 16.  Past nbytes it writes zeros.
@@ -183,11 +180,16 @@ __device__ __forceinline__ void fill_rows(lds_char *dst, const char *src, uint32
                                           int lane) {
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(src), 0, nbytes, 0x00020000);
-    const uint32_t voff = static_cast<uint32_t>((lane >> 2) * 64 +
-                                                ((lane & 3) ^ swz_row(lane >> 2)) * 16);
+    const uint32_t voff = static_cast<uint32_t>(
+        (lane >> 2) * 64 + ((lane & 3) ^ swz_row(16 * (u & 1) + (lane >> 2))) * 16);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + u * 1024), 16, voff, u * 1024, 0,
                                              0);
 }
+
+// Where the sum runs over rows: the halves of a row's 64 bytes change places in
+// every other eight rows, so that the 32 lanes of one LDS cycle, which read 32
+// bytes each of four rows and of four rows eight further, hit all banks.
+__device__ __forceinline__ int swz_col(int k) { return (k >> 3) & 1; }
 
 // The rows [32 s, 32 s + 32) of panels of `panel` bytes each, in LDS one
 // panel's 2 KB after the other; load u: half a panel's.
@@ -195,32 +197,32 @@ __device__ __forceinline__ void fill_cols(lds_char *dst, const char *src, uint32
                                           uint32_t panel, int s, int u, int lane) {
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(src), 0, nbytes, 0x00020000);
+    const uint32_t voff = static_cast<uint32_t>((lane ^ (swz_col(lane >> 2) << 1)) * 16);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        r, (lds_void *)(dst + u * 1024), 16, static_cast<uint32_t>(lane) * 16u,
+        r, (lds_void *)(dst + u * 1024), 16, voff,
         static_cast<uint32_t>(u >> 1) * panel + (u & 1) * 1024 + s * 2048, 0, 0);
 }
 
-// Operand of 32 rows and 16 elements of the sum: this lane's row, its 8.
-__device__ __forceinline__ f16x8 read_rows(const lds_char *t, int row, int ks, int lane) {
-    const int c = (ks * 2 + (lane >> 5)) ^ swz_row(row);
-    return *(const lds_f16x8 *)(t + row * 64 + c * 16);
+// Operand of 16 rows and 32 elements of the sum: this lane's row, its 8.
+__device__ __forceinline__ f16x8 read_rows(const lds_char *t, int row, int lane) {
+    return *(const lds_f16x8 *)(t + row * 64 + ((lane >> 4) ^ swz_row(row)) * 16);
 }
 
-// Four rows at t, row bytes apart, of 16 columns: lane l of a 16-lane group
-// reads 4 neighbouring columns (8 bytes) of row l >> 2, and gets column l of
-// the 16 that lanes 0 to 3 read, of those 4 rows.  (restrict: with aliasing
-// facts on the read the compiler does not wait for every load to LDS that is
-// under way before it; the borders wait for those that matter.)
+// Four rows of 16 columns: lane l of a 16-lane group reads 4 neighbouring
+// columns (8 bytes at t) of row l >> 2, and gets column l of the 16 that lanes
+// 0 to 3 read, of those 4 rows.  (restrict: with aliasing facts on the read the
+// compiler does not wait for every load to LDS that is under way before it;
+// the borders wait for those that matter.)
 __device__ __forceinline__ s16x4 read_tr(lds_char *__restrict__ t) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)t);
 }
 
-// The operand from a tile with the sum over rows; col: the first column that
-// this lane reads.  No swizzle is needed: the 32 lanes of one LDS cycle read
-// four whole rows of a panel.
-__device__ __forceinline__ f16x8 read_cols(lds_char *t, int col, int ks, int lane) {
-    const int k = ks * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3);
-    lds_char *at = t + (col >> 5) * 2048 + k * 64 + (col & 31) * 2;
+// The operand from a tile with the sum over rows, of 16 neighbouring columns
+// from col.
+__device__ __forceinline__ f16x8 read_cols(lds_char *t, int col, int lane) {
+    const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);
+    lds_char *at = t + (col >> 5) * 2048 + k * 64 +
+                   ((((col >> 4) & 1) ^ swz_col(k)) * 32) + (lane & 3) * 8;
     union {
         s16x4 s[2];
         f16x8 v;
@@ -242,25 +244,9 @@ __device__ __forceinline__ float settled(float x) {
 union Half8 {
     f16x8 f;
     s16x8 s;
+    s16x4 q[2];
     u32x4 w;
 };
-
-// A wave's 32 x 32 block turned over: in, this lane's column j = perm_row(lane
-// & 31) with rows 16 c + 8 h .. + 8 in v[c]; out, row turned_row(lane) with
-// columns 16 t + 8 (lane >> 5) .. + 8 in v[t].  st: 2 KB of LDS of the wave's.
-__device__ __forceinline__ int turned_row(int lane) { return lane & 31; }
-__device__ __forceinline__ void turn(lds_char *st, Half8 (&v)[2], int lane) {
-    const int h = lane >> 5, j = perm_row(lane & 31);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) *(lds_s16x8 *)(st + j * 64 + c * 32 + h * 16) = v[c].s;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        lds_char *at = st + (16 * t + 8 * h + ((lane >> 2) & 3)) * 64 + ((lane >> 4) & 1) * 32 +
-                       (lane & 3) * 8;
-        const s16x4 a = read_tr(at), b = read_tr(at + 4 * 64);
-        v[t].s = s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    }
-}
 
 // n of 8 bf16 at p, in one store where they are all there and p allows it.
 __device__ __forceinline__ void store_out(uint16_t *p, const Half8 &v, int n, bool vec) {
@@ -286,23 +272,25 @@ __device__ __forceinline__ void border() {
 
 // C = alpha * (sums of P's rows i with Q's rows j), one BM x BN tile a block.
 //
-// NST stages of LDS, of which NST - 1 are on their way while one is read, and
-// two sets of operand registers: while the matrix cores work on one set the
-// other is read, across the stages' borders too.  At a border every wave has
-// its last operands of the old stage in registers (lgkmcnt) and its loads of
-// the next one landed (vmcnt: those after it may be under way); past the barrier the next stage may be read and the old one
-// overwritten.
-template <int KIND, int BM, int BN, int WM, int WN, int NST>
+// NST stages of LDS, of which NST - 1 are on their way while one is read.  A
+// stage's products are made in two parts, for the first and the second half of
+// the wave's rows i; while the matrix cores work on one part the operands of
+// the next are read, across the stages' borders too (rows j alternate between
+// two sets of registers).  At a border every wave has its last operands of the
+// old stage in registers (lgkmcnt) and its loads of the next one landed
+// (vmcnt: those after it may be under way); past the barrier the next stage
+// may be read and the old one overwritten.
+template <int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const OrthoTile *__restrict__ tiles, const OrthoMat *__restrict__ mats, void *ws, int32_t src,
     int32_t first, OrthoCoef coef) {
-    constexpr int WAVES = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
+    constexpr int WAVES = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
+    constexpr int NST = 4;
     constexpr bool kSym = KIND == kGram || KIND == kPoly;
     constexpr int kStage = (BM + BN) * kBK * 2, kLoadsP = BM / 16 / WAVES,
                   kLoadsQ = BN / 16 / WAVES;
     static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0, "whole loads per wave");
-    static_assert(NST * kStage >= WAVES * 2048 && NST >= 3 && NST <= 4,
-                  "LDS of the epilogue; the shortest sum has four stages");
+    static_assert(NST * kStage >= WAVES * 2048 && kBK == 32 && FM % 4 == 0 && FN % 2 == 0, "");
     __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
     lds_char *lds = (lds_char *)smem;
 
@@ -312,16 +300,13 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int i0 = tl.ti * BM, j0 = tl.tj * BN;
-    const int h = lane >> 5;
-    // both operands take their rows through the same permutation
-    const int prow = perm_row(lane & 31);
-    const int pcol = perm_row((lane & 16) | ((lane & 3) << 2));
+    const int g = lane >> 4;
     const OrthoScal sc = *reinterpret_cast<const OrthoScal *>(at(ws, M.scal));
     const char *T = at(ws, src ? M.t[1] : M.t[0]);
 
     // load k of this wave's kLoadsP of stage s's rows i, or of its kLoadsQ of the rows j
-    auto fill_p = [&](int s, int buf, int k) {
-        lds_char *b = lds + buf * kStage;
+    auto fill_p = [&](int s, int k) {
+        lds_char *b = lds + (s & (NST - 1)) * kStage;
         const int u = k * WAVES + wave;
         if constexpr (KIND == kGram) {
             // rows of X^T are the sum, columns i and j
@@ -334,8 +319,8 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
             fill_rows(b, A + (static_cast<int64_t>(s) * M.mp + i0) * 64, n * 64u, u, lane);
         }
     };
-    auto fill_q = [&](int s, int buf, int k) {
-        lds_char *b = lds + buf * kStage + BM * 64;
+    auto fill_q = [&](int s, int k) {
+        lds_char *b = lds + (s & (NST - 1)) * kStage + BM * 64;
         const int u = k * WAVES + wave;
         if constexpr (KIND == kGram) {
             const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
@@ -347,108 +332,114 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
             fill_rows(b, A + (static_cast<int64_t>(s) * rq + j0) * 64, n * 64u, u, lane);
         }
     };
-    f16x8 p[2][FM], q[2][FN];
-    // operand k of a set, the first product's first: rows i, then j, in turn
-    auto read = [&](int set, int buf, int ks, int k) {
-        lds_char *bp = lds + buf * kStage, *bq = bp + BM * 64;
-        const bool isq = k == 1 || k > FM;
-        const int x = isq ? (k == 1 ? 0 : k - FM) : (k == 0 ? 0 : k - 1);
-        const int base = isq ? wn * WTN + x * 32 : wm * WTM + x * 32;
-        f16x8 v;
-        if constexpr (KIND == kGram) v = read_cols(isq ? bq : bp, base + pcol, ks, lane);
-        else v = read_rows(isq ? bq : bp, base + prow, ks, lane);
-        if (isq) q[set][x] = v;
-        else p[set][x] = v;
+    f16x8 p[2][FM / 2], q[2][FN];
+    // operand k of part h of stage s's rows i; of its rows j, into set `set`
+    auto read_p = [&](int s, int h, int k) {
+        lds_char *t = lds + (s & (NST - 1)) * kStage;
+        const int x = h * (FM / 2) + k, base = wm * WTM + (x >> 1) * 32;
+        if constexpr (KIND == kGram) p[h][k] = read_cols(t, base + (x & 1) * 16, lane);
+        else p[h][k] = read_rows(t, base + perm_row(lane & 15, x & 1), lane);
+    };
+    auto read_q = [&](int s, int set, int y) {
+        lds_char *t = lds + (s & (NST - 1)) * kStage + BM * 64;
+        const int base = wn * WTN + (y >> 1) * 32;
+        if constexpr (KIND == kGram) q[set][y] = read_cols(t, base + (y & 1) * 16, lane);
+        else q[set][y] = read_rows(t, base + perm_row(lane & 15, y & 1), lane);
     };
 
-    const int steps = (KIND == kGram ? M.np : M.mp) / kBK;       // four at least
+    const int steps = (KIND == kGram ? M.np : M.mp) / kBK;       // a multiple of four
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s) {
 #pragma unroll
-        for (int k = 0; k < kLoadsP; ++k) fill_p(s, s, k);
+        for (int k = 0; k < kLoadsP; ++k) fill_p(s, k);
 #pragma unroll
-        for (int k = 0; k < kLoadsQ; ++k) fill_q(s, s, k);
+        for (int k = 0; k < kLoadsQ; ++k) fill_q(s, k);
     }
-    f32x16 acc[FM][FN];
+    f32x4 acc[FM][FN];
     if constexpr (kSym) {
 #pragma unroll
         for (int x = 0; x < FM; ++x)
 #pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
+            for (int y = 0; y < FN; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     } else {
         // the sums start from a X, so that its loads overlap the first stages'
         const float ca = ldexpf(coef.a, kLogA);
 #pragma unroll
-        for (int x = 0; x < FM; ++x)
+        for (int x = 0; x < FM; x += 2)
 #pragma unroll
-            for (int y = 0; y < FN; ++y)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int i = i0 + wm * WTM + x * 32 + 16 * c + 8 * h;
-                    const int j = j0 + wn * WTN + y * 32 + prow;
-                    f16x8 hi{}, lo{};
-                    if (i < M.mp && j < M.np) {
-                        const int64_t o = panel_at(M.np, j, i);
-                        hi = reinterpret_cast<const f16x8 *>(T)[o >> 3];
-                        lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o >> 3];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[x][y][8 * c + e] =
-                            ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e]));
+            for (int y = 0; y < FN; ++y) {
+                const int i = i0 + wm * WTM + x * 16 + 8 * g;
+                const int j = j0 + wn * WTN + (y >> 1) * 32 + perm_row(lane & 15, y & 1);
+                f16x8 hi{}, lo{};
+                if (i < M.mp && j < M.np) {
+                    const int64_t o = panel_at(M.np, j, i) >> 3;
+                    hi = reinterpret_cast<const f16x8 *>(T)[o];
+                    lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o];
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    acc[x + (e >> 2)][y][e & 3] =
+                        ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e]));
+            }
     }
     border<0>();
 #pragma unroll
-    for (int k = 0; k < FM + FN; ++k) read(0, 0, 0, k);
-    // The products of one set; after each, its share of the next set's reads
+    for (int k = 0; k < FM / 2; ++k) read_p(0, 0, k);
+#pragma unroll
+    for (int y = 0; y < FN; ++y) read_q(0, 0, y);
+    // The products of one part; after each, its share of the next part's reads
     // and of the loads: a wave issues in order, and a burst of loads that the
     // memory path cannot take at once would hold up its products.
-    auto multiply = [&](int set, auto reads, auto loads, auto &&rd, auto &&ld) {
-        constexpr int n = FM * FN, R = reads.value, L = loads.value;
+    auto multiply = [&](int h, int set, auto reads, auto loads, auto &&rd, auto &&ld) {
+        constexpr int n = FM / 2 * FN, R = reads.value, L = loads.value;
 #pragma unroll
         for (int k = 0; k < n; ++k) {
             const int x = k / FN, y = k % FN;
-            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(p[set][x], q[set][y], acc[x][y], 0,
-                                                               0, 0);
-            // the reads go first, so that the last have a product or more to land
+            f32x4 &c = acc[h * (FM / 2) + x][y];
+            c = __builtin_amdgcn_mfma_f32_16x16x32_f16(p[h][x], q[set][y], c, 0, 0, 0);
+            // the reads go first, so that the last have some products to land
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (r * (n - 1) / (FM + FN) == k) rd(r);
+                if (r * (n - 2) / (R > 0 ? R : 1) == k) rd(r);
 #pragma unroll
             for (int l = 0; l < L; ++l)
                 if ((2 * l + 1) * n / (2 * (L > 0 ? L : 1)) == k) ld(l);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // One stage: two sets.  No branch lies between a read of operands and their
-    // use, so that the compiler waits for the older set of reads alone.
-    static_assert(kBK == 32, "a stage is two sets of operands");
-    int buf = 0;
-    auto stage = [&](auto wait, auto more, int s) {
+    // One stage; set: its rows j.  No branch lies between a read of operands
+    // and their use, so that the compiler waits for the older reads alone.
+    auto stage = [&](auto wait, auto more, int set, int s) {
         constexpr int LP = more.value > 1 ? kLoadsP : 0, LQ = more.value > 1 ? kLoadsQ : 0;
-        constexpr int R = FM + FN;
-        const int last = buf == 0 ? NST - 1 : buf - 1;      // read before the last border
-        multiply(0, Int<R>{}, Int<LP>{}, [&](int k) { read(1, buf, 1, k); },
-                 [&](int k) { fill_p(s + NST - 1, last, k); });
-        buf = buf == NST - 1 ? 0 : buf + 1;
+        multiply(0, set, Int<FM / 2>{}, Int<LP>{}, [&](int k) { read_p(s, 1, k); },
+                 [&](int k) { fill_p(s + NST - 1, k); });
         if constexpr (more.value > 0) border<wait.value>();
-        multiply(1, Int<(more.value > 0 ? R : 0)>{}, Int<LQ>{}, [&](int k) { read(0, buf, 0, k); },
-                 [&](int k) { fill_q(s + NST - 1, last, k); });
+        multiply(1, set, Int<(more.value > 0 ? FM / 2 + FN : 0)>{}, Int<LQ>{},
+                 [&](int k) {
+                     // the first product's operands first
+                     if (k == 0) read_p(s + 1, 0, 0);
+                     else if (k <= FN) read_q(s + 1, set ^ 1, k - 1);
+                     else read_p(s + 1, 0, k - FN);
+                 },
+                 [&](int k) { fill_q(s + NST - 1, k); });
     };
     constexpr int kLoads = kLoadsP + kLoadsQ;
-    int s = 0;
     // loads younger than the next stage's: NST - 3 stages and this one's first
-    for (; s + NST - 1 < steps; ++s) stage(Int<kLoads *(NST - 3) + kLoadsP>{}, Int<2>{}, s);
-    // what is left was filled: NST - 2 stages with a border, and the last one
-    if constexpr (NST > 3) stage(Int<kLoads *(NST - 3)>{}, Int<1>{}, s++);
-    if constexpr (NST > 2) stage(Int<0>{}, Int<1>{}, s++);
-    stage(Int<0>{}, Int<0>{}, s);
+    constexpr Int<kLoads *(NST - 3) + kLoadsP> kWait{};
+    int s = 0;
+    for (; s + NST < steps; s += 2) {
+        stage(kWait, Int<2>{}, 0, s);
+        stage(kWait, Int<2>{}, 1, s + 1);
+    }
+    // the last four: one more to load, two with a border, the last
+    stage(kWait, Int<2>{}, 0, s);
+    stage(Int<kLoads>{}, Int<1>{}, 1, s + 1);
+    stage(Int<0>{}, Int<1>{}, 0, s + 2);
+    stage(Int<0>{}, Int<0>{}, 1, s + 3);
 
-    // Epilogue.  Of block (x, y) this lane has column j and, for c = 0, 1, the
-    // rows 16 c + 8 h .. + 8 in acc[8 c .. 8 c + 8).
+    // Epilogue, block by block of 32 x 32.  For b = 0, 1 this lane has column
+    // colb(b) and, in v[b], the rows 8 g .. + 8 (X X^T: 4 g .. + 4 of either
+    // half of the rows).
     lds_char *st = lds + wave * 2048;
     if constexpr (kSym || KIND == kLast) border<0>();
     const float phi = first ? sc.phi0 : sc.phi, rho = first ? sc.rho : 1.0f;
@@ -457,74 +448,88 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                                         : ldexpf(rho, -kLogA);
     const bool vec = KIND == kLast && (lo32(M.out) & 15u) == 0 && (M.cols & 7) == 0;
 #pragma unroll
-    for (int x = 0; x < FM; ++x)
+    for (int x = 0; x < FM; x += 2)
 #pragma unroll
-        for (int y = 0; y < FN; ++y) {
-            const int ib = i0 + wm * WTM + x * 32, jb = j0 + wn * WTN + y * 32, j = jb + prow;
+        for (int y = 0; y < FN; y += 2) {
+            const int ib = i0 + wm * WTM + x * 16, jb = j0 + wn * WTN + y * 16;
             if (ib >= M.mp || jb >= (kSym ? M.mp : M.np)) continue;
             Half8 v[2];
+            int col[2], row[2];         // of the block; rows: of the first and second four
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int i = ib + 16 * c + 8 * h;
-                if constexpr (kSym) {
-                    f16x8 *C = reinterpret_cast<f16x8 *>(at(ws, KIND == kGram ? M.a : M.b));
-                    const int64_t o = panel_at(M.mp, j, i) >> 3;
-                    f16x8 old{};
-                    if constexpr (KIND == kPoly)
-                        old = reinterpret_cast<const f16x8 *>(at(ws, M.a))[o];
+            for (int b = 0; b < 2; ++b) {
+                col[b] = KIND == kGram ? 16 * b + (lane & 15) : perm_row(lane & 15, b);
+                row[b] = KIND == kGram ? 16 * b + 4 * g : 8 * g + 4 * b;
+            }
+            char *C = at(ws, KIND == kGram ? M.a : M.b);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float t = alpha * acc[x][y][8 * c + e];
-                        if constexpr (KIND == kPoly) t = coef.b * static_cast<float>(old[e]) + t;
-                        v[c].f[e] = static_cast<_Float16>(t);
-                    }
-                    C[o] = v[c].f;
+            for (int b = 0; b < 2; ++b) {
+                float t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = alpha * acc[x + (e >> 2)][y + b][e & 3];
+                const int64_t o = panel_at(kSym ? M.mp : M.np, jb + col[b], ib + row[0]);
+                if constexpr (KIND == kGram) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[b].f[e] = static_cast<_Float16>(t[e]);
+                    s16x4 *c = reinterpret_cast<s16x4 *>(C) + (o >> 2);
+                    c[0] = v[b].q[0];
+                    c[4] = v[b].q[1];
+                } else if constexpr (KIND == kPoly) {
+                    const f16x8 old = reinterpret_cast<const f16x8 *>(at(ws, M.a))[o >> 3];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[b].f[e] =
+                            static_cast<_Float16>(coef.b * static_cast<float>(old[e]) + t[e]);
+                    reinterpret_cast<f16x8 *>(C)[o >> 3] = v[b].f;
                 } else if constexpr (KIND == kApply) {
-                    const int64_t o = panel_at(M.np, j, i) >> 3;
-                    f16x8 vl;
+                    f16x8 lo;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float t = settled(alpha * acc[x][y][8 * c + e]);
-                        v[c].f[e] = static_cast<_Float16>(t);
-                        vl[e] = static_cast<_Float16>(t - static_cast<float>(v[c].f[e]));
+                        const float f = settled(t[e]);
+                        v[b].f[e] = static_cast<_Float16>(f);
+                        lo[e] = static_cast<_Float16>(f - static_cast<float>(v[b].f[e]));
                     }
-                    reinterpret_cast<f16x8 *>(at(ws, src ? M.t[0] : M.t[1]))[o] = v[c].f;
-                    reinterpret_cast<f16x8 *>(at(ws, M.lo))[o] = vl;
+                    reinterpret_cast<f16x8 *>(at(ws, src ? M.t[0] : M.t[1]))[o >> 3] = v[b].f;
+                    reinterpret_cast<f16x8 *>(at(ws, M.lo))[o >> 3] = lo;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[c].s[e] = static_cast<short>(
-                            bf16_rne(alpha * acc[x][y][8 * c + e] * sc.phi));
+                        v[b].s[e] = static_cast<short>(bf16_rne(t[e] * sc.phi));
                 }
             }
+            // the block turned over, through 2 KB of LDS: row ib + (lane & 31), its
+            // columns 16 t + 8 (lane >> 5) .. + 8 in v[t]
+            if ((kSym && tl.ti != tl.tj) || (KIND == kLast && M.wide)) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *(lds_s16x4 *)(st + col[b] * 64 + row[c] * 2) = v[b].q[c];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    lds_char *a = st + (16 * t + 8 * (lane >> 5) + ((lane >> 2) & 3)) * 64 +
+                                  (g & 1) * 32 + (lane & 3) * 8;
+                    v[t].q[0] = read_tr(a);
+                    v[t].q[1] = read_tr(a + 4 * 64);
+                }
+            }
+            const int tr = ib + (lane & 31);
             if constexpr (kSym) {
                 // a tile off the diagonal is its mirror image's values too
                 if (tl.ti != tl.tj) {
-                    turn(st, v, lane);
-                    f16x8 *C = reinterpret_cast<f16x8 *>(at(ws, KIND == kGram ? M.a : M.b));
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        C[panel_at(M.mp, ib + turned_row(lane), jb + 16 * t + 8 * h) >> 3] = v[t].f;
+                        reinterpret_cast<f16x8 *>(
+                            C)[panel_at(M.mp, tr, jb + 16 * t + 8 * (lane >> 5)) >> 3] = v[t].f;
                 }
             } else if constexpr (KIND == kLast) {
-                if (M.wide) {
-                    turn(st, v, lane);
-                    const int i = ib + turned_row(lane);
+                // the row and the first of 8 neighbouring columns of the output
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int jj = jb + 16 * t + 8 * h;
-                        if (i < M.m && jj < M.n)
-                            store_out(M.out + static_cast<int64_t>(i) * M.cols + jj, v[t],
-                                      M.n - jj, vec);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int i = ib + 16 * c + 8 * h;
-                        if (i < M.m && j < M.n)
-                            store_out(M.out + static_cast<int64_t>(j) * M.cols + i, v[c], M.m - i,
-                                      vec);
-                    }
+                for (int t = 0; t < 2; ++t) {
+                    const int r = M.wide ? tr : jb + col[t];
+                    const int c = M.wide ? jb + 16 * t + 8 * (lane >> 5) : ib + 8 * g;
+                    if (r < M.rows && c < M.cols)
+                        store_out(M.out + static_cast<int64_t>(r) * M.cols + c, v[t], M.cols - c,
+                                  vec);
                 }
             }
         }
@@ -542,10 +547,7 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
 #define FSDP_ORTHO_WM 2
 #define FSDP_ORTHO_WN 2
 #endif
-#ifndef FSDP_ORTHO_NST
-#define FSDP_ORTHO_NST 4
-#endif
-#define TILE_ARGS FSDP_ORTHO_BM, FSDP_ORTHO_BN, FSDP_ORTHO_WM, FSDP_ORTHO_WN, FSDP_ORTHO_NST
+#define TILE_ARGS FSDP_ORTHO_BM, FSDP_ORTHO_BN, FSDP_ORTHO_WM, FSDP_ORTHO_WN
 #define TILE_THR (64 * FSDP_ORTHO_WM * FSDP_ORTHO_WN)
 
 hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
