@@ -605,8 +605,9 @@ fsdp_status fsdp_muon_update(const fsdp_plan *plan, const uint16_t *upd, uint16_
  * to 22 bits: the result is within about 2e-3 of the exact iterate before its
  * rounding to bf16 (relative, in the 2-norm, for the default coefficients).  A
  * matrix that holds a NaN or an infinity becomes NaN throughout; one of zeros
- * stays zero (with eps > 0).  Results do not depend on the other matrices of
- * the plan.
+ * stays zero (with eps > 0).  A plan gives the same bits every time; which other
+ * matrices a plan has may change how a matrix's fp32 sums are split, and so its
+ * last bits, but never by what those hold.
  *
  * A plan covers many matrices of any shapes (their products share launches);
  * binding names their memory; executing enqueues the products. */

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstdint>
 #include <string>
 #include <vector>
@@ -16,7 +17,9 @@ struct fsdp_ortho_plan {
     std::vector<fsdp::OrthoMat> mats;       // matrices with elements; in, out set by bind
     std::vector<int32_t> index;             // their places in the caller's list
     std::vector<fsdp::OrthoCoef> coef;
-    std::vector<fsdp::OrthoTile> norm, init, sym, apply;
+    std::vector<fsdp::OrthoTile> norm, init, gram, join, poly, apply;
+    std::vector<fsdp::OrthoTile> one[3], slabs[3], sums;    // few rows: 32, 64, 128
+    int32_t t_gram = 128, t_poly = 128, t_apply = 128, split = 1;   // tiles' sides, parts of X X^T
     int32_t n_mats = 0, growth = 0;
     double eps = 0.0;
     int64_t ws_bytes = 0;
@@ -108,6 +111,43 @@ void spread(std::vector<fsdp::OrthoTile> *tiles) {
     }
 }
 
+// Bytes of parts of A that a block sums by itself.
+constexpr int64_t kSumsInBlock = 192 << 10;
+
+// Tile sides and the parts of X X^T's sum.
+void choose(fsdp_ortho_plan *p) {
+    auto env = [](const char *n, int32_t d) { const char *v = std::getenv(n); return v ? std::atoi(v) : d; };
+    p->t_gram = env("OT_G", 128);
+    p->t_poly = env("OT_P", 128);
+    p->t_apply = env("OT_A", 128);
+    p->split = env("OT_S", 1);
+    for (const fsdp::OrthoMat &M : p->mats)
+        if (M.m > fsdp::kSmallMax) p->split = std::min(p->split, M.np / 128);
+}
+
+// A matrix of few rows: its slabs; true if it needs no norm of its own (one
+// slab: the block that works on it takes it).
+template <typename F>
+bool few_rows(int32_t id, fsdp::OrthoMat *M, fsdp_ortho_plan *p, F &&take) {
+    const int cls = M->mp == 32 ? 0 : M->mp == 64 ? 1 : 2;
+    const int32_t nb = fsdp::small_slab(M->mp), slabs = (M->n + nb - 1) / nb;
+    if (slabs == 1) {
+        p->one[cls].push_back({id, 0, 0, 0});
+        return true;
+    }
+    const int64_t part = static_cast<int64_t>(M->mp) * M->mp * 4;
+    M->t[0] = take(static_cast<int64_t>(slabs) * nb * M->mp * 4);
+    M->a = take(slabs * part);
+    M->b = take(slabs * part);
+    for (int32_t s = 0; s < slabs; ++s) p->slabs[cls].push_back({id, s, 0, 0});
+    M->n_sums = slabs;
+    if (slabs * part > kSumsInBlock) {
+        M->n_sums = 1;
+        for (int32_t t = 0; t < part / 16 / 256; ++t) p->sums.push_back({id, t, slabs, 0});
+    }
+    return false;
+}
+
 void layout(fsdp_ortho_plan *p) {
     int64_t off = 0;
     auto take = [&](int64_t bytes) {
@@ -117,6 +157,15 @@ void layout(fsdp_ortho_plan *p) {
     };
     for (size_t i = 0; i < p->mats.size(); ++i) {
         fsdp::OrthoMat &M = p->mats[i];
+        const int32_t id = static_cast<int32_t>(i);
+        const int64_t total = static_cast<int64_t>(M.rows) * M.cols;
+        if (M.m <= fsdp::kSmallMax && few_rows(id, &M, p, take)) continue;
+        M.n_parts = static_cast<int32_t>(std::max<int64_t>(
+            1, std::min<int64_t>(fsdp::kOrthoParts, total / fsdp::kOrthoPartMin)));
+        M.parts = take(M.n_parts * 8);
+        M.scal = take(sizeof(fsdp::OrthoScal));
+        for (int32_t t = 0; t < M.n_parts; ++t) p->norm.push_back({id, t, 0, 0});
+        if (M.m <= fsdp::kSmallMax) continue;
         const int64_t x = static_cast<int64_t>(M.np) * M.mp * 2;
         const int64_t s = static_cast<int64_t>(M.mp) * M.mp * 2;
         M.t[0] = take(x);
@@ -124,26 +173,50 @@ void layout(fsdp_ortho_plan *p) {
         M.lo = take(x);
         M.a = take(s);
         M.b = take(s);
-        const int64_t total = static_cast<int64_t>(M.rows) * M.cols;
-        M.n_parts = static_cast<int32_t>(std::max<int64_t>(
-            1, std::min<int64_t>(fsdp::kOrthoParts, total / fsdp::kOrthoPartMin)));
-        M.parts = take(M.n_parts * 8);
-        M.scal = take(sizeof(fsdp::OrthoScal));
-        const int32_t id = static_cast<int32_t>(i);
-        for (int32_t t = 0; t < M.n_parts; ++t) p->norm.push_back({id, t, 0, 0});
         for (int32_t j = 0; j < M.np / 64; ++j)
             for (int32_t k = 0; k < M.mp / 64; ++k) p->init.push_back({id, k, j, 0});
-#ifndef FSDP_ORTHO_BM
-#define FSDP_ORTHO_BM 128
-#define FSDP_ORTHO_BN 128
-#endif
-        const int32_t ta = (M.mp + FSDP_ORTHO_BM - 1) / FSDP_ORTHO_BM;
-        blocks(id, ta, ta, true, &p->sym);
-        blocks(id, ta, (M.np + FSDP_ORTHO_BN - 1) / FSDP_ORTHO_BN, false, &p->apply);
+    }
+    choose(p);
+    for (size_t i = 0; i < p->mats.size(); ++i) {
+        const fsdp::OrthoMat &M = p->mats[i];
+        const int32_t id = static_cast<int32_t>(i);
+        if (M.m <= fsdp::kSmallMax) continue;
+        auto count = [](int32_t side, int32_t tile) { return (side + tile - 1) / tile; };
+        blocks(id, count(M.mp, p->t_gram), count(M.mp, p->t_gram), true, &p->gram);
+        blocks(id, count(M.mp, p->t_poly), count(M.mp, p->t_poly), true, &p->poly);
+        blocks(id, count(M.mp, p->t_apply), count(M.np, p->t_apply), false, &p->apply);
+    }
+    if (p->split > 1) {
+        p->join = p->gram;
+        p->gram.clear();
+        int32_t part = 0;
+        for (fsdp::OrthoTile &t : p->join) {
+            t.part = part;
+            for (int32_t k = 0; k < p->split; ++k) p->gram.push_back({t.mat, t.ti, t.tj, part++});
+        }
+        const int64_t sums = take(static_cast<int64_t>(part) * p->t_gram * p->t_gram * 4);
+        for (fsdp::OrthoMat &M : p->mats) M.sums = sums;
     }
     p->ws_bytes = off;
-    spread(&p->sym);
+    spread(&p->gram);
+    spread(&p->join);
+    spread(&p->poly);
     spread(&p->apply);
+}
+
+// The device tables in their order: matrices, coefficients, tiles.
+struct Table {
+    const void *src;
+    size_t bytes;
+};
+std::vector<Table> tables(const fsdp_ortho_plan &p, const std::vector<fsdp::OrthoMat> &mats) {
+    std::vector<Table> t = {{mats.data(), mats.size() * sizeof(fsdp::OrthoMat)},
+                            {p.coef.data(), p.coef.size() * sizeof(fsdp::OrthoCoef)}};
+    for (const std::vector<fsdp::OrthoTile> *v :
+         {&p.norm, &p.init, &p.gram, &p.join, &p.poly, &p.apply, &p.one[0], &p.one[1], &p.one[2],
+          &p.slabs[0], &p.slabs[1], &p.slabs[2], &p.sums})
+        t.push_back({v->data(), v->size() * sizeof(fsdp::OrthoTile)});
+    return t;
 }
 
 fsdp_status hip_error(hipError_t e, const char *what) { return fsdp::set_hip_error(e, what); }
@@ -184,14 +257,15 @@ fsdp_status fsdp_ortho_plan_create(const int64_t *rows, const int64_t *cols, int
             M.wide = M.rows <= M.cols ? 1 : 0;
             M.m = std::min(M.rows, M.cols);
             M.n = std::max(M.rows, M.cols);
-            M.mp = static_cast<int32_t>(round_up(M.m, fsdp::kOrthoPad));
+            M.mp = M.m <= fsdp::kSmallMax ? fsdp::small_rows_of(M.m)
+                                          : static_cast<int32_t>(round_up(M.m, fsdp::kOrthoPad));
             M.np = static_cast<int32_t>(round_up(M.n, fsdp::kOrthoPad));
             p->mats.push_back(M);
             p->index.push_back(i);
         }
         if (s == FSDP_OK) layout(p);
         const size_t most = size_t{1} << 30;
-        if (s == FSDP_OK && (p->apply.size() > most || p->init.size() > most))
+        if (s == FSDP_OK && (p->apply.size() > most || p->gram.size() > most || p->init.size() > most))
             s = set_error(FSDP_E_UNSUPPORTED, "fsdp_ortho_plan_create: too many tiles for one launch");
         if (s != FSDP_OK) {
             delete p;
@@ -267,14 +341,7 @@ fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *p, const void *const *in, uint16_t 
     if (e != hipSuccess) return hip_error(e, "fsdp_ortho_bind: hipGetDevice");
     if (p->dmem != nullptr && dev != p->device)
         return set_error(FSDP_E_STATE, "fsdp_ortho_bind: plan already bound on another device");
-    const struct {
-        const void *src;
-        size_t bytes;
-    } tabs[5] = {{mats.data(), mats.size() * sizeof(fsdp::OrthoMat)},
-                 {p->norm.data(), p->norm.size() * sizeof(fsdp::OrthoTile)},
-                 {p->init.data(), p->init.size() * sizeof(fsdp::OrthoTile)},
-                 {p->sym.data(), p->sym.size() * sizeof(fsdp::OrthoTile)},
-                 {p->apply.data(), p->apply.size() * sizeof(fsdp::OrthoTile)}};
+    const std::vector<Table> tabs = tables(*p, mats);
     if (p->dmem == nullptr) {
         size_t total = 256;
         for (const auto &t : tabs) total += round_up(static_cast<int64_t>(t.bytes), 256);
@@ -312,7 +379,7 @@ fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *p, void *workspace, int64_
     if (p == nullptr) return set_error(FSDP_E_INVAL, "fsdp_ortho_execute: null plan");
     if (!p->bound) return set_error(FSDP_E_STATE, "fsdp_ortho_execute: plan not bound");
     if (p->mats.empty()) return FSDP_OK;
-    if (workspace == nullptr || workspace_bytes < p->ws_bytes)
+    if ((workspace == nullptr && p->ws_bytes > 0) || workspace_bytes < p->ws_bytes)
         return set_error(FSDP_E_INVAL, "fsdp_ortho_execute: the workspace needs " +
                                            std::to_string(p->ws_bytes) + " bytes");
     const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace);
@@ -329,41 +396,65 @@ fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *p, void *workspace, int64_
         return set_error(FSDP_E_STATE, "fsdp_ortho_execute: current device differs from the bound one");
 
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    const std::vector<Table> tabs = tables(*p, p->mats);
     const char *cur = p->dmem;
-    auto table = [&](size_t bytes) {
-        const char *t = cur;
-        cur += round_up(static_cast<int64_t>(bytes), 256);
-        return t;
-    };
-    auto tiles = [&](const std::vector<fsdp::OrthoTile> &v) {
-        return reinterpret_cast<const fsdp::OrthoTile *>(table(v.size() * sizeof(fsdp::OrthoTile)));
-    };
-    const auto *mats = reinterpret_cast<const fsdp::OrthoMat *>(
-        table(p->mats.size() * sizeof(fsdp::OrthoMat)));
-    const fsdp::OrthoTile *norm = tiles(p->norm), *init = tiles(p->init), *sym = tiles(p->sym),
-                          *apply = tiles(p->apply);
-    auto run = [&](auto &&launch) {
-        if (e == hipSuccess) e = fsdp::injected_fault();
+    const char *where[15];
+    for (size_t t = 0; t < tabs.size(); ++t) {
+        where[t] = cur;
+        cur += round_up(static_cast<int64_t>(tabs[t].bytes), 256);
+    }
+    const auto *mats = reinterpret_cast<const fsdp::OrthoMat *>(where[0]);
+    const auto *coefs = reinterpret_cast<const fsdp::OrthoCoef *>(where[1]);
+    auto tiles = [&](int t) { return reinterpret_cast<const fsdp::OrthoTile *>(where[t]); };
+    const fsdp::OrthoTile *norm = tiles(2), *init = tiles(3), *gram = tiles(4), *join = tiles(5),
+                          *poly = tiles(6), *apply = tiles(7), *sums = tiles(14);
+    auto count = [](const std::vector<fsdp::OrthoTile> &v) { return static_cast<int64_t>(v.size()); };
+    const int32_t n_steps = static_cast<int32_t>(p->coef.size());
+    auto run = [&](const std::vector<fsdp::OrthoTile> &v, auto &&launch) {
+        if (v.empty() || e != hipSuccess) return;
+        e = fsdp::injected_fault();
         if (e == hipSuccess) e = launch();
     };
-    run([&] {
+    // matrices of few rows: the classes' one-slab launches, or one of the slabs'
+    auto small = [&](int32_t mode, int32_t step) {
+        for (int c = 0; c < 3; ++c) {
+            const std::vector<fsdp::OrthoTile> &v = mode == fsdp::kSmallAll ? p->one[c] : p->slabs[c];
+            run(v, [&] {
+                return fsdp::launch_ortho_small(32 << c, tiles((mode == fsdp::kSmallAll ? 8 : 11) + c),
+                                                count(v), mats, workspace, p->f32, mode, step,
+                                                n_steps, coefs, p->eps, p->growth, st);
+            });
+        }
+    };
+    run(p->norm, [&] {
         return fsdp::launch_ortho_norm(norm, static_cast<int64_t>(p->norm.size()), mats, workspace,
                                        p->f32, st);
     });
-    run([&] {
+    small(fsdp::kSmallAll, 0);
+    small(fsdp::kSmallStart, 0);
+    run(p->init, [&] {
         return fsdp::launch_ortho_init(init, static_cast<int64_t>(p->init.size()), mats, workspace,
                                        p->f32, p->eps, p->growth, st);
     });
-    const int64_t n_sym = static_cast<int64_t>(p->sym.size());
-    const int64_t n_apply = static_cast<int64_t>(p->apply.size());
     for (size_t k = 0; k < p->coef.size(); ++k) {
         const int32_t src = static_cast<int32_t>(k & 1);
         const bool last = k + 1 == p->coef.size();
-        run([&] { return fsdp::launch_ortho_gram(sym, n_sym, mats, workspace, src, k == 0, st); });
-        run([&] { return fsdp::launch_ortho_poly(sym, n_sym, mats, workspace, p->coef[k], st); });
-        run([&] {
-            return fsdp::launch_ortho_apply(apply, n_apply, mats, workspace, src, k == 0, last,
-                                            p->coef[k], st);
+        run(p->sums, [&] {
+            return fsdp::launch_ortho_sums(sums, count(p->sums), mats, workspace,
+                                           static_cast<int32_t>(k), st);
+        });
+        small(last ? fsdp::kSmallLast : fsdp::kSmallStep, static_cast<int32_t>(k));
+        run(p->gram, [&] {
+            return fsdp::launch_ortho_gram(p->t_gram, gram, count(p->gram), join, count(p->join),
+                                           p->split, mats, workspace, src, k == 0, st);
+        });
+        run(p->poly, [&] {
+            return fsdp::launch_ortho_poly(p->t_poly, poly, count(p->poly), mats, workspace,
+                                           p->coef[k], st);
+        });
+        run(p->apply, [&] {
+            return fsdp::launch_ortho_apply(p->t_apply, apply, count(p->apply), mats, workspace, src,
+                                            k == 0, last, p->coef[k], st);
         });
     }
     return e == hipSuccess ? FSDP_OK : hip_error(e, (std::string(call) + ": launch").c_str());

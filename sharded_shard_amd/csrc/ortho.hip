@@ -38,6 +38,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) s16x8 lds_s16x8;
+typedef __attribute__((address_space(3))) f16x4 lds_f16x4;
 typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
 
 // log2 of the scale of A and B
@@ -95,9 +96,34 @@ __global__ __launch_bounds__(kBlock) void ortho_norm_kernel(const OrthoTile *__r
     if (threadIdx.x == 0) reinterpret_cast<double *>(at(ws, M.parts))[tl.ti] = s;
 }
 
+// The scalars of a matrix from its norm: X = U / (norm + eps) is stored as U
+// 2^k, which puts the norm at 2^kLogX or up to twice that.  X is small where
+// eps outweighs the norm; up to what the iterations can magnify it back
+// (2^growth), it is scaled up instead.  A norm that is not finite makes the
+// scalars NaN and so every output; the stored X is then to be zero.
+__device__ __forceinline__ OrthoScal scalars(double norm, double eps, int32_t growth, int *k) {
+    OrthoScal s{__builtin_nanf(""), 0.0f, __builtin_nanf(""), 0.0f};
+    *k = 0;
+    if (!isfinite(norm)) return s;
+    int e = 0, up = 0;
+    double p0 = eps > 0.0 ? 1.0 : s.phi0;       // X = stored * p0; zero / 0 is NaN
+    if (norm > 0.0) {
+        e = ilogb(norm);
+        const double r = norm / (norm + eps);
+        up = r > 0.0 ? -ilogb(r) - growth : 100;
+        up = up < 0 ? 0 : (up > 100 ? 100 : up);
+        p0 = 1.0 / ldexp(norm + eps, kLogX - e);
+    }
+    *k = kLogX - e;
+    s.phi = ldexpf(1.0f, -(kLogX + up));
+    s.phi0 = static_cast<float>(p0);
+    s.rho = static_cast<float>(ldexp(p0, kLogX + up));
+    return s;
+}
+
 // X^T's 64 x 64 piece (rows 64 tj of n, columns 64 ti of m).  Stored is U
 // 2^k, exact in fp16 for bf16 inputs within 2^-26 of the norm (the low part
-// holds the rest), where 2^k puts the norm at 2^kLogX or up to twice that.
+// holds the rest).
 template <bool kF32>
 __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__restrict__ tiles,
                                                             const OrthoMat *__restrict__ mats,
@@ -109,29 +135,11 @@ __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__r
     double s = 0.0;
     for (int i = threadIdx.x; i < M.n_parts; i += kBlock) s += parts[i];
     const double norm = sqrt(block_sum(s));
-    // A norm that is not finite makes the scalars NaN and so every output; the
-    // stored X is then zero.  X = U / (norm + eps) is small where eps
-    // outweighs the norm: up to what the iterations can magnify it back, X is
-    // scaled up instead.
     const bool fine = isfinite(norm);
-    int e = 0, up = 0;
-    float phi0 = __builtin_nanf(""), phi = 0.0f, rho = __builtin_nanf("");
-    if (fine) {
-        double p0 = eps > 0.0 ? 1.0 : phi0;       // X = stored * p0; zero / 0 is NaN
-        if (norm > 0.0) {
-            e = ilogb(norm);
-            const double r = norm / (norm + eps);
-            up = r > 0.0 ? -ilogb(r) - growth : 100;
-            up = up < 0 ? 0 : (up > 100 ? 100 : up);
-            p0 = 1.0 / ldexp(norm + eps, kLogX - e);
-        }
-        phi = ldexpf(1.0f, -(kLogX + up));
-        phi0 = static_cast<float>(p0);
-        rho = static_cast<float>(ldexp(p0, kLogX + up));
-    }
+    int k;
+    const OrthoScal sc = scalars(norm, eps, growth, &k);
     if (tl.ti == 0 && tl.tj == 0 && threadIdx.x == 0)
-        *reinterpret_cast<OrthoScal *>(at(ws, M.scal)) = OrthoScal{phi0, phi, rho, 0.0f};
-    const int k = kLogX - e;
+        *reinterpret_cast<OrthoScal *>(at(ws, M.scal)) = sc;
     const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
     const int r0 = (M.wide ? tl.ti : tl.tj) * 64, c0 = (M.wide ? tl.tj : tl.ti) * 64;
     for (int y = ty; y < 64; y += kBlock / 64) {
@@ -157,7 +165,8 @@ __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__r
 // products
 // ---------------------------------------------------------------------------
 
-enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
+// kGramPart: a stretch of kGram's sum, left in fp32; kGramJoin: their sum
+enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3, kGramPart = 4, kGramJoin = 5 };
 
 // elements of the sum per stage: one panel of columns
 constexpr int kBK = 32;
@@ -283,14 +292,15 @@ __device__ __forceinline__ void border() {
 template <int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const OrthoTile *__restrict__ tiles, const OrthoMat *__restrict__ mats, void *ws, int32_t src,
-    int32_t first, OrthoCoef coef) {
+    int32_t first, int32_t split, OrthoCoef coef) {
     constexpr int WAVES = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
     constexpr int NST = 4;
-    constexpr bool kSym = KIND == kGram || KIND == kPoly;
+    constexpr bool kXXT = KIND == kGram || KIND == kGramPart || KIND == kGramJoin;
+    constexpr bool kSym = kXXT || KIND == kPoly;
     constexpr int kStage = (BM + BN) * kBK * 2, kLoadsP = BM / 16 / WAVES,
                   kLoadsQ = BN / 16 / WAVES;
     static_assert(BM % (16 * WAVES) == 0 && BN % (16 * WAVES) == 0, "whole loads per wave");
-    static_assert(NST * kStage >= WAVES * 2048 && kBK == 32 && FM % 4 == 0 && FN % 2 == 0, "");
+    static_assert(NST * kStage >= WAVES * 2048 && kBK == 32 && FM % 2 == 0 && FN % 2 == 0, "");
     __shared__ __attribute__((aligned(1024))) char smem[NST * kStage];
     lds_char *lds = (lds_char *)smem;
 
@@ -304,138 +314,171 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const OrthoScal sc = *reinterpret_cast<const OrthoScal *>(at(ws, M.scal));
     const char *T = at(ws, src ? M.t[1] : M.t[0]);
 
-    // load k of this wave's kLoadsP of stage s's rows i, or of its kLoadsQ of the rows j
-    auto fill_p = [&](int s, int k) {
-        lds_char *b = lds + (s & (NST - 1)) * kStage;
-        const int u = k * WAVES + wave;
-        if constexpr (KIND == kGram) {
-            // rows of X^T are the sum, columns i and j
-            const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
-            const int at = i0 / 32, n = M.mp / 32 - at < BM / 32 ? M.mp / 32 - at : BM / 32;
-            fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
-        } else {
-            const char *A = at(ws, KIND == kPoly ? M.a : M.b);
-            const int n = M.mp - i0 < BM ? M.mp - i0 : BM;
-            fill_rows(b, A + (static_cast<int64_t>(s) * M.mp + i0) * 64, n * 64u, u, lane);
-        }
-    };
-    auto fill_q = [&](int s, int k) {
-        lds_char *b = lds + (s & (NST - 1)) * kStage + BM * 64;
-        const int u = k * WAVES + wave;
-        if constexpr (KIND == kGram) {
-            const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
-            const int at = j0 / 32, n = M.mp / 32 - at < BN / 32 ? M.mp / 32 - at : BN / 32;
-            fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
-        } else {
-            const char *A = KIND == kPoly ? at(ws, M.a) : T;
-            const int rq = KIND == kPoly ? M.mp : M.np, n = rq - j0 < BN ? rq - j0 : BN;
-            fill_rows(b, A + (static_cast<int64_t>(s) * rq + j0) * 64, n * 64u, u, lane);
-        }
-    };
-    f16x8 p[2][FM / 2], q[2][FN];
-    // operand k of part h of stage s's rows i; of its rows j, into set `set`
-    auto read_p = [&](int s, int h, int k) {
-        lds_char *t = lds + (s & (NST - 1)) * kStage;
-        const int x = h * (FM / 2) + k, base = wm * WTM + (x >> 1) * 32;
-        if constexpr (KIND == kGram) p[h][k] = read_cols(t, base + (x & 1) * 16, lane);
-        else p[h][k] = read_rows(t, base + perm_row(lane & 15, x & 1), lane);
-    };
-    auto read_q = [&](int s, int set, int y) {
-        lds_char *t = lds + (s & (NST - 1)) * kStage + BM * 64;
-        const int base = wn * WTN + (y >> 1) * 32;
-        if constexpr (KIND == kGram) q[set][y] = read_cols(t, base + (y & 1) * 16, lane);
-        else q[set][y] = read_rows(t, base + perm_row(lane & 15, y & 1), lane);
-    };
-
-    const int steps = (KIND == kGram ? M.np : M.mp) / kBK;       // a multiple of four
-#pragma unroll
-    for (int s = 0; s < NST - 1; ++s) {
-#pragma unroll
-        for (int k = 0; k < kLoadsP; ++k) fill_p(s, k);
-#pragma unroll
-        for (int k = 0; k < kLoadsQ; ++k) fill_q(s, k);
-    }
     f32x4 acc[FM][FN];
-    if constexpr (kSym) {
+    if constexpr (KIND == kGramJoin) {
+        // the parts in order
+        const f32x4 *part = reinterpret_cast<const f32x4 *>(at(ws, M.sums)) +
+                            static_cast<int64_t>(tl.part) * (BM * BN / 4) + threadIdx.x;
 #pragma unroll
         for (int x = 0; x < FM; ++x)
 #pragma unroll
-            for (int y = 0; y < FN; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    } else {
-        // the sums start from a X, so that its loads overlap the first stages'
-        const float ca = ldexpf(coef.a, kLogA);
+            for (int y = 0; y < FN; ++y) acc[x][y] = part[(x * FN + y) * 64 * WAVES];
+        for (int k = 1; k < split; ++k) {
+            part += BM * BN / 4;
 #pragma unroll
-        for (int x = 0; x < FM; x += 2)
+            for (int x = 0; x < FM; ++x)
 #pragma unroll
-            for (int y = 0; y < FN; ++y) {
-                const int i = i0 + wm * WTM + x * 16 + 8 * g;
-                const int j = j0 + wn * WTN + (y >> 1) * 32 + perm_row(lane & 15, y & 1);
-                f16x8 hi{}, lo{};
-                if (i < M.mp && j < M.np) {
-                    const int64_t o = panel_at(M.np, j, i) >> 3;
-                    hi = reinterpret_cast<const f16x8 *>(T)[o];
-                    lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o];
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    acc[x + (e >> 2)][y][e & 3] =
-                        ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e]));
-            }
-    }
-    border<0>();
-#pragma unroll
-    for (int k = 0; k < FM / 2; ++k) read_p(0, 0, k);
-#pragma unroll
-    for (int y = 0; y < FN; ++y) read_q(0, 0, y);
-    // The products of one part; after each, its share of the next part's reads
-    // and of the loads: a wave issues in order, and a burst of loads that the
-    // memory path cannot take at once would hold up its products.
-    auto multiply = [&](int h, int set, auto reads, auto loads, auto &&rd, auto &&ld) {
-        constexpr int n = FM / 2 * FN, R = reads.value, L = loads.value;
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            const int x = k / FN, y = k % FN;
-            f32x4 &c = acc[h * (FM / 2) + x][y];
-            c = __builtin_amdgcn_mfma_f32_16x16x32_f16(p[h][x], q[set][y], c, 0, 0, 0);
-            // the reads go first, so that the last have some products to land
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (r * (n - 2) / (R > 0 ? R : 1) == k) rd(r);
-#pragma unroll
-            for (int l = 0; l < L; ++l)
-                if ((2 * l + 1) * n / (2 * (L > 0 ? L : 1)) == k) ld(l);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int y = 0; y < FN; ++y) acc[x][y] += part[(x * FN + y) * 64 * WAVES];
         }
-    };
-    // One stage; set: its rows j.  No branch lies between a read of operands
-    // and their use, so that the compiler waits for the older reads alone.
-    auto stage = [&](auto wait, auto more, int set, int s) {
-        constexpr int LP = more.value > 1 ? kLoadsP : 0, LQ = more.value > 1 ? kLoadsQ : 0;
-        multiply(0, set, Int<FM / 2>{}, Int<LP>{}, [&](int k) { read_p(s, 1, k); },
-                 [&](int k) { fill_p(s + NST - 1, k); });
-        if constexpr (more.value > 0) border<wait.value>();
-        multiply(1, set, Int<(more.value > 0 ? FM / 2 + FN : 0)>{}, Int<LQ>{},
-                 [&](int k) {
-                     // the first product's operands first
-                     if (k == 0) read_p(s + 1, 0, 0);
-                     else if (k <= FN) read_q(s + 1, set ^ 1, k - 1);
-                     else read_p(s + 1, 0, k - FN);
-                 },
-                 [&](int k) { fill_q(s + NST - 1, k); });
-    };
-    constexpr int kLoads = kLoadsP + kLoadsQ;
-    // loads younger than the next stage's: NST - 3 stages and this one's first
-    constexpr Int<kLoads *(NST - 3) + kLoadsP> kWait{};
-    int s = 0;
-    for (; s + NST < steps; s += 2) {
+    } else {
+        // load k of this wave's kLoadsP of stage s's rows i, or of its kLoadsQ of the rows j
+        auto fill_p = [&](int s, int k) {
+            lds_char *b = lds + (s & (NST - 1)) * kStage;
+            const int u = k * WAVES + wave;
+            if constexpr (kXXT) {
+                // rows of X^T are the sum, columns i and j
+                const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
+                const int at = i0 / 32, n = M.mp / 32 - at < BM / 32 ? M.mp / 32 - at : BM / 32;
+                fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
+            } else {
+                const char *A = at(ws, KIND == kPoly ? M.a : M.b);
+                const int n = M.mp - i0 < BM ? M.mp - i0 : BM;
+                fill_rows(b, A + (static_cast<int64_t>(s) * M.mp + i0) * 64, n * 64u, u, lane);
+            }
+        };
+        auto fill_q = [&](int s, int k) {
+            lds_char *b = lds + (s & (NST - 1)) * kStage + BM * 64;
+            const int u = k * WAVES + wave;
+            if constexpr (kXXT) {
+                const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
+                const int at = j0 / 32, n = M.mp / 32 - at < BN / 32 ? M.mp / 32 - at : BN / 32;
+                fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
+            } else {
+                const char *A = KIND == kPoly ? at(ws, M.a) : T;
+                const int rq = KIND == kPoly ? M.mp : M.np, n = rq - j0 < BN ? rq - j0 : BN;
+                fill_rows(b, A + (static_cast<int64_t>(s) * rq + j0) * 64, n * 64u, u, lane);
+            }
+        };
+        f16x8 p[2][FM / 2], q[2][FN];
+        // operand k of part h of stage s's rows i; of its rows j, into set `set`
+        auto read_p = [&](int s, int h, int k) {
+            lds_char *t = lds + (s & (NST - 1)) * kStage;
+            const int x = h * (FM / 2) + k, base = wm * WTM + (x >> 1) * 32;
+            if constexpr (kXXT) p[h][k] = read_cols(t, base + (x & 1) * 16, lane);
+            else p[h][k] = read_rows(t, base + perm_row(lane & 15, x & 1), lane);
+        };
+        auto read_q = [&](int s, int set, int y) {
+            lds_char *t = lds + (s & (NST - 1)) * kStage + BM * 64;
+            const int base = wn * WTN + (y >> 1) * 32;
+            if constexpr (kXXT) q[set][y] = read_cols(t, base + (y & 1) * 16, lane);
+            else q[set][y] = read_rows(t, base + perm_row(lane & 15, y & 1), lane);
+        };
+
+        // stages of the sum, or of this part's stretch of it: a multiple of four
+        int steps = (kXXT ? M.np : M.mp) / kBK;
+        if constexpr (KIND == kGramPart) {
+            const int units = steps / NST, k = tl.part % split;
+            const int from = units * k / split, to = units * (k + 1) / split;
+            T += static_cast<int64_t>(from) * NST * 2048;
+            steps = (to - from) * NST;
+        }
+#pragma unroll
+        for (int s = 0; s < NST - 1; ++s) {
+#pragma unroll
+            for (int k = 0; k < kLoadsP; ++k) fill_p(s, k);
+#pragma unroll
+            for (int k = 0; k < kLoadsQ; ++k) fill_q(s, k);
+        }
+        if constexpr (kSym) {
+#pragma unroll
+            for (int x = 0; x < FM; ++x)
+#pragma unroll
+                for (int y = 0; y < FN; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        } else {
+            // the sums start from a X, so that its loads overlap the first stages'
+            const float ca = ldexpf(coef.a, kLogA);
+#pragma unroll
+            for (int x = 0; x < FM; x += 2)
+#pragma unroll
+                for (int y = 0; y < FN; ++y) {
+                    const int i = i0 + wm * WTM + x * 16 + 8 * g;
+                    const int j = j0 + wn * WTN + (y >> 1) * 32 + perm_row(lane & 15, y & 1);
+                    f16x8 hi{}, lo{};
+                    if (i < M.mp && j < M.np) {
+                        const int64_t o = panel_at(M.np, j, i) >> 3;
+                        hi = reinterpret_cast<const f16x8 *>(T)[o];
+                        lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        acc[x + (e >> 2)][y][e & 3] =
+                            ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e]));
+                }
+        }
+        border<0>();
+#pragma unroll
+        for (int k = 0; k < FM / 2; ++k) read_p(0, 0, k);
+#pragma unroll
+        for (int y = 0; y < FN; ++y) read_q(0, 0, y);
+        // The products of one part; after each, its share of the next part's reads
+        // and of the loads: a wave issues in order, and a burst of loads that the
+        // memory path cannot take at once would hold up its products.
+        auto multiply = [&](int h, int set, auto reads, auto loads, auto &&rd, auto &&ld) {
+            constexpr int n = FM / 2 * FN, R = reads.value, L = loads.value;
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                const int x = k / FN, y = k % FN;
+                f32x4 &c = acc[h * (FM / 2) + x][y];
+                c = __builtin_amdgcn_mfma_f32_16x16x32_f16(p[h][x], q[set][y], c, 0, 0, 0);
+                // the reads go first, so that the last have some products to land
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (r * (n - 2) / (R > 0 ? R : 1) == k) rd(r);
+#pragma unroll
+                for (int l = 0; l < L; ++l)
+                    if ((2 * l + 1) * n / (2 * (L > 0 ? L : 1)) == k) ld(l);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        // One stage; set: its rows j.  No branch lies between a read of operands
+        // and their use, so that the compiler waits for the older reads alone.
+        auto stage = [&](auto wait, auto more, int set, int s) {
+            constexpr int LP = more.value > 1 ? kLoadsP : 0, LQ = more.value > 1 ? kLoadsQ : 0;
+            multiply(0, set, Int<FM / 2>{}, Int<LP>{}, [&](int k) { read_p(s, 1, k); },
+                     [&](int k) { fill_p(s + NST - 1, k); });
+            if constexpr (more.value > 0) border<wait.value>();
+            multiply(1, set, Int<(more.value > 0 ? FM / 2 + FN : 0)>{}, Int<LQ>{},
+                     [&](int k) {
+                         // the first product's operands first
+                         if (k == 0) read_p(s + 1, 0, 0);
+                         else if (k <= FN) read_q(s + 1, set ^ 1, k - 1);
+                         else read_p(s + 1, 0, k - FN);
+                     },
+                     [&](int k) { fill_q(s + NST - 1, k); });
+        };
+        constexpr int kLoads = kLoadsP + kLoadsQ;
+        // loads younger than the next stage's: NST - 3 stages and this one's first
+        constexpr Int<kLoads *(NST - 3) + kLoadsP> kWait{};
+        int s = 0;
+        for (; s + NST < steps; s += 2) {
+            stage(kWait, Int<2>{}, 0, s);
+            stage(kWait, Int<2>{}, 1, s + 1);
+        }
+        // the last four: one more to load, two with a border, the last
         stage(kWait, Int<2>{}, 0, s);
-        stage(kWait, Int<2>{}, 1, s + 1);
+        stage(Int<kLoads>{}, Int<1>{}, 1, s + 1);
+        stage(Int<0>{}, Int<1>{}, 0, s + 2);
+        stage(Int<0>{}, Int<0>{}, 1, s + 3);
     }
-    // the last four: one more to load, two with a border, the last
-    stage(kWait, Int<2>{}, 0, s);
-    stage(Int<kLoads>{}, Int<1>{}, 1, s + 1);
-    stage(Int<0>{}, Int<1>{}, 0, s + 2);
-    stage(Int<0>{}, Int<0>{}, 1, s + 3);
+    if constexpr (KIND == kGramPart) {
+        f32x4 *part = reinterpret_cast<f32x4 *>(at(ws, M.sums)) +
+                      static_cast<int64_t>(tl.part) * (BM * BN / 4) + threadIdx.x;
+#pragma unroll
+        for (int x = 0; x < FM; ++x)
+#pragma unroll
+            for (int y = 0; y < FN; ++y) part[(x * FN + y) * 64 * WAVES] = acc[x][y];
+        return;
+    }
 
     // Epilogue, block by block of 32 x 32.  For b = 0, 1 this lane has column
     // colb(b) and, in v[b], the rows 8 g .. + 8 (X X^T: 4 g .. + 4 of either
@@ -443,7 +486,7 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     lds_char *st = lds + wave * 2048;
     if constexpr (kSym || KIND == kLast) border<0>();
     const float phi = first ? sc.phi0 : sc.phi, rho = first ? sc.rho : 1.0f;
-    const float alpha = KIND == kGram   ? ldexpf(phi * phi, kLogA)
+    const float alpha = kXXT   ? ldexpf(phi * phi, kLogA)
                         : KIND == kPoly ? ldexpf(coef.c, -kLogA)
                                         : ldexpf(rho, -kLogA);
     const bool vec = KIND == kLast && (lo32(M.out) & 15u) == 0 && (M.cols & 7) == 0;
@@ -457,17 +500,17 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
             int col[2], row[2];         // of the block; rows: of the first and second four
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                col[b] = KIND == kGram ? 16 * b + (lane & 15) : perm_row(lane & 15, b);
-                row[b] = KIND == kGram ? 16 * b + 4 * g : 8 * g + 4 * b;
+                col[b] = kXXT ? 16 * b + (lane & 15) : perm_row(lane & 15, b);
+                row[b] = kXXT ? 16 * b + 4 * g : 8 * g + 4 * b;
             }
-            char *C = at(ws, KIND == kGram ? M.a : M.b);
+            char *C = at(ws, kXXT ? M.a : M.b);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float t[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] = alpha * acc[x + (e >> 2)][y + b][e & 3];
                 const int64_t o = panel_at(kSym ? M.mp : M.np, jb + col[b], ib + row[0]);
-                if constexpr (KIND == kGram) {
+                if constexpr (kXXT) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[b].f[e] = static_cast<_Float16>(t[e]);
                     s16x4 *c = reinterpret_cast<s16x4 *>(C) + (o >> 2);
@@ -535,20 +578,338 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
         }
 }
 
+// ---------------------------------------------------------------------------
+// matrices with few rows
+// ---------------------------------------------------------------------------
+
+// Up to kSmallMax rows a block holds all m rows of a slab of NB columns of X in
+// LDS and goes through the iteration by itself: with one slab the whole
+// orthogonalisation is one launch, with more each iteration is one (its
+// block sums the slabs' X X^T, makes B, multiplies its slab and leaves its part
+// of the next X X^T), and a second one where there are too many parts to sum in
+// every block.
+//
+// Every operand is taken as a high and a low fp16 part (three products of the
+// four), to 2^-22: with few rows the roundings of A, of B and of X in the
+// products are few and do not average out (fp16 alone was up to 5e-3 off with
+// one to four rows), and the products are too small to bound the time.
+
+constexpr int kSmallBlock = 512;
+
+template <int MP>
+struct Small {
+    static constexpr int NB = small_slab(MP);           // columns of a slab
+    static constexpr int nb = MP / 16;                  // 16 x 16 blocks a side
+    static constexpr int kWaves = kSmallBlock / 64;
+    // blocks of a row that one wave has: its row of blocks and bj0 .. + kBJ
+    static constexpr int kBJ = MP == 128 ? 8 : MP == 64 ? 2 : 1;
+    static constexpr int kHalves = MP == 32 ? 2 : 1;    // stretches of the sum over columns
+    static constexpr int kT = NB * MP * 2, kA = MP * MP * 2;     // bytes of one part in LDS
+    static constexpr int kScratch = MP == 32 ? 4096 : 0;
+    static constexpr int kLds = 2 * kT + 2 * kA + kScratch;
+};
+
+// Element (row, col .. + 4 or 8) in LDS panels of 32 columns with `rows` rows;
+// the halves of a row change places in every other eight rows, for the reads
+// along rows and for the transposing ones alike.
+__device__ __forceinline__ int small_at(int rows, int row, int col) {
+    return (col >> 5) * rows * 64 + row * 64 + ((((col >> 3) & 3) ^ (((row >> 3) & 1) << 1)) * 16) +
+           (col & 7) * 2;
+}
+
+// Operand: 16 rows from row0, 32 columns from col0.
+__device__ __forceinline__ f16x8 small_rows(const lds_char *t, int rows, int row0, int col0,
+                                            int lane) {
+    return *(const lds_f16x8 *)(t + small_at(rows, row0 + (lane & 15), col0 + 8 * (lane >> 4)));
+}
+
+// Operand: 16 columns from col0, 32 rows (the sum) from row0.
+__device__ __forceinline__ f16x8 small_cols(lds_char *t, int rows, int row0, int col0, int lane) {
+    const int k = row0 + (lane >> 4) * 8 + ((lane >> 2) & 3);
+    lds_char *at = t + small_at(rows, k, col0 + (lane & 3) * 4);
+    union {
+        s16x4 s[2];
+        f16x8 v;
+    } u;
+    u.s[0] = read_tr(at);
+    u.s[1] = read_tr(at + 4 * 64);
+    return u.v;
+}
+
+// c += (ph + pl) (qh + ql) without pl ql
+__device__ __forceinline__ f32x4 fine_product(f16x8 ph, f16x8 pl, f16x8 qh, f16x8 ql, f32x4 c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, ql, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, qh, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, qh, c, 0, 0, 0);
+}
+
+// Four neighbouring values as high and low parts at byte offset o of hi and lo.
+__device__ __forceinline__ void put_split(lds_char *hi, lds_char *lo, int o, const float (&x)[4]) {
+    f16x4 h, l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float f = settled(x[e]);
+        h[e] = static_cast<_Float16>(f);
+        l[e] = static_cast<_Float16>(f - static_cast<float>(h[e]));
+    }
+    *(lds_f16x4 *)(hi + o) = h;
+    *(lds_f16x4 *)(lo + o) = l;
+}
+
+template <int MP, bool kF32>
+__global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
+    const OrthoTile *__restrict__ tiles, const OrthoMat *__restrict__ mats, void *ws, int32_t mode,
+    int32_t step, int32_t n_steps, const OrthoCoef *__restrict__ coefs, double eps, int32_t growth) {
+    using S = Small<MP>;
+    constexpr int NB = S::NB, nb = S::nb, kBJ = S::kBJ;
+    __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
+    __shared__ double sums[S::kWaves];
+    lds_char *th = (lds_char *)smem, *tlo = th + S::kT, *ah = tlo + S::kT, *al = ah + S::kA;
+    f32x4 *scratch = reinterpret_cast<f32x4 *>(smem + 2 * S::kT + 2 * S::kA);
+
+    const OrthoTile tl = tiles[blockIdx.x];
+    const OrthoMat M = mats[tl.mat];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
+    const int slab = tl.ti, j0 = slab * NB;
+    const int rows = M.n - j0 < NB ? M.n - j0 : NB, rows32 = (rows + 31) & ~31;
+    // this wave's blocks of A and B, and of a split sum its stretch
+    const int bi = MP == 128 ? wave : MP == 64 ? wave >> 1 : (wave >> 1) & 1;
+    const int bj0 = MP == 128 ? 0 : MP == 64 ? (wave & 1) * 2 : wave & 1;
+    const int half = MP == 32 ? wave >> 2 : 0;
+    char *image = at(ws, M.t[0]) + static_cast<int64_t>(slab) * 2 * S::kT;
+
+    OrthoScal sc;
+    if (mode == kSmallAll || mode == kSmallStart) {
+        // eight neighbouring rows i of one column j a thread and turn
+        constexpr int kTurns = NB * MP / 8 / kSmallBlock;
+        float x[kTurns][8];
+        double s = 0.0;
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int u = t * kSmallBlock + tid;
+            const int j = M.wide ? u % NB : u / (MP / 8), i = (M.wide ? u / NB : u % (MP / 8)) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool in = j < rows && i + e < M.m;
+                const int64_t o = M.wide ? static_cast<int64_t>(i + e) * M.cols + j0 + j
+                                         : static_cast<int64_t>(j0 + j) * M.cols + i + e;
+                x[t][e] = in ? load_in<kF32>(M.in, o) : 0.0f;
+                s += static_cast<double>(x[t][e]) * x[t][e];
+            }
+        }
+        if (mode == kSmallStart) {
+            s = 0.0;
+            const double *parts = reinterpret_cast<const double *>(at(ws, M.parts));
+            for (int i = tid; i < M.n_parts; i += kSmallBlock) s += parts[i];
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+        if (lane == 0) sums[wave] = s;
+        __syncthreads();
+        s = 0.0;
+#pragma unroll
+        for (int w = 0; w < S::kWaves; ++w) s += sums[w];
+        int k;
+        sc = scalars(sqrt(s), eps, growth, &k);
+        const bool fine = sc.phi0 == sc.phi0 || isfinite(s);
+        if (mode == kSmallStart && slab == 0 && tid == 0)
+            *reinterpret_cast<OrthoScal *>(at(ws, M.scal)) = sc;
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int u = t * kSmallBlock + tid;
+            const int j = M.wide ? u % NB : u / (MP / 8), i = (M.wide ? u / NB : u % (MP / 8)) * 8;
+            if (j < rows32) {
+                Half8 h, l;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float f = fine ? settled(ldexpf(x[t][e], k)) : 0.0f;
+                    h.f[e] = static_cast<_Float16>(f);
+                    l.f[e] = static_cast<_Float16>(f - static_cast<float>(h.f[e]));
+                }
+                const int o = small_at(NB, j, i);
+                *(lds_f16x8 *)(th + o) = h.f;
+                *(lds_f16x8 *)(tlo + o) = l.f;
+            }
+        }
+    } else {
+        sc = *reinterpret_cast<const OrthoScal *>(at(ws, M.scal));
+        // the slab as it was left: whole panels' rows
+        for (int q = 0; q < MP / 32; ++q)
+            for (int o = tid * 16; o < rows32 * 64; o += kSmallBlock * 16) {
+                const int at16 = q * NB * 64 + o;
+                *reinterpret_cast<u32x4 *>(smem + at16) =
+                    *reinterpret_cast<const u32x4 *>(image + at16);
+                *reinterpret_cast<u32x4 *>(smem + S::kT + at16) =
+                    *reinterpret_cast<const u32x4 *>(image + S::kT + at16);
+            }
+    }
+    __syncthreads();
+
+    f32x4 a[kBJ];
+    // this wave's blocks of X X^T over the slab
+    auto gram = [&]() {
+#pragma unroll
+        for (int y = 0; y < kBJ; ++y) a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = half * 32; r < rows32; r += 32 * S::kHalves) {
+            const f16x8 ph = small_cols(th, NB, r, bi * 16, lane);
+            const f16x8 pl = small_cols(tlo, NB, r, bi * 16, lane);
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y)
+                a[y] = fine_product(ph, pl, small_cols(th, NB, r, (bj0 + y) * 16, lane),
+                                    small_cols(tlo, NB, r, (bj0 + y) * 16, lane), a[y]);
+        }
+        if constexpr (S::kHalves > 1) {
+            if (half == 1) scratch[(wave & 3) * 64 + lane] = a[0];
+            __syncthreads();
+            a[0] += scratch[(wave & 3) * 64 + lane];     // the first stretch's waves use it
+        }
+    };
+    // parts of A: one 16 x 16 block after the other, a lane's four values together
+    auto part = [&](int k, int y) {
+        return reinterpret_cast<f32x4 *>(at(ws, (k & 1) ? M.b : M.a)) + (bi * nb + bj0 + y) * 64 +
+               lane;
+    };
+    const bool mine = half == 0;
+    if (mode == kSmallAll || mode == kSmallStart) gram();
+    if (mode == kSmallStart && mine) {
+#pragma unroll
+        for (int y = 0; y < kBJ; ++y) part(0, y)[static_cast<int64_t>(slab) * MP * MP / 4] = a[y];
+    }
+    const int from = mode == kSmallAll ? 0 : step;
+    const int to = mode == kSmallAll ? n_steps : mode == kSmallStart ? 0 : step + 1;
+    for (int k = from; k < to; ++k) {
+        const OrthoCoef c = coefs[k];
+        if (mode != kSmallAll && mine) {
+            // the parts' sum, in order
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y) {
+                const f32x4 *p = part(k, y);
+                a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+                for (int t = 0; t < M.n_sums; ++t) a[y] += p[static_cast<int64_t>(t) * MP * MP / 4];
+            }
+        }
+        const float phi = k == 0 ? sc.phi0 : sc.phi, rho = k == 0 ? sc.rho : 1.0f;
+        // A, scaled, as operands: rows bj 16 + (lane & 15) (A is symmetric), columns bi 16 + 4 g ..
+        const float alpha = ldexpf(phi * phi, kLogA);
+        float av[kBJ][4];
+        if (mine) {
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) av[y][e] = alpha * a[y][e];
+                put_split(ah, al, small_at(MP, (bj0 + y) * 16 + (lane & 15), bi * 16 + 4 * g), av[y]);
+            }
+        }
+        __syncthreads();
+        f32x4 b[kBJ];
+        if (mine) {
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y) b[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int q = 0; q < MP; q += 32) {
+                const f16x8 ph = small_rows(ah, MP, bi * 16, q, lane);
+                const f16x8 pl = small_rows(al, MP, bi * 16, q, lane);
+#pragma unroll
+                for (int y = 0; y < kBJ; ++y)
+                    b[y] = fine_product(ph, pl, small_rows(ah, MP, (bj0 + y) * 16, q, lane),
+                                        small_rows(al, MP, (bj0 + y) * 16, q, lane), b[y]);
+            }
+        }
+        __syncthreads();
+        if (mine) {
+            const float cc = ldexpf(c.c, -kLogA);
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = c.b * av[y][e] + cc * b[y][e];
+                put_split(ah, al, small_at(MP, (bj0 + y) * 16 + (lane & 15), bi * 16 + 4 * g), v);
+            }
+        }
+        __syncthreads();
+        // X = a X + B X: a wave takes 16 columns j at a time, which no other wave reads or writes
+        const bool last = k + 1 == n_steps;
+        const float ca = ldexpf(c.a, kLogA), cb = ldexpf(rho, -kLogA);
+        for (int r = wave * 16; r < rows; r += S::kWaves * 16) {
+            f16x8 qh[MP / 32], ql[MP / 32];
+#pragma unroll
+            for (int q = 0; q < MP / 32; ++q) {
+                qh[q] = small_rows(th, NB, r, q * 32, lane);
+                ql[q] = small_rows(tlo, NB, r, q * 32, lane);
+            }
+            const int j = r + (lane & 15);
+#pragma unroll
+            for (int x = 0; x < nb; ++x) {
+                const int o = small_at(NB, j, x * 16 + 4 * g);
+                const f16x4 xh = *(lds_f16x4 *)(th + o), xl = *(lds_f16x4 *)(tlo + o);
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = ca * (static_cast<float>(xh[e]) + static_cast<float>(xl[e]));
+#pragma unroll
+                for (int q = 0; q < MP / 32; ++q)
+                    v = fine_product(small_rows(ah, MP, x * 16, q * 32, lane),
+                                     small_rows(al, MP, x * 16, q * 32, lane), qh[q], ql[q], v);
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = cb * v[e];
+                if (!last) {
+                    put_split(th, tlo, o, w);
+                } else if (j < rows) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = x * 16 + 4 * g + e;
+                        const int64_t at = M.wide ? static_cast<int64_t>(i) * M.cols + j0 + j
+                                                  : static_cast<int64_t>(j0 + j) * M.cols + i;
+                        if (i < M.m) M.out[at] = static_cast<uint16_t>(bf16_rne(w[e] * sc.phi));
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (last) break;
+        gram();
+        if (mode == kSmallStep && mine) {
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y)
+                part(k + 1, y)[static_cast<int64_t>(slab) * MP * MP / 4] = a[y];
+        }
+    }
+    if (mode == kSmallStart || mode == kSmallStep) {
+        __syncthreads();
+        for (int q = 0; q < MP / 32; ++q)
+            for (int o = tid * 16; o < rows32 * 64; o += kSmallBlock * 16) {
+                const int at16 = q * NB * 64 + o;
+                *reinterpret_cast<u32x4 *>(image + at16) =
+                    *reinterpret_cast<const u32x4 *>(smem + at16);
+                *reinterpret_cast<u32x4 *>(image + S::kT + at16) =
+                    *reinterpret_cast<const u32x4 *>(smem + S::kT + at16);
+            }
+    }
+}
+
+// Sums the parts of A of the matrices that have too many for every block to sum
+// them: the sum replaces the first part.
+__global__ __launch_bounds__(kBlock) void ortho_sums_kernel(const OrthoTile *__restrict__ tiles,
+                                                            const OrthoMat *__restrict__ mats,
+                                                            void *ws, int32_t step) {
+    const OrthoTile tl = tiles[blockIdx.x];
+    const OrthoMat M = mats[tl.mat];
+    const int64_t size = static_cast<int64_t>(M.mp) * M.mp / 4;
+    f32x4 *p = reinterpret_cast<f32x4 *>(at(ws, (step & 1) ? M.b : M.a)) + tl.ti * kBlock +
+               threadIdx.x;
+    f32x4 v = p[0];
+#pragma unroll 8
+    for (int t = 1; t < tl.tj; ++t) v += p[t * size];
+    p[0] = v;
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
-
-#ifndef FSDP_ORTHO_BM
-#define FSDP_ORTHO_BM 128
-#define FSDP_ORTHO_BN 128
-#define FSDP_ORTHO_WM 2
-#define FSDP_ORTHO_WN 2
-#endif
-#define TILE_ARGS FSDP_ORTHO_BM, FSDP_ORTHO_BN, FSDP_ORTHO_WM, FSDP_ORTHO_WN
-#define TILE_THR (64 * FSDP_ORTHO_WM * FSDP_ORTHO_WN)
 
 hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              bool f32, hipStream_t st) {
@@ -570,32 +931,92 @@ hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *
     return hipGetLastError();
 }
 
-hipError_t launch_ortho_gram(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
-                             int32_t src, bool first, hipStream_t st) {
-    if (n == 0) return hipSuccess;
-    ortho_product_kernel<kGram, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
-        tiles, mats, ws, src, first, OrthoCoef{});
-    return hipGetLastError();
-}
+namespace {
 
-hipError_t launch_ortho_poly(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
-                             OrthoCoef c, hipStream_t st) {
+// 256 x 256 by eight waves, one block a CU; 128 x 128 and 64 x 64 by four, two
+// and five blocks a CU
+template <int KIND>
+hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
+                          void *ws, int32_t src, bool first, int32_t split, OrthoCoef c,
+                          hipStream_t st) {
     if (n == 0) return hipSuccess;
-    ortho_product_kernel<kPoly, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
-        tiles, mats, ws, 0, 0, c);
-    return hipGetLastError();
-}
-
-hipError_t launch_ortho_apply(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
-                              int32_t src, bool first, bool last, OrthoCoef c, hipStream_t st) {
-    if (n == 0) return hipSuccess;
-    if (last)
-        ortho_product_kernel<kLast, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
-            tiles, mats, ws, src, first, c);
+    const unsigned grid = static_cast<unsigned>(n);
+    if (tile == 256)
+        ortho_product_kernel<KIND, 256, 256, 2, 4>
+            <<<grid, 512, 0, st>>>(tiles, mats, ws, src, first, split, c);
+    else if (tile == 128)
+        ortho_product_kernel<KIND, 128, 128, 2, 2>
+            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, first, split, c);
     else
-        ortho_product_kernel<kApply, TILE_ARGS><<<static_cast<unsigned>(n), TILE_THR, 0, st>>>(
-            tiles, mats, ws, src, first, c);
+        ortho_product_kernel<KIND, 64, 64, 2, 2>
+            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, first, split, c);
     return hipGetLastError();
+}
+
+}  // namespace
+
+namespace {
+
+template <bool kF32>
+void small(int32_t mp, unsigned n, const OrthoTile *tiles, const OrthoMat *mats, void *ws,
+           int32_t mode, int32_t step, int32_t n_steps, const OrthoCoef *coefs, double eps,
+           int32_t growth, hipStream_t st) {
+    if (mp == 32)
+        ortho_small_kernel<32, kF32><<<n, kSmallBlock, 0, st>>>(tiles, mats, ws, mode, step,
+                                                                n_steps, coefs, eps, growth);
+    else if (mp == 64)
+        ortho_small_kernel<64, kF32><<<n, kSmallBlock, 0, st>>>(tiles, mats, ws, mode, step,
+                                                                n_steps, coefs, eps, growth);
+    else
+        ortho_small_kernel<128, kF32><<<n, kSmallBlock, 0, st>>>(tiles, mats, ws, mode, step,
+                                                                 n_steps, coefs, eps, growth);
+}
+
+}  // namespace
+
+hipError_t launch_ortho_small(int32_t mp, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
+                              void *ws, bool f32, int32_t mode, int32_t step, int32_t n_steps,
+                              const OrthoCoef *coefs, double eps, int32_t growth, hipStream_t st) {
+    if (n == 0) return hipSuccess;
+    if (f32)
+        small<true>(mp, static_cast<unsigned>(n), tiles, mats, ws, mode, step, n_steps, coefs, eps,
+                    growth, st);
+    else
+        small<false>(mp, static_cast<unsigned>(n), tiles, mats, ws, mode, step, n_steps, coefs, eps,
+                     growth, st);
+    return hipGetLastError();
+}
+
+hipError_t launch_ortho_sums(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
+                             int32_t step, hipStream_t st) {
+    if (n == 0) return hipSuccess;
+    ortho_sums_kernel<<<static_cast<unsigned>(n), kBlock, 0, st>>>(tiles, mats, ws, step);
+    return hipGetLastError();
+}
+
+hipError_t launch_ortho_gram(int32_t tile, const OrthoTile *tiles, int64_t n,
+                             const OrthoTile *join, int64_t n_join, int32_t split,
+                             const OrthoMat *mats, void *ws, int32_t src, bool first,
+                             hipStream_t st) {
+    if (split == 1)
+        return launch_product<kGram>(tile, tiles, n, mats, ws, src, first, 1, OrthoCoef{}, st);
+    const hipError_t e =
+        launch_product<kGramPart>(tile, tiles, n, mats, ws, src, first, split, OrthoCoef{}, st);
+    if (e != hipSuccess) return e;
+    return launch_product<kGramJoin>(tile, join, n_join, mats, ws, src, first, split, OrthoCoef{},
+                                     st);
+}
+
+hipError_t launch_ortho_poly(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
+                             void *ws, OrthoCoef c, hipStream_t st) {
+    return launch_product<kPoly>(tile, tiles, n, mats, ws, 0, false, 1, c, st);
+}
+
+hipError_t launch_ortho_apply(int32_t tile, const OrthoTile *tiles, int64_t n,
+                              const OrthoMat *mats, void *ws, int32_t src, bool first, bool last,
+                              OrthoCoef c, hipStream_t st) {
+    if (last) return launch_product<kLast>(tile, tiles, n, mats, ws, src, first, 1, c, st);
+    return launch_product<kApply>(tile, tiles, n, mats, ws, src, first, 1, c, st);
 }
 
 }  // namespace fsdp

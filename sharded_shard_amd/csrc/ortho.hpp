@@ -3,7 +3,9 @@
 // Per matrix the workspace holds, for m = the smaller and n = the larger side
 // padded to mp and np (multiples of kOrthoPad, padding zero), X^T as fp16 high
 // and low parts ([np][mp]; the high part twice, read and written by turns) and
-// the m x m products A and B in fp16.
+// the m x m products A and B in fp16.  Where m is at most kSmallMax, and X has
+// more columns than a block holds, it has the slabs' X^T, high and low, and two
+// sets of the slabs' parts of A in fp32.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -26,9 +28,11 @@ struct OrthoMat {
     int64_t a, b;        // A, B
     int64_t parts;       // partial sums of squares (double), n_parts of them
     int64_t scal;        // float[4], see OrthoScal
+    int64_t sums;        // fp32 parts of split sums, the plan's
     int32_t rows, cols;
     int32_t m, n, mp, np;
     int32_t n_parts, wide;  // wide: rows <= cols, X = U; else X = U^T
+    int32_t n_sums, rsv;    // few rows: parts of A that every block sums
 };
 
 // What one init pass leaves for the products: the true X is phi0 times the
@@ -40,12 +44,20 @@ struct OrthoScal {
 struct OrthoTile {
     int32_t mat;
     int32_t ti, tj;
-    int32_t rsv;
+    int32_t part;        // of a split sum: this part's place among all
 };
 
 struct OrthoCoef {
     float a, b, c;
 };
+
+// Matrices of at most kSmallMax rows (the smaller side): padded to 32, 64 or
+// 128 rows, worked on in slabs of so many columns.
+constexpr int32_t kSmallMax = 128;
+constexpr int32_t small_rows_of(int32_t m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+constexpr int32_t small_slab(int32_t mp) { return mp == 128 ? 128 : mp == 64 ? 512 : 1024; }
+// What a launch does: all steps (one slab), the start, one step, the last step.
+enum { kSmallAll = 0, kSmallStart = 1, kSmallStep = 2, kSmallLast = 3 };
 
 // Partial sums of squares; tiles: (matrix, part).
 hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
@@ -54,15 +66,29 @@ hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *
 // log2 of the most that the iterations can magnify a singular value.
 hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              bool f32, double eps, int32_t growth, hipStream_t st);
-// A = X X^T, tiles (ti >= tj) of the lower triangle; src: which high part is read.
-hipError_t launch_ortho_gram(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
-                             int32_t src, bool first, hipStream_t st);
+// Matrices of few rows, tiles: (matrix, slab), all of mp padded rows.
+hipError_t launch_ortho_small(int32_t mp, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
+                              void *ws, bool f32, int32_t mode, int32_t step, int32_t n_steps,
+                              const OrthoCoef *coefs, double eps, int32_t growth, hipStream_t st);
+// Sums their parts of step's A where every block would have too many to sum;
+// tiles: (matrix, 256 x 4 elements of it, number of parts).
+hipError_t launch_ortho_sums(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
+                             int32_t step, hipStream_t st);
+// The products; tile: 256, 128 or 64 rows and columns of a tile.
+// A = X X^T, tiles (ti >= tj) of the lower triangle; src: which high part is
+// read.  With split > 1 every tile comes split times (its part its place among
+// all parts), and join has each once, with its first part.
+hipError_t launch_ortho_gram(int32_t tile, const OrthoTile *tiles, int64_t n,
+                             const OrthoTile *join, int64_t n_join, int32_t split,
+                             const OrthoMat *mats, void *ws, int32_t src, bool first,
+                             hipStream_t st);
 // B = b A + c A A, tiles of the lower triangle
-hipError_t launch_ortho_poly(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
-                             OrthoCoef c, hipStream_t st);
+hipError_t launch_ortho_poly(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
+                             void *ws, OrthoCoef c, hipStream_t st);
 // X^T = a X^T + X^T B into the other high part and the low part, or with last
 // into out; tiles (ti of mp, tj of np)
-hipError_t launch_ortho_apply(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
-                              int32_t src, bool first, bool last, OrthoCoef c, hipStream_t st);
+hipError_t launch_ortho_apply(int32_t tile, const OrthoTile *tiles, int64_t n,
+                              const OrthoMat *mats, void *ws, int32_t src, bool first, bool last,
+                              OrthoCoef c, hipStream_t st);
 
 }  // namespace fsdp

@@ -7,7 +7,9 @@ in [0.7, 1.2], a + 3 b s^2 + 5 c s^4, is at most 3.4 in size, and what the
 rounding of A, of B and of X puts into an iteration is at most |b| s^2 + 2 |c|
 s^4, 2 (|b| s^2 + |c| s^4) and |b s^2 + c s^4| half steps, about 10 of 2^-11
 at s = 1 in the worst case and a third of that where they do not all add up:
-2^-8 once more.
+2^-8 once more.  Up to 128 rows every operand has a second fp16 part, 2^-22, of
+which the iterations magnify at most 485 times (3.4445^5): 2^-13, for each of
+four roundings: 2^-11 in place of the second 2^-8.
 """
 import numpy as np
 import pytest
@@ -22,7 +24,7 @@ capi = pytest.importorskip("sharded_shard_amd.capi")
 from sharded_shard_amd.group import NS_COEFFS, Orthogonalizer, ShardedGroup  # noqa: E402
 
 DEV = "cuda"
-TOL = 2 * 2.0 ** -8
+HALF = 2.0 ** -8
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -69,19 +71,21 @@ def run(mats, coeffs=NS_COEFFS, eps=1e-7, outs=None):
     return outs
 
 
-def close(got, u, coeffs=NS_COEFFS, eps=1e-7, tol=TOL):
+def close(got, u, coeffs=NS_COEFFS, eps=1e-7):
+    inner = 2.0 ** -11 if min(u.shape) <= 128 else HALF
     want = M.orthogonalize(f64(u), coeffs, eps)
     got = f64(got)
     assert np.isfinite(got).all()
     err, norm = np.linalg.norm(got - want), np.linalg.norm(want)
-    assert err <= tol * norm, (u.shape, err / norm)
+    assert err <= (HALF + inner) * norm, (u.shape, err / norm)
     rms = norm / np.sqrt(want.size)
-    assert (np.abs(got - want) <= tol * np.maximum(np.abs(want), 10 * rms)).all(), u.shape
+    assert (np.abs(got - want) <= HALF * np.abs(want) + 10 * inner * rms).all(), u.shape
 
 
 SHAPES = [(1, 1), (1, 7), (9, 1), (4, 32), (32, 16), (33, 31), (64, 64), (65, 2047), (127, 128),
           (128, 129), (129, 128), (200, 130), (130, 515), (256, 256), (257, 255), (384, 1000),
-          (1000, 384), (1, 2048), (2048, 5), (640, 640)]
+          (1000, 384), (1, 2048), (2048, 5), (640, 640), (31, 1024), (32, 1025), (2100, 20),
+          (50, 512), (513, 33), (1300, 64), (97, 128), (100, 129), (1000, 128), (128, 500)]
 
 
 @pytest.mark.parametrize("kind", ["noise", "falling", "low"])
@@ -98,7 +102,9 @@ def test_fp32_inputs(shape):
     close(run([u])[0], u)
 
 
-def test_many_matrices_in_one_plan_equal_each_alone_and_repeat():
+def test_many_matrices_in_one_plan_repeat_and_are_as_right_as_each_alone():
+    """The same plan gives the same bits; alone, a matrix's sums may be split
+    otherwise, which moves fp32 sums and what is rounded from them."""
     shapes = [(200, 300), (1, 5), (0, 4), (300, 200), (64, 64), (130, 700), (200, 300)]
     mats = [matrix(s, i, "falling") for i, s in enumerate(shapes)]
     together = run(mats)
@@ -106,7 +112,8 @@ def test_many_matrices_in_one_plan_equal_each_alone_and_repeat():
     for u, x, y in zip(mats, together, again):
         assert torch.equal(x, y)
         if u.numel():
-            assert torch.equal(x, run([u])[0]), u.shape
+            close(x, u)
+            close(run([u])[0], u)
 
 
 @pytest.mark.parametrize("shape", [(8, 20), (150, 260), (260, 150)], ids=lambda s: "%dx%d" % s)
@@ -159,7 +166,7 @@ def test_other_coefficients(coeffs, shape):
 
 def test_long_sum_and_offsets():
     """Few rows of many columns, both ways round."""
-    for shape in ((130, 40000), (40000, 130), (3, 100001)):
+    for shape in ((130, 40000), (40000, 130), (3, 100001), (100, 20000), (20000, 60)):
         u = matrix(shape, 5, "noise")
         close(run([u])[0], u)
 
@@ -211,10 +218,11 @@ def test_two_executions_at_once_with_their_own_workspaces():
 
 
 def test_refusals_on_the_device():
-    u = matrix((8, 16), 0).to(DEV)
-    o = Orthogonalizer([(8, 16), (8, 16)])
-    x = torch.zeros(400, dtype=torch.bfloat16, device=DEV)
-    views = lambda a, b: [x[a:a + 128].view(8, 16), x[b:b + 128].view(8, 16)]
+    u = matrix((130, 2), 0).to(DEV).repeat(1, 80).contiguous()
+    n = u.numel()
+    o = Orthogonalizer([u.shape, u.shape])
+    x = torch.zeros(4 * n, dtype=torch.bfloat16, device=DEV)
+    views = lambda a, b: [x[a:a + n].view(u.shape), x[b:b + n].view(u.shape)]
 
     def refused(status, call):
         with pytest.raises(capi.FsdpError) as ei:
@@ -222,15 +230,15 @@ def test_refusals_on_the_device():
         assert ei.value.status == status, str(ei.value)
 
     refused(capi.FSDP_E_STATE, lambda: o.execute())
-    refused(capi.FSDP_E_INVAL, lambda: o.bind([u, u], views(0, 127)))
-    refused(capi.FSDP_E_INVAL, lambda: o.bind(views(0, 128), views(64, 256)))
+    refused(capi.FSDP_E_INVAL, lambda: o.bind([u, u], views(0, n - 1)))
+    refused(capi.FSDP_E_INVAL, lambda: o.bind(views(0, n), views(64, 3 * n)))
     with pytest.raises(ValueError):
         o.bind([u], [u])
     with pytest.raises(ValueError):
-        o.bind([u, u.float()], views(0, 128))
+        o.bind([u, u.float()], views(0, n))
     with pytest.raises(ValueError):
-        o.bind([u, u.t().contiguous().t()], views(0, 128))
-    o.bind([u, u], views(0, 128))         # the same input twice
+        o.bind([u, u.t().contiguous().t()], views(0, n))
+    o.bind([u, u], views(0, n))         # the same input twice
     need = o.workspace_bytes
     ws = torch.empty(need + 512, dtype=torch.uint8, device=DEV)
     refused(capi.FSDP_E_INVAL, lambda: capi.fsdp_ortho_execute(o.plan, ws.data_ptr(), need - 1))
@@ -240,12 +248,10 @@ def test_refusals_on_the_device():
         o.allocate(ws[:need - 1])
     o.execute()
     torch.cuda.synchronize()
-    assert torch.equal(x[:128], x[128:256])
-    with Orthogonalizer([(16, 8)]) as over:     # the workspace holds the input
-        inside = ws[256:512].view(torch.bfloat16).view(16, 8)
-        over.bind([inside])
-        big = torch.empty(over.workspace_bytes + 1024, dtype=torch.uint8, device=DEV)
-        over.bind([big[512:768].view(torch.bfloat16).view(16, 8)])
+    assert torch.equal(x[:n], x[n:2 * n])
+    with Orthogonalizer([(1, 2000)]) as over:     # the workspace holds the input
+        big = torch.empty(over.workspace_bytes + 8192, dtype=torch.uint8, device=DEV)
+        over.bind([big[512:4512].view(torch.bfloat16).view(1, 2000)])
         refused(capi.FSDP_E_INVAL, lambda: capi.fsdp_ortho_execute(over.plan, big))
     o.close()
 

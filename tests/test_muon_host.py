@@ -125,7 +125,7 @@ def test_muon_binding_rejects_undersized_and_host_tensors():
 
 def test_ortho_plan_layout_and_refusals():
     ns = [(3.4445, -4.7750, 2.0315)] * 5
-    p = capi.fsdp_ortho_plan_create([5, 0, 300], [7, 4, 20], ns)
+    p = capi.fsdp_ortho_plan_create([5, 0, 300], [7, 4, 200], ns)
     n, ws = capi.fsdp_ortho_plan_info(p)
     assert n == 3 and ws > 0 and ws % 256 == 0
     assert _status(lambda: capi.fsdp_ortho_execute(p, 0x1000, ws, stream=0)) == capi.FSDP_E_STATE
@@ -141,7 +141,7 @@ def test_ortho_plan_layout_and_refusals():
             (ptr, [0x30000, 0, 0x30000 + 2 * 34], 0, capi.FSDP_E_INVAL),
             (ptr, [0x20000, 0, 0x40000], 0, capi.FSDP_E_INVAL),
             (ptr, [0x30000, 0, 0x10000 + 2 * 34], 0, capi.FSDP_E_INVAL),
-            ([0x10000, 0, 0x30000], [0x30000 + 5990 * 4, 0, 0x40000], 1, capi.FSDP_E_INVAL)):
+            ([0x10000, 0, 0x30000], [0x30000 + 59990 * 4, 0, 0x90000], 1, capi.FSDP_E_INVAL)):
         assert _status(lambda: capi.fsdp_ortho_bind(p, ins, outs, dtype, stream=0)) == status
     capi.fsdp_ortho_plan_destroy(p)
     capi.fsdp_ortho_plan_destroy(None)
