@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <cstdint>
 #include <string>
 #include <vector>
@@ -114,15 +113,67 @@ void spread(std::vector<fsdp::OrthoTile> *tiles) {
 // Bytes of parts of A that a block sums by itself.
 constexpr int64_t kSumsInBlock = 192 << 10;
 
-// Tile sides and the parts of X X^T's sum.
+// Tile sides and the parts of X X^T's sum: what a model of a launch's time says,
+// in clocks.  A CU takes `per` clocks for each element of a tile's sum, and a
+// tile no less than `alone` however many CUs are idle; measured on products of
+// 256 to 4096 rows (256: 46 clocks where every CU has a tile; 128: 13 each and
+// 16 alone; 64: 6 and 11).  Larger tiles read their operands less often, smaller
+// ones fill the CUs where there are few: one 4096 x 4096 matrix's a X + B X takes
+// 150 us in 256 x 256 tiles and 165 in 128 x 128, one 2048 x 2048's 31 and 12; two
+// such matrices' X X^T (272 tiles of 256) 135 and 105.  A split sum costs a launch
+// and its fp32 parts' way through memory: X X^T of two 1024 x 8192 matrices takes
+// 131 us whole in 128 x 128 tiles, 113 in two parts.
+struct Tile {
+    int32_t side;
+    double per, alone;
+};
+constexpr Tile kTiles[] = {{256, 46.0, 46.0}, {128, 13.0, 16.0}, {64, 6.0, 11.0}};
+constexpr double kCus = 256.0, kJoinClocks = 12000.0, kPartBytesPerClock = 2000.0;
+
+enum Product { kXXT, kAA, kBX };
+
+// Clocks of one launch over the plan's matrices.
+double clocks(const fsdp_ortho_plan &p, Product what, const Tile &tile, int32_t split) {
+    double work = 0.0, shortest = 1e300, longest = 0.0, tiles = 0.0;
+    for (const fsdp::OrthoMat &M : p.mats) {
+        if (M.m <= fsdp::kSmallMax) continue;
+        const double a = (M.mp + tile.side - 1) / tile.side, b = (M.np + tile.side - 1) / tile.side;
+        const double n = what == kBX ? a * b : a * (a + 1) / 2;
+        const double sum = static_cast<double>(what == kXXT ? M.np : M.mp) / split;
+        work += n * split * sum;
+        tiles += n;
+        shortest = std::min(shortest, sum);
+        longest = std::max(longest, sum);
+    }
+    // whole tiles a CU
+    const double busy = std::ceil(work / (kCus * shortest)) * shortest * tile.per;
+    const double join = split == 1 ? 0.0
+                                   : kJoinClocks + 2.0 * tiles * split * tile.side * tile.side * 4.0 /
+                                                       kPartBytesPerClock;
+    return std::max(busy, longest * tile.alone) + join;
+}
+
 void choose(fsdp_ortho_plan *p) {
-    auto env = [](const char *n, int32_t d) { const char *v = std::getenv(n); return v ? std::atoi(v) : d; };
-    p->t_gram = env("OT_G", 128);
-    p->t_poly = env("OT_P", 128);
-    p->t_apply = env("OT_A", 128);
-    p->split = env("OT_S", 1);
+    int32_t most = 16;
+    bool any = false;
     for (const fsdp::OrthoMat &M : p->mats)
-        if (M.m > fsdp::kSmallMax) p->split = std::min(p->split, M.np / 128);
+        if (M.m > fsdp::kSmallMax) {
+            most = std::min(most, M.np / 128);
+            any = true;
+        }
+    if (!any) return;
+    double best[3] = {1e300, 1e300, 1e300};
+    for (const Tile &tile : kTiles) {
+        int32_t *side[3] = {&p->t_gram, &p->t_poly, &p->t_apply};
+        for (Product what : {kXXT, kAA, kBX})
+            for (int32_t split = 1; split <= (what == kXXT ? most : 1); ++split) {
+                const double t = clocks(*p, what, tile, split);
+                if (t >= best[what]) continue;
+                best[what] = t;
+                *side[what] = tile.side;
+                if (what == kXXT) p->split = split;
+            }
+    }
 }
 
 // A matrix of few rows: its slabs; true if it needs no norm of its own (one
@@ -177,9 +228,14 @@ void layout(fsdp_ortho_plan *p) {
             for (int32_t k = 0; k < M.mp / 64; ++k) p->init.push_back({id, k, j, 0});
     }
     choose(p);
-    for (size_t i = 0; i < p->mats.size(); ++i) {
-        const fsdp::OrthoMat &M = p->mats[i];
-        const int32_t id = static_cast<int32_t>(i);
+    // the matrices with the longest sums first, so that short tiles come last
+    std::vector<int32_t> order(p->mats.size());
+    for (size_t i = 0; i < order.size(); ++i) order[i] = static_cast<int32_t>(i);
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
+        return p->mats[x].np > p->mats[y].np;
+    });
+    for (const int32_t id : order) {
+        const fsdp::OrthoMat &M = p->mats[id];
         if (M.m <= fsdp::kSmallMax) continue;
         auto count = [](int32_t side, int32_t tile) { return (side + tile - 1) / tile; };
         blocks(id, count(M.mp, p->t_gram), count(M.mp, p->t_gram), true, &p->gram);
@@ -454,7 +510,7 @@ fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *p, void *workspace, int64_
         });
         run(p->apply, [&] {
             return fsdp::launch_ortho_apply(p->t_apply, apply, count(p->apply), mats, workspace, src,
-                                            k == 0, last, p->coef[k], st);
+                                            k == 0, k == 0 && !p->f32, last, p->coef[k], st);
         });
     }
     return e == hipSuccess ? FSDP_OK : hip_error(e, (std::string(call) + ": launch").c_str());

@@ -48,6 +48,15 @@ constexpr int kLogX = 12;
 
 __device__ __forceinline__ char *at(void *ws, int64_t off) { return static_cast<char *>(ws) + off; }
 
+// x as one fp32 value.  Without this the compiler may take a product and its
+// conversion to fp16 as one operation of one rounding in one place and as two
+// in another, and a high part that is stored then differs, where the two
+// round apart, from the one that the low part was taken against.
+__device__ __forceinline__ float settled(float x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // Element (row, col) of a matrix in panels of 32 columns with `rows` rows.
 __device__ __forceinline__ int64_t panel_at(int rows, int row, int col) {
     return (static_cast<int64_t>(col >> 5) * rows + row) * 32 + (col & 31);
@@ -76,24 +85,68 @@ __device__ __forceinline__ double block_sum(double x) {
     return s;
 }
 
+// Eight neighbouring values from i; one load, or two, where `vec` says that
+// they may be.
+template <bool kF32>
+__device__ __forceinline__ void load_in8(const void *in, int64_t i, bool vec, float (&x)[8]) {
+    if constexpr (kF32) {
+        const float *p = static_cast<const float *>(in) + i;
+        if (vec) {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = a[e], x[e + 4] = b[e];
+            return;
+        }
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(in) + i;
+        if (vec) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[2 * e] = bf16_lo(w[e]), x[2 * e + 1] = bf16_hi(w[e]);
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = load_in<kF32>(in, i + e);
+}
+
 // Sums of squares in fp64: no scaling is needed for the smallest and largest
-// values, and the order is fixed.
+// values, and the order is fixed.  Parts start at multiples of eight elements,
+// and a thread has four loads of eight under way.
 template <bool kF32>
 __global__ __launch_bounds__(kBlock) void ortho_norm_kernel(const OrthoTile *__restrict__ tiles,
                                                             const OrthoMat *__restrict__ mats,
                                                             void *ws) {
     const OrthoTile tl = tiles[blockIdx.x];
     const OrthoMat M = mats[tl.mat];
-    const int64_t total = static_cast<int64_t>(M.rows) * M.cols;
-    const int64_t per = (total + M.n_parts - 1) / M.n_parts;
-    const int64_t lo = per * tl.ti, hi = lo + per < total ? lo + per : total;
-    double s = 0.0;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kBlock) {
-        const double x = load_in<kF32>(M.in, i);
-        s += x * x;
+    const int64_t total = static_cast<int64_t>(M.rows) * M.cols, eights = total >> 3;
+    const int64_t per = (eights + M.n_parts - 1) / M.n_parts;
+    const int64_t lo = per * tl.ti, hi = lo + per < eights ? lo + per : eights;
+    const bool vec = (lo32(M.in) & 15u) == 0;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int64_t i = lo + threadIdx.x; i < hi; i += 4 * kBlock) {
+        float x[4][8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            if (i + t * kBlock < hi) {
+                load_in8<kF32>(M.in, (i + t * kBlock) * 8, vec, x[t]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[t][e] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[t] += static_cast<double>(x[t][e]) * x[t][e];
     }
-    s = block_sum(s);
-    if (threadIdx.x == 0) reinterpret_cast<double *>(at(ws, M.parts))[tl.ti] = s;
+    if (tl.ti == M.n_parts - 1 && eights * 8 + threadIdx.x < total) {
+        const double x = load_in<kF32>(M.in, eights * 8 + threadIdx.x);
+        s[0] += x * x;
+    }
+    const double sum = block_sum((s[0] + s[1]) + (s[2] + s[3]));
+    if (threadIdx.x == 0) reinterpret_cast<double *>(at(ws, M.parts))[tl.ti] = sum;
 }
 
 // The scalars of a matrix from its norm: X = U / (norm + eps) is stored as U
@@ -121,16 +174,38 @@ __device__ __forceinline__ OrthoScal scalars(double norm, double eps, int32_t gr
     return s;
 }
 
-// X^T's 64 x 64 piece (rows 64 tj of n, columns 64 ti of m).  Stored is U
-// 2^k, exact in fp16 for bf16 inputs within 2^-26 of the norm (the low part
-// holds the rest).
+// X^T's 64 x 64 piece (rows 64 tj of n, columns 64 ti of m), eight neighbouring
+// values a thread and turn: of a tall U as they lie, of a wide one turned over in
+// LDS.  A bf16 input times 2^k is an fp16 value but for what lies under 2^-26 of
+// the norm (2^-37 of the norm at most is lost there); an fp32 input leaves a low
+// part.
 template <bool kF32>
 __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__restrict__ tiles,
                                                             const OrthoMat *__restrict__ mats,
                                                             void *ws, double eps, int32_t growth) {
-    __shared__ float buf[64][65];
+    constexpr int kParts = kF32 ? 2 : 1;
+    // rows of 64 halves and 8 more: a turned row's reads start in other banks
+    __shared__ __attribute__((aligned(16))) _Float16 buf[kParts][64][72];
     const OrthoTile tl = tiles[blockIdx.x];
     const OrthoMat M = mats[tl.mat];
+    const int r0 = (M.wide ? tl.ti : tl.tj) * 64, c0 = (M.wide ? tl.tj : tl.ti) * 64;
+    const bool vec = (lo32(M.in) & 15u) == 0 && (M.cols & 7) == 0;
+    // the values leave before the norm's parts are summed
+    float x[2][8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int u = t * kBlock + threadIdx.x, r = r0 + (u >> 3), c = c0 + (u & 7) * 8;
+        const int64_t o = static_cast<int64_t>(r) * M.cols + c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[t][e] = 0.0f;
+        if (r < M.rows && c + 8 <= M.cols) {
+            load_in8<kF32>(M.in, o, vec, x[t]);
+        } else if (r < M.rows) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < M.cols) x[t][e] = load_in<kF32>(M.in, o + e);
+        }
+    }
     const double *parts = reinterpret_cast<const double *>(at(ws, M.parts));
     double s = 0.0;
     for (int i = threadIdx.x; i < M.n_parts; i += kBlock) s += parts[i];
@@ -140,24 +215,43 @@ __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__r
     const OrthoScal sc = scalars(norm, eps, growth, &k);
     if (tl.ti == 0 && tl.tj == 0 && threadIdx.x == 0)
         *reinterpret_cast<OrthoScal *>(at(ws, M.scal)) = sc;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    const int r0 = (M.wide ? tl.ti : tl.tj) * 64, c0 = (M.wide ? tl.tj : tl.ti) * 64;
-    for (int y = ty; y < 64; y += kBlock / 64) {
-        const int r = r0 + y, c = c0 + tx;
-        float x = 0.0f;
-        if (fine && r < M.rows && c < M.cols)
-            x = ldexpf(load_in<kF32>(M.in, static_cast<int64_t>(r) * M.cols + c), k);
-        buf[y][tx] = x;
+    f16x8 *hi = reinterpret_cast<f16x8 *>(at(ws, M.t[0]));
+    f16x8 *lo = reinterpret_cast<f16x8 *>(at(ws, M.lo));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int u = t * kBlock + threadIdx.x, y = u >> 3, c = (u & 7) * 8;
+        f16x8 h, l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float f = fine ? settled(ldexpf(x[t][e], k)) : 0.0f;
+            h[e] = static_cast<_Float16>(f);
+            l[e] = static_cast<_Float16>(f - static_cast<float>(h[e]));
+        }
+        if (M.wide) {
+            *reinterpret_cast<f16x8 *>(&buf[0][y][c]) = h;
+            if constexpr (kF32) *reinterpret_cast<f16x8 *>(&buf[kParts - 1][y][c]) = l;
+        } else {
+            const int64_t o = panel_at(M.np, tl.tj * 64 + y, tl.ti * 64 + c) >> 3;
+            hi[o] = h;
+            if constexpr (kF32) lo[o] = l;
+        }
     }
+    if (!M.wide) return;
     __syncthreads();
-    _Float16 *hi = reinterpret_cast<_Float16 *>(at(ws, M.t[0]));
-    _Float16 *lo = reinterpret_cast<_Float16 *>(at(ws, M.lo));
-    for (int y = ty; y < 64; y += kBlock / 64) {
-        const float x = M.wide ? buf[tx][y] : buf[y][tx];
-        const _Float16 h = static_cast<_Float16>(x);
-        const int64_t o = panel_at(M.np, tl.tj * 64 + y, tl.ti * 64 + tx);
-        hi[o] = h;
-        lo[o] = static_cast<_Float16>(x - static_cast<float>(h));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        // row y of X^T, its columns c .. + 8; a wave's lanes take 64 rows
+        const int u = t * kBlock + threadIdx.x, y = u & 63, c = (u >> 6) * 8;
+        const int64_t o = panel_at(M.np, tl.tj * 64 + y, tl.ti * 64 + c) >> 3;
+        f16x8 v;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = buf[0][c + e][y];
+        hi[o] = v;
+        if constexpr (kF32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = buf[kParts - 1][c + e][y];
+            lo[o] = v;
+        }
     }
 }
 
@@ -165,6 +259,8 @@ __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__r
 // products
 // ---------------------------------------------------------------------------
 
+// when: the first iteration; X has no low part yet (bf16 inputs)
+enum { kFirst = 1, kHigh = 2 };
 // kGramPart: a stretch of kGram's sum, left in fp32; kGramJoin: their sum
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3, kGramPart = 4, kGramJoin = 5 };
 
@@ -241,15 +337,6 @@ __device__ __forceinline__ f16x8 read_cols(lds_char *t, int col, int lane) {
     return u.v;
 }
 
-// x as one fp32 value.  Without this the compiler may take a product and its
-// conversion to fp16 as one operation of one rounding in one place and as two
-// in another, and a high part that is stored then differs, where the two
-// round apart, from the one that the low part was taken against.
-__device__ __forceinline__ float settled(float x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
 union Half8 {
     f16x8 f;
     s16x8 s;
@@ -292,7 +379,7 @@ __device__ __forceinline__ void border() {
 template <int KIND, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const OrthoTile *__restrict__ tiles, const OrthoMat *__restrict__ mats, void *ws, int32_t src,
-    int32_t first, int32_t split, OrthoCoef coef) {
+    int32_t when, int32_t split, OrthoCoef coef) {
     constexpr int WAVES = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
     constexpr int NST = 4;
     constexpr bool kXXT = KIND == kGram || KIND == kGramPart || KIND == kGramJoin;
@@ -407,7 +494,7 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                     if (i < M.mp && j < M.np) {
                         const int64_t o = panel_at(M.np, j, i) >> 3;
                         hi = reinterpret_cast<const f16x8 *>(T)[o];
-                        lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o];
+                        if (!(when & kHigh)) lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o];
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -485,7 +572,7 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     // half of the rows).
     lds_char *st = lds + wave * 2048;
     if constexpr (kSym || KIND == kLast) border<0>();
-    const float phi = first ? sc.phi0 : sc.phi, rho = first ? sc.rho : 1.0f;
+    const float phi = when & kFirst ? sc.phi0 : sc.phi, rho = when & kFirst ? sc.rho : 1.0f;
     const float alpha = kXXT   ? ldexpf(phi * phi, kLogA)
                         : KIND == kPoly ? ldexpf(coef.c, -kLogA)
                                         : ldexpf(rho, -kLogA);
@@ -937,19 +1024,19 @@ namespace {
 // and five blocks a CU
 template <int KIND>
 hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
-                          void *ws, int32_t src, bool first, int32_t split, OrthoCoef c,
+                          void *ws, int32_t src, int32_t when, int32_t split, OrthoCoef c,
                           hipStream_t st) {
     if (n == 0) return hipSuccess;
     const unsigned grid = static_cast<unsigned>(n);
     if (tile == 256)
         ortho_product_kernel<KIND, 256, 256, 2, 4>
-            <<<grid, 512, 0, st>>>(tiles, mats, ws, src, first, split, c);
+            <<<grid, 512, 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 128)
         ortho_product_kernel<KIND, 128, 128, 2, 2>
-            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, first, split, c);
+            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, when, split, c);
     else
         ortho_product_kernel<KIND, 64, 64, 2, 2>
-            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, first, split, c);
+            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, when, split, c);
     return hipGetLastError();
 }
 
@@ -998,25 +1085,27 @@ hipError_t launch_ortho_gram(int32_t tile, const OrthoTile *tiles, int64_t n,
                              const OrthoTile *join, int64_t n_join, int32_t split,
                              const OrthoMat *mats, void *ws, int32_t src, bool first,
                              hipStream_t st) {
+    const int32_t when = first ? kFirst : 0;
     if (split == 1)
-        return launch_product<kGram>(tile, tiles, n, mats, ws, src, first, 1, OrthoCoef{}, st);
+        return launch_product<kGram>(tile, tiles, n, mats, ws, src, when, 1, OrthoCoef{}, st);
     const hipError_t e =
-        launch_product<kGramPart>(tile, tiles, n, mats, ws, src, first, split, OrthoCoef{}, st);
+        launch_product<kGramPart>(tile, tiles, n, mats, ws, src, when, split, OrthoCoef{}, st);
     if (e != hipSuccess) return e;
-    return launch_product<kGramJoin>(tile, join, n_join, mats, ws, src, first, split, OrthoCoef{},
+    return launch_product<kGramJoin>(tile, join, n_join, mats, ws, src, when, split, OrthoCoef{},
                                      st);
 }
 
 hipError_t launch_ortho_poly(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
                              void *ws, OrthoCoef c, hipStream_t st) {
-    return launch_product<kPoly>(tile, tiles, n, mats, ws, 0, false, 1, c, st);
+    return launch_product<kPoly>(tile, tiles, n, mats, ws, 0, 0, 1, c, st);
 }
 
 hipError_t launch_ortho_apply(int32_t tile, const OrthoTile *tiles, int64_t n,
-                              const OrthoMat *mats, void *ws, int32_t src, bool first, bool last,
-                              OrthoCoef c, hipStream_t st) {
-    if (last) return launch_product<kLast>(tile, tiles, n, mats, ws, src, first, 1, c, st);
-    return launch_product<kApply>(tile, tiles, n, mats, ws, src, first, 1, c, st);
+                              const OrthoMat *mats, void *ws, int32_t src, bool first, bool high,
+                              bool last, OrthoCoef c, hipStream_t st) {
+    const int32_t when = (first ? kFirst : 0) | (high ? kHigh : 0);
+    if (last) return launch_product<kLast>(tile, tiles, n, mats, ws, src, when, 1, c, st);
+    return launch_product<kApply>(tile, tiles, n, mats, ws, src, when, 1, c, st);
 }
 
 }  // namespace fsdp

@@ -62,8 +62,9 @@ enum { kSmallAll = 0, kSmallStart = 1, kSmallStep = 2, kSmallLast = 3 };
 // Partial sums of squares; tiles: (matrix, part).
 hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              bool f32, hipStream_t st);
-// The scaled X^T and the scalars; tiles: 64 x 64 pieces of [np][mp].  growth:
-// log2 of the most that the iterations can magnify a singular value.
+// The scaled X^T (for fp32 inputs the low part too) and the scalars; tiles: 64 x
+// 64 pieces of [np][mp].  growth: log2 of the most that the iterations can
+// magnify a singular value.
 hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              bool f32, double eps, int32_t growth, hipStream_t st);
 // Matrices of few rows, tiles: (matrix, slab), all of mp padded rows.
@@ -86,9 +87,9 @@ hipError_t launch_ortho_gram(int32_t tile, const OrthoTile *tiles, int64_t n,
 hipError_t launch_ortho_poly(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
                              void *ws, OrthoCoef c, hipStream_t st);
 // X^T = a X^T + X^T B into the other high part and the low part, or with last
-// into out; tiles (ti of mp, tj of np)
+// into out; tiles (ti of mp, tj of np); high: there is no low part yet
 hipError_t launch_ortho_apply(int32_t tile, const OrthoTile *tiles, int64_t n,
-                              const OrthoMat *mats, void *ws, int32_t src, bool first, bool last,
-                              OrthoCoef c, hipStream_t st);
+                              const OrthoMat *mats, void *ws, int32_t src, bool first, bool high,
+                              bool last, OrthoCoef c, hipStream_t st);
 
 }  // namespace fsdp
