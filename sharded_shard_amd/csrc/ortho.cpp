@@ -181,12 +181,18 @@ void choose(fsdp_ortho_plan *p) {
 template <typename F>
 bool few_rows(int32_t id, fsdp::OrthoMat *M, fsdp_ortho_plan *p, F &&take) {
     const int cls = M->mp == 32 ? 0 : M->mp == 64 ? 1 : 2;
-    const int32_t nb = fsdp::small_slab(M->mp), slabs = (M->n + nb - 1) / nb;
-    if (slabs == 1) {
+    const int32_t nb = fsdp::small_slab(M->mp);
+    const int64_t part = static_cast<int64_t>(M->mp) * M->mp * 4;
+    M->slab = nb;
+    if (M->n <= nb) {
         p->one[cls].push_back({id, 0, 0, 0});
         return true;
     }
-    const int64_t part = static_cast<int64_t>(M->mp) * M->mp * 4;
+    // shorter slabs as long as every block can sum their parts by itself
+    auto count = [&](int32_t slab) { return (M->n + slab - 1) / slab; };
+    while (M->slab > 128 && count(round_up(M->slab / 2, 32)) * part <= kSumsInBlock)
+        M->slab = static_cast<int32_t>(round_up(M->slab / 2, 32));
+    const int32_t slabs = count(M->slab);
     M->t[0] = take(static_cast<int64_t>(slabs) * nb * M->mp * 4);
     M->a = take(slabs * part);
     M->b = take(slabs * part);

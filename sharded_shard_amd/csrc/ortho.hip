@@ -681,19 +681,20 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
 // products are few and do not average out (fp16 alone was up to 5e-3 off with
 // one to four rows), and the products are too small to bound the time.
 
-constexpr int kSmallBlock = 512;
-
 template <int MP>
 struct Small {
-    static constexpr int NB = small_slab(MP);           // columns of a slab
+    static constexpr int NB = small_slab(MP);           // columns of a slab, at most
     static constexpr int nb = MP / 16;                  // 16 x 16 blocks a side
-    static constexpr int kWaves = kSmallBlock / 64;
-    // blocks of a row that one wave has: its row of blocks and bj0 .. + kBJ
-    static constexpr int kBJ = MP == 128 ? 8 : MP == 64 ? 2 : 1;
-    static constexpr int kHalves = MP == 32 ? 2 : 1;    // stretches of the sum over columns
+    // with 128 rows the work of one block of threads is long: 16 waves (58 -> 54 us
+    // for a 128 x 128 matrix, 326 -> 277 for 32 of 128 x 2048)
+    static constexpr int kThreads = MP == 128 ? 1024 : 512, kWaves = kThreads / 64;
+    // blocks of A and B that one wave has: of its row of blocks, bj0 .. + kBJ
+    static constexpr int kBJ = MP == 128 ? 4 : MP == 64 ? 2 : 1;
+    // up to 64 rows a wave sums 32 x 32 of A over one stretch in kStretches
+    static constexpr int kStretches = MP == 32 ? 8 : MP == 64 ? 2 : 1;
     static constexpr int kT = NB * MP * 2, kA = MP * MP * 2;     // bytes of one part in LDS
-    static constexpr int kScratch = MP == 32 ? 4096 : 0;
-    static constexpr int kLds = 2 * kT + 2 * kA + kScratch;
+    // those sums have LDS of their own: no barrier before A takes their place
+    static constexpr int kLds = 2 * kT + 2 * kA + (MP == 128 ? 0 : kWaves * 4096);
 };
 
 // Element (row, col .. + 4 or 8) in LDS panels of 32 columns with `rows` rows;
@@ -744,11 +745,11 @@ __device__ __forceinline__ void put_split(lds_char *hi, lds_char *lo, int o, con
 }
 
 template <int MP, bool kF32>
-__global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
+__global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
     const OrthoTile *__restrict__ tiles, const OrthoMat *__restrict__ mats, void *ws, int32_t mode,
     int32_t step, int32_t n_steps, const OrthoCoef *__restrict__ coefs, double eps, int32_t growth) {
     using S = Small<MP>;
-    constexpr int NB = S::NB, nb = S::nb, kBJ = S::kBJ;
+    constexpr int NB = S::NB, nb = S::nb, kBJ = S::kBJ, kSmallBlock = S::kThreads;
     __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
     __shared__ double sums[S::kWaves];
     lds_char *th = (lds_char *)smem, *tlo = th + S::kT, *ah = tlo + S::kT, *al = ah + S::kA;
@@ -757,18 +758,16 @@ __global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
     const OrthoTile tl = tiles[blockIdx.x];
     const OrthoMat M = mats[tl.mat];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
-    const int slab = tl.ti, j0 = slab * NB;
-    const int rows = M.n - j0 < NB ? M.n - j0 : NB, rows32 = (rows + 31) & ~31;
-    // this wave's blocks of A and B, and of a split sum its stretch
-    const int bi = MP == 128 ? wave : MP == 64 ? wave >> 1 : (wave >> 1) & 1;
-    const int bj0 = MP == 128 ? 0 : MP == 64 ? (wave & 1) * 2 : wave & 1;
-    const int half = MP == 32 ? wave >> 2 : 0;
+    const int slab = tl.ti, j0 = slab * M.slab;
+    const int rows = M.n - j0 < M.slab ? M.n - j0 : M.slab, rows32 = (rows + 31) & ~31;
+    // this wave's blocks of A and B
+    const int bi = MP == 32 ? (wave >> 1) & 1 : wave >> 1, bj0 = (wave & 1) * kBJ;
     char *image = at(ws, M.t[0]) + static_cast<int64_t>(slab) * 2 * S::kT;
 
     OrthoScal sc;
     if (mode == kSmallAll || mode == kSmallStart) {
         // eight neighbouring rows i of one column j a thread and turn
-        constexpr int kTurns = NB * MP / 8 / kSmallBlock;
+        constexpr int kTurns = (NB * MP / 8 + kSmallBlock - 1) / kSmallBlock;
         float x[kTurns][8];
         double s = 0.0;
 #pragma unroll
@@ -805,7 +804,7 @@ __global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
         for (int t = 0; t < kTurns; ++t) {
             const int u = t * kSmallBlock + tid;
             const int j = M.wide ? u % NB : u / (MP / 8), i = (M.wide ? u / NB : u % (MP / 8)) * 8;
-            if (j < rows32) {
+            if (j < rows32 && i < MP) {
                 Half8 h, l;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -835,20 +834,56 @@ __global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
     f32x4 a[kBJ];
     // this wave's blocks of X X^T over the slab
     auto gram = [&]() {
+        if constexpr (S::kStretches > 1) {
+            const int quad = MP == 64 ? wave & 3 : 0, qi = (quad >> 1) * 32, qj = (quad & 1) * 32;
+            const int stretch = MP == 64 ? wave >> 2 : wave;
+            f32x4 c[2][2];
 #pragma unroll
-        for (int y = 0; y < kBJ; ++y) a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int r = half * 32; r < rows32; r += 32 * S::kHalves) {
-            const f16x8 ph = small_cols(th, NB, r, bi * 16, lane);
-            const f16x8 pl = small_cols(tlo, NB, r, bi * 16, lane);
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int y = 0; y < kBJ; ++y)
-                a[y] = fine_product(ph, pl, small_cols(th, NB, r, (bj0 + y) * 16, lane),
-                                    small_cols(tlo, NB, r, (bj0 + y) * 16, lane), a[y]);
-        }
-        if constexpr (S::kHalves > 1) {
-            if (half == 1) scratch[(wave & 3) * 64 + lane] = a[0];
+                for (int y = 0; y < 2; ++y) c[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+            for (int r = stretch * 32; r < rows32; r += 32 * S::kStretches) {
+                f16x8 ph[2], pl[2], qh[2], ql[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    ph[x] = small_cols(th, NB, r, qi + 16 * x, lane);
+                    pl[x] = small_cols(tlo, NB, r, qi + 16 * x, lane);
+                    qh[x] = small_cols(th, NB, r, qj + 16 * x, lane);
+                    ql[x] = small_cols(tlo, NB, r, qj + 16 * x, lane);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        c[x][y] = fine_product(ph[x], pl[x], qh[y], ql[y], c[x][y]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) scratch[(wave * 4 + x * 2 + y) * 64 + lane] = c[x][y];
             __syncthreads();
-            a[0] += scratch[(wave & 3) * 64 + lane];     // the first stretch's waves use it
+            // the stretches in order
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y) {
+                const int bj = bj0 + y, of = (bi >> 1) * 2 + (bj >> 1), sub = (bi & 1) * 2 + (bj & 1);
+                a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int t = 0; t < S::kStretches; ++t)
+                    if (32 * t < rows32)
+                        a[y] += scratch[((MP == 64 ? t * 4 + of : t) * 4 + sub) * 64 + lane];
+            }
+        } else {
+#pragma unroll
+            for (int y = 0; y < kBJ; ++y) a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < rows32; r += 32) {
+                const f16x8 ph = small_cols(th, NB, r, bi * 16, lane);
+                const f16x8 pl = small_cols(tlo, NB, r, bi * 16, lane);
+#pragma unroll
+                for (int y = 0; y < kBJ; ++y)
+                    a[y] = fine_product(ph, pl, small_cols(th, NB, r, (bj0 + y) * 16, lane),
+                                        small_cols(tlo, NB, r, (bj0 + y) * 16, lane), a[y]);
+            }
         }
     };
     // parts of A: one 16 x 16 block after the other, a lane's four values together
@@ -856,7 +891,7 @@ __global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
         return reinterpret_cast<f32x4 *>(at(ws, (k & 1) ? M.b : M.a)) + (bi * nb + bj0 + y) * 64 +
                lane;
     };
-    const bool mine = half == 0;
+    const bool mine = MP > 32 || wave < 4;
     if (mode == kSmallAll || mode == kSmallStart) gram();
     if (mode == kSmallStart && mine) {
 #pragma unroll
@@ -918,16 +953,35 @@ __global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
         // X = a X + B X: a wave takes 16 columns j at a time, which no other wave reads or writes
         const bool last = k + 1 == n_steps;
         const float ca = ldexpf(c.a, kLogA), cb = ldexpf(rho, -kLogA);
-        for (int r = wave * 16; r < rows; r += S::kWaves * 16) {
+        // up to 64 rows B's operands stay in registers
+        constexpr bool kHeld = MP <= 64;
+        f16x8 ph[kHeld ? nb : 1][MP / 32], pl[kHeld ? nb : 1][MP / 32];
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int x = 0; x < nb; ++x)
+#pragma unroll
+                for (int q = 0; q < MP / 32; ++q) {
+                    ph[x][q] = small_rows(ah, MP, x * 16, q * 32, lane);
+                    pl[x][q] = small_rows(al, MP, x * 16, q * 32, lane);
+                }
+        }
+        // with 128 rows two waves share 16 columns, half of the rows each
+        constexpr int kSide = kHeld ? 1 : 2, kX = nb / kSide;
+        const int x0 = kHeld ? 0 : (wave & 1) * kX;
+        static_assert(kHeld || NB == S::kWaves / kSide * 16, "one turn");
+        for (int r = wave / kSide * 16; r < (kHeld ? rows : NB); r += S::kWaves / kSide * 16) {
             f16x8 qh[MP / 32], ql[MP / 32];
 #pragma unroll
             for (int q = 0; q < MP / 32; ++q) {
                 qh[q] = small_rows(th, NB, r, q * 32, lane);
                 ql[q] = small_rows(tlo, NB, r, q * 32, lane);
             }
+            if constexpr (!kHeld) __syncthreads();      // both have read them
             const int j = r + (lane & 15);
 #pragma unroll
-            for (int x = 0; x < nb; ++x) {
+            for (int y = 0; y < kX; ++y) {
+                if (!kHeld && r >= rows) break;
+                const int x = kHeld ? y : x0 + y;
                 const int o = small_at(NB, j, x * 16 + 4 * g);
                 const f16x4 xh = *(lds_f16x4 *)(th + o), xl = *(lds_f16x4 *)(tlo + o);
                 f32x4 v;
@@ -935,9 +989,13 @@ __global__ __launch_bounds__(kSmallBlock) void ortho_small_kernel(
                 for (int e = 0; e < 4; ++e)
                     v[e] = ca * (static_cast<float>(xh[e]) + static_cast<float>(xl[e]));
 #pragma unroll
-                for (int q = 0; q < MP / 32; ++q)
-                    v = fine_product(small_rows(ah, MP, x * 16, q * 32, lane),
-                                     small_rows(al, MP, x * 16, q * 32, lane), qh[q], ql[q], v);
+                for (int q = 0; q < MP / 32; ++q) {
+                    if constexpr (!kHeld) {
+                        ph[0][q] = small_rows(ah, MP, x * 16, q * 32, lane);
+                        pl[0][q] = small_rows(al, MP, x * 16, q * 32, lane);
+                    }
+                    v = fine_product(ph[kHeld ? x : 0][q], pl[kHeld ? x : 0][q], qh[q], ql[q], v);
+                }
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = cb * v[e];
@@ -1049,13 +1107,13 @@ void small(int32_t mp, unsigned n, const OrthoTile *tiles, const OrthoMat *mats,
            int32_t mode, int32_t step, int32_t n_steps, const OrthoCoef *coefs, double eps,
            int32_t growth, hipStream_t st) {
     if (mp == 32)
-        ortho_small_kernel<32, kF32><<<n, kSmallBlock, 0, st>>>(tiles, mats, ws, mode, step,
+        ortho_small_kernel<32, kF32><<<n, Small<32>::kThreads, 0, st>>>(tiles, mats, ws, mode, step,
                                                                 n_steps, coefs, eps, growth);
     else if (mp == 64)
-        ortho_small_kernel<64, kF32><<<n, kSmallBlock, 0, st>>>(tiles, mats, ws, mode, step,
+        ortho_small_kernel<64, kF32><<<n, Small<64>::kThreads, 0, st>>>(tiles, mats, ws, mode, step,
                                                                 n_steps, coefs, eps, growth);
     else
-        ortho_small_kernel<128, kF32><<<n, kSmallBlock, 0, st>>>(tiles, mats, ws, mode, step,
+        ortho_small_kernel<128, kF32><<<n, Small<128>::kThreads, 0, st>>>(tiles, mats, ws, mode, step,
                                                                  n_steps, coefs, eps, growth);
 }
 

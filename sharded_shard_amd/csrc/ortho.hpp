@@ -32,7 +32,7 @@ struct OrthoMat {
     int32_t rows, cols;
     int32_t m, n, mp, np;
     int32_t n_parts, wide;  // wide: rows <= cols, X = U; else X = U^T
-    int32_t n_sums, rsv;    // few rows: parts of A that every block sums
+    int32_t n_sums, slab;   // few rows: parts of A that every block sums, columns of a slab
 };
 
 // What one init pass leaves for the products: the true X is phi0 times the
@@ -55,7 +55,7 @@ struct OrthoCoef {
 // 128 rows, worked on in slabs of so many columns.
 constexpr int32_t kSmallMax = 128;
 constexpr int32_t small_rows_of(int32_t m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
-constexpr int32_t small_slab(int32_t mp) { return mp == 128 ? 128 : mp == 64 ? 512 : 1024; }
+constexpr int32_t small_slab(int32_t mp) { return mp == 128 ? 128 : mp == 64 ? 416 : 896; }
 // What a launch does: all steps (one slab), the start, one step, the last step.
 enum { kSmallAll = 0, kSmallStart = 1, kSmallStep = 2, kSmallLast = 3 };
 
