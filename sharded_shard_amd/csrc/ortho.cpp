@@ -127,7 +127,7 @@ struct Tile {
     int32_t side;
     double per, alone;
 };
-constexpr Tile kTiles[] = {{256, 46.0, 46.0}, {128, 13.0, 16.0}, {64, 6.0, 11.0}};
+constexpr Tile kTiles[] = {{256, 46.0, 46.0}, {192, 34.0, 34.0}, {128, 13.0, 16.0}, {64, 6.0, 11.0}};
 constexpr double kCus = 256.0, kJoinClocks = 12000.0, kPartBytesPerClock = 2000.0;
 
 enum Product { kXXT, kAA, kBX };

@@ -1078,8 +1078,8 @@ hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *
 
 namespace {
 
-// 256 x 256 by eight waves, one block a CU; 128 x 128 and 64 x 64 by four, two
-// and five blocks a CU
+// 256 x 256 by eight waves and 192 x 192 by twelve, one block a CU; 128 x 128 and
+// 64 x 64 by four, two and five blocks a CU
 template <int KIND>
 hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
                           void *ws, int32_t src, int32_t when, int32_t split, OrthoCoef c,
@@ -1089,6 +1089,9 @@ hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const
     if (tile == 256)
         ortho_product_kernel<KIND, 256, 256, 2, 4>
             <<<grid, 512, 0, st>>>(tiles, mats, ws, src, when, split, c);
+    else if (tile == 192)
+        ortho_product_kernel<KIND, 192, 192, 6, 2>
+            <<<grid, 768, 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 128)
         ortho_product_kernel<KIND, 128, 128, 2, 2>
             <<<grid, 256, 0, st>>>(tiles, mats, ws, src, when, split, c);
