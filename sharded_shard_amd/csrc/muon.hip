@@ -11,8 +11,12 @@
 // rows of the reduce-scatter input, summed as the reduction does.
 //
 // All three move 12 to 14 bytes an element (2N + 10 with the reduction) for a
-// handful of operations: HBM bounds them, and the tiles, sub-ranges and cache
-// policies are the fused AdamW step's.
+// handful of operations: HBM bounds them.  One decoder block's matrices at 8
+// ranks (27 million elements a rank): momentum 64 us, 6.7 TB/s; with the
+// reduction 122 us, 6.5; update 55 us, 6.6.  Non-temporal loads and stores of the
+// shards are worth a fifth (78 us without either), plain stores of the segment
+// 5% over non-temporal ones.  Reserving LDS to hold fewer blocks a CU, which the
+// fused AdamW step gains from, costs 3 to 14% here.
 #include "muon.hpp"
 #include "rows.hpp"
 
@@ -24,7 +28,8 @@
 #ifndef FSDP_MUON_OUT_NT
 #define FSDP_MUON_OUT_NT 0
 #endif
-// elements per block where one row is read
+// elements per block where one row or none is read (1024 and 4096: 2 and 3%
+// slower)
 #ifndef FSDP_MUON_SUB
 #define FSDP_MUON_SUB 2048
 #endif
@@ -120,7 +125,7 @@ __device__ __forceinline__ void muon_run(float *X, const Src &src, uint16_t *dst
         vec = ap == (lo32(src.g) & 15u);
     }
     if (!vec) {
-        for (int64_t e = tid; e < valid; e += kBlock) scalar_at(X, src, dst, e, op);
+        for (int64_t e = tid; e < valid; e += blockDim.x) scalar_at(X, src, dst, e, op);
     } else {
         if (tid < head) scalar_at(X, src, dst, tid, op);
         const int64_t nq = (valid - head) >> 2;
@@ -128,7 +133,7 @@ __device__ __forceinline__ void muon_run(float *X, const Src &src, uint16_t *dst
         const int64_t lane = tid & 63;
         char *xb = reinterpret_cast<char *>(X + head);
         const uint32_t sb = static_cast<uint32_t>(nq) << 4;
-        for (int64_t qb = (tid >> 6) * 64 * QP; qb < nq; qb += (kBlock >> 6) * 64 * QP) {
+        for (int64_t qb = (tid >> 6) * 64 * QP; qb < nq; qb += (blockDim.x >> 6) * 64 * QP) {
             float in[QP][4];
             f32x4 x[QP], g[QP];
 #pragma unroll
@@ -237,25 +242,37 @@ __global__ __launch_bounds__(kBlock) void muon_update_kernel(
 }
 
 template <bool kNesterov>
-void reduce_momentum(unsigned grid, int32_t sp, hipStream_t st, const PackTile *tiles, int64_t n,
-                     const DevEntry *ents, const uint16_t *rs_in, uint16_t *ag_in, int64_t S,
-                     int32_t N, const float scal[2], bool aligned) {
+void reduce_momentum(hipStream_t st, const PackTile *tiles, int64_t n, const DevEntry *ents,
+                     const uint16_t *rs_in, uint16_t *ag_in, int64_t S, int32_t N,
+                     const float scal[2], bool aligned) {
     const Momentum<kNesterov> op{scal[0], scal[1]};
-    const int64_t sub = kTilePack / sp;
     const float fN = static_cast<float>(N);
-    // rows in flight as in the fused AdamW step: one up to 8 ranks, four above
-    if (aligned && N <= 8)
-        muon_reduce_momentum_kernel<kNesterov, 1, true><<<grid, kBlock, 0, st>>>(
-            tiles, n, sp, sub, ents, rs_in, ag_in, S, N, fN, op);
+    auto go = [&](auto kernel, int64_t want, int threads) {
+        const int32_t sp = split_for(kTilePack, want);
+        kernel<<<grid_for(n, sp), threads, 0, st>>>(tiles, n, sp, kTilePack / sp, ents, rs_in, ag_in,
+                                                   S, N, fN, op);
+    };
+    // Rows in flight and elements a block, from a sweep over both for 1 to 64
+    // ranks.  From 16 ranks a wave a block, two rows at a time: 64 ranks 6.4 TB/s
+    // (5.95 with four rows, 4.5 with one row and 2048 elements for four waves);
+    // misaligned 4.5 (3.9).  Below, as many rows as divide N, in fewer elements
+    // the more rows there are: 8 ranks 5.9 TB/s (5.4 with one row and 2048
+    // elements), 6 ranks 5.95 (5.45); misaligned rows two at a time, 5.3 TB/s at 6
+    // ranks (5.0 with one, 5.1 with three).
+    const int64_t most = 6144 / N;
+    const int64_t want = most > 2048 ? 2048 : (most < 512 ? 512 : most);
+    if (aligned && N >= 16)
+        go(muon_reduce_momentum_kernel<kNesterov, 2, true>, 512, 64);
+    else if (aligned && N % 3 == 0)
+        go(muon_reduce_momentum_kernel<kNesterov, 3, true>, want, kBlock);
+    else if (aligned && N >= 4)
+        go(muon_reduce_momentum_kernel<kNesterov, 4, true>, want, kBlock);
     else if (aligned)
-        muon_reduce_momentum_kernel<kNesterov, 4, true><<<grid, kBlock, 0, st>>>(
-            tiles, n, sp, sub, ents, rs_in, ag_in, S, N, fN, op);
-    else if (N <= 8)
-        muon_reduce_momentum_kernel<kNesterov, 1, false><<<grid, kBlock, 0, st>>>(
-            tiles, n, sp, sub, ents, rs_in, ag_in, S, N, fN, op);
+        go(muon_reduce_momentum_kernel<kNesterov, 2, true>, want, kBlock);
+    else if (N >= 16)
+        go(muon_reduce_momentum_kernel<kNesterov, 2, false>, 512, 64);
     else
-        muon_reduce_momentum_kernel<kNesterov, 4, false><<<grid, kBlock, 0, st>>>(
-            tiles, n, sp, sub, ents, rs_in, ag_in, S, N, fN, op);
+        go(muon_reduce_momentum_kernel<kNesterov, 2, false>, 2048, kBlock);
 }
 
 }  // namespace
@@ -280,14 +297,10 @@ hipError_t launch_muon_reduce_momentum(const PackTile *tiles, int64_t n, const D
                                        int32_t N, const float scal[2], bool nesterov,
                                        bool chunk_aligned, hipStream_t st) {
     if (n == 0) return hipSuccess;
-    // the state read and written: two more fp32 streams besides the N rows
-    const int32_t sp = split_rows(kTilePack, N, 4);
     if (nesterov)
-        reduce_momentum<true>(grid_for(n, sp), sp, st, tiles, n, ents, rs_in, ag_in, S, N, scal,
-                              chunk_aligned);
+        reduce_momentum<true>(st, tiles, n, ents, rs_in, ag_in, S, N, scal, chunk_aligned);
     else
-        reduce_momentum<false>(grid_for(n, sp), sp, st, tiles, n, ents, rs_in, ag_in, S, N, scal,
-                               chunk_aligned);
+        reduce_momentum<false>(st, tiles, n, ents, rs_in, ag_in, S, N, scal, chunk_aligned);
     return hipGetLastError();
 }
 
