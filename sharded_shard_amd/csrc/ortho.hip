@@ -766,20 +766,35 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
 
     OrthoScal sc;
     if (mode == kSmallAll || mode == kSmallStart) {
-        // eight neighbouring rows i of one column j a thread and turn
+        // eight neighbouring rows i of one column j a thread and turn; of a wide U a
+        // wave takes 16 columns and 32 rows, whose 1 KB in LDS is of one piece
+        auto wide_j = [](int u) { return (u >> 6) % (NB / 16) * 16 + (u & 15); };
+        auto wide_i = [](int u) { return (u >> 6) / (NB / 16) * 4 + ((u >> 4) & 3); };
         constexpr int kTurns = (NB * MP / 8 + kSmallBlock - 1) / kSmallBlock;
+        // every load leaves before the first is waited for: no branch around them,
+        // places outside U read its first element instead
         float x[kTurns][8];
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int u = t * kSmallBlock + tid;
+            const int j = M.wide ? wide_j(u) : u / (MP / 8);
+            const int i = (M.wide ? wide_i(u) : u % (MP / 8)) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t o = M.wide ? static_cast<int64_t>(i + e) * M.cols + j0 + j
+                                         : static_cast<int64_t>(j0 + j) * M.cols + i + e;
+                x[t][e] = load_in<kF32>(M.in, j < rows && i + e < M.m ? o : 0);
+            }
+        }
         double s = 0.0;
 #pragma unroll
         for (int t = 0; t < kTurns; ++t) {
             const int u = t * kSmallBlock + tid;
-            const int j = M.wide ? u % NB : u / (MP / 8), i = (M.wide ? u / NB : u % (MP / 8)) * 8;
+            const int j = M.wide ? wide_j(u) : u / (MP / 8);
+            const int i = (M.wide ? wide_i(u) : u % (MP / 8)) * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const bool in = j < rows && i + e < M.m;
-                const int64_t o = M.wide ? static_cast<int64_t>(i + e) * M.cols + j0 + j
-                                         : static_cast<int64_t>(j0 + j) * M.cols + i + e;
-                x[t][e] = in ? load_in<kF32>(M.in, o) : 0.0f;
+                x[t][e] = j < rows && i + e < M.m ? x[t][e] : 0.0f;
                 s += static_cast<double>(x[t][e]) * x[t][e];
             }
         }
@@ -803,7 +818,8 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
 #pragma unroll
         for (int t = 0; t < kTurns; ++t) {
             const int u = t * kSmallBlock + tid;
-            const int j = M.wide ? u % NB : u / (MP / 8), i = (M.wide ? u / NB : u % (MP / 8)) * 8;
+            const int j = M.wide ? wide_j(u) : u / (MP / 8);
+            const int i = (M.wide ? wide_i(u) : u % (MP / 8)) * 8;
             if (j < rows32 && i < MP) {
                 Half8 h, l;
 #pragma unroll
@@ -955,7 +971,7 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
         const float ca = ldexpf(c.a, kLogA), cb = ldexpf(rho, -kLogA);
         // up to 64 rows B's operands stay in registers
         constexpr bool kHeld = MP <= 64;
-        f16x8 ph[kHeld ? nb : 1][MP / 32], pl[kHeld ? nb : 1][MP / 32];
+        f16x8 ph[kHeld ? nb : 1][kHeld ? MP / 32 : 1], pl[kHeld ? nb : 1][kHeld ? MP / 32 : 1];
         if constexpr (kHeld) {
 #pragma unroll
             for (int x = 0; x < nb; ++x)
@@ -965,6 +981,8 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
                     pl[x][q] = small_rows(al, MP, x * 16, q * 32, lane);
                 }
         }
+        // a tall matrix's fours of a row in one store where they lie at 8 bytes
+        const bool quads = !M.wide && (M.cols & 3) == 0 && (lo32(M.out) & 7u) == 0;
         // with 128 rows two waves share 16 columns, half of the rows each
         constexpr int kSide = kHeld ? 1 : 2, kX = nb / kSide;
         const int x0 = kHeld ? 0 : (wave & 1) * kX;
@@ -978,36 +996,71 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
             }
             if constexpr (!kHeld) __syncthreads();      // both have read them
             const int j = r + (lane & 15);
+            // kAt blocks of rows at a time, whose products do not wait for each other: all
+            // of them, or one where the registers hold no more beside the column's
+            constexpr int kAt = kHeld ? kX : 1;
 #pragma unroll
-            for (int y = 0; y < kX; ++y) {
-                if (!kHeld && r >= rows) break;
-                const int x = kHeld ? y : x0 + y;
-                const int o = small_at(NB, j, x * 16 + 4 * g);
-                const f16x4 xh = *(lds_f16x4 *)(th + o), xl = *(lds_f16x4 *)(tlo + o);
-                f32x4 v;
+            for (int xs = 0; xs < kX; xs += kAt) {
+                f32x4 v[kAt];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = ca * (static_cast<float>(xh[e]) + static_cast<float>(xl[e]));
+                for (int y = 0; y < kAt; ++y) {
+                    const int o = small_at(NB, j, (x0 + xs + y) * 16 + 4 * g);
+                    const f16x4 xh = *(lds_f16x4 *)(th + o), xl = *(lds_f16x4 *)(tlo + o);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[y][e] = ca * (static_cast<float>(xh[e]) + static_cast<float>(xl[e]));
+                }
 #pragma unroll
                 for (int q = 0; q < MP / 32; ++q) {
-                    if constexpr (!kHeld) {
-                        ph[0][q] = small_rows(ah, MP, x * 16, q * 32, lane);
-                        pl[0][q] = small_rows(al, MP, x * 16, q * 32, lane);
-                    }
-                    v = fine_product(ph[kHeld ? x : 0][q], pl[kHeld ? x : 0][q], qh[q], ql[q], v);
-                }
-                float w[4];
+                    f16x8 h[kAt], l[kAt];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = cb * v[e];
+                    for (int y = 0; y < kAt; ++y) {
+                        if constexpr (kHeld) {
+                            h[y] = ph[xs + y][q];
+                            l[y] = pl[xs + y][q];
+                        } else {
+                            h[y] = small_rows(ah, MP, (x0 + xs + y) * 16, q * 32, lane);
+                            l[y] = small_rows(al, MP, (x0 + xs + y) * 16, q * 32, lane);
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < kAt; ++y)
+                        v[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[y], ql[q], v[y], 0, 0, 0);
+#pragma unroll
+                    for (int y = 0; y < kAt; ++y)
+                        v[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(l[y], qh[q], v[y], 0, 0, 0);
+#pragma unroll
+                    for (int y = 0; y < kAt; ++y)
+                        v[y] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[y], qh[q], v[y], 0, 0, 0);
+                }
                 if (!last) {
-                    put_split(th, tlo, o, w);
+                    if (kHeld || r < rows) {
+#pragma unroll
+                        for (int y = 0; y < kAt; ++y) {
+                            const float w[4] = {cb * v[y].x, cb * v[y].y, cb * v[y].z, cb * v[y].w};
+                            put_split(th, tlo, small_at(NB, j, (x0 + xs + y) * 16 + 4 * g), w);
+                        }
+                    }
                 } else if (j < rows) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = x * 16 + 4 * g + e;
-                        const int64_t at = M.wide ? static_cast<int64_t>(i) * M.cols + j0 + j
-                                                  : static_cast<int64_t>(j0 + j) * M.cols + i;
-                        if (i < M.m) M.out[at] = static_cast<uint16_t>(bf16_rne(w[e] * sc.phi));
+                    for (int y = 0; y < kAt; ++y) {
+                        const int i = (x0 + xs + y) * 16 + 4 * g;
+                        uint16_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = static_cast<uint16_t>(bf16_rne(cb * v[y][e] * sc.phi));
+                        uint16_t *at = M.out + (M.wide ? static_cast<int64_t>(i) * M.cols + j0 + j
+                                                       : static_cast<int64_t>(j0 + j) * M.cols + i);
+                        if (quads && i < M.m) {
+                            *reinterpret_cast<u32x2 *>(at) =
+                                u32x2{static_cast<uint32_t>(w[0]) | (static_cast<uint32_t>(w[1]) << 16),
+                                      static_cast<uint32_t>(w[2]) | (static_cast<uint32_t>(w[3]) << 16)};
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (i + e < M.m)
+                                    at[e * (M.wide ? static_cast<int64_t>(M.cols) : 1)] = w[e];
+                        }
                     }
                 }
             }
