@@ -57,6 +57,11 @@ __device__ __forceinline__ float settled(float x) {
     return x;
 }
 
+// To nearest even, by the instruction: no branch for NaN.
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+}
+
 // Element (row, col) of a matrix in panels of 32 columns with `rows` rows.
 __device__ __forceinline__ int64_t panel_at(int rows, int row, int col) {
     return (static_cast<int64_t>(col >> 5) * rows + row) * 32 + (col & 31);
@@ -623,7 +628,7 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[b].s[e] = static_cast<short>(bf16_rne(t[e] * sc.phi));
+                        v[b].s[e] = static_cast<short>(to_bf16(t[e] * sc.phi));
                 }
             }
             // the block turned over, through 2 KB of LDS: row ib + (lane & 31), its
@@ -697,30 +702,47 @@ struct Small {
     static constexpr int kLds = 2 * kT + 2 * kA + (MP == 128 ? 0 : kWaves * 4096);
 };
 
-// Element (row, col .. + 4 or 8) in LDS panels of 32 columns with `rows` rows;
-// the halves of a row change places in every other eight rows, for the reads
-// along rows and for the transposing ones alike.
+// Element (row, col .. + 4 or 8) in LDS panels of 32 columns with `rows` rows; a
+// row's 16-byte chunk sits at its index xor a number that the row's place among
+// four fours gives: 0, 2, 1, 3.  Reads along rows of 16 bytes a lane, the products'
+// results of 8 bytes in 16 rows and the transposing reads below all hit 64 banks
+// then (with 0, 0, 2, 2 the results took 16 LDS cycles for 4: 37 % of all).
 __device__ __forceinline__ int small_at(int rows, int row, int col) {
-    return (col >> 5) * rows * 64 + row * 64 + ((((col >> 3) & 3) ^ (((row >> 3) & 1) << 1)) * 16) +
-           (col & 7) * 2;
+    return (col >> 5) * rows * 64 + row * 64 +
+           ((((col >> 3) & 3) ^ (-(row >> 2) & 3)) * 16) + (col & 7) * 2;
+}
+
+// Of the rows from row0, a multiple of 16, and the panel of column col0: what all
+// lanes add to the place of a row and a column counted from there.
+__device__ __forceinline__ int small_block(int rows, int row0, int col0) {
+    return (col0 >> 5) * rows * 64 + row0 * 64;
+}
+
+// Place of this lane's four of a result: rows row0 .. + 16, columns col0 .. + 16.
+__device__ __forceinline__ int small_four(int rows, int row0, int col0, int lane) {
+    return small_block(rows, row0, col0) +
+           small_at(rows, lane & 15, (col0 & 16) + 4 * (lane >> 4));
 }
 
 // Operand: 16 rows from row0, 32 columns from col0.
 __device__ __forceinline__ f16x8 small_rows(const lds_char *t, int rows, int row0, int col0,
                                             int lane) {
-    return *(const lds_f16x8 *)(t + small_at(rows, row0 + (lane & 15), col0 + 8 * (lane >> 4)));
+    return *(const lds_f16x8 *)(t + small_block(rows, row0, col0) +
+                                small_at(rows, lane & 15, 8 * (lane >> 4)));
 }
 
-// Operand: 16 columns from col0, 32 rows (the sum) from row0.
+// Operand: 16 columns from col0, 32 rows (the sum) from row0.  The sum's order is
+// free as long as both operands have it: lanes 16 g .. + 16 take fours 0, 1, 4, 5
+// of the rows and then fours 2, 3, 6, 7, so that two of them hit all banks.
 __device__ __forceinline__ f16x8 small_cols(lds_char *t, int rows, int row0, int col0, int lane) {
-    const int k = row0 + (lane >> 4) * 8 + ((lane >> 2) & 3);
-    lds_char *at = t + small_at(rows, k, col0 + (lane & 3) * 4);
+    const int k = (lane >> 4) * 8 + ((lane >> 2) & 3), col = (col0 & 16) + (lane & 3) * 4;
+    t += small_block(rows, row0, col0);
     union {
         s16x4 s[2];
         f16x8 v;
     } u;
-    u.s[0] = read_tr(at);
-    u.s[1] = read_tr(at + 4 * 64);
+    u.s[0] = read_tr(t + small_at(rows, k, col));
+    u.s[1] = read_tr(t + small_at(rows, k + 4, col));
     return u.v;
 }
 
@@ -732,16 +754,17 @@ __device__ __forceinline__ f32x4 fine_product(f16x8 ph, f16x8 pl, f16x8 qh, f16x
 }
 
 // Four neighbouring values as high and low parts at byte offset o of hi and lo.
-__device__ __forceinline__ void put_split(lds_char *hi, lds_char *lo, int o, const float (&x)[4]) {
-    f16x4 h, l;
+// (A factor that the compiler does not see the value of: the differences are then
+// one instruction each that reads the half itself.)
+__device__ __forceinline__ void put_split(lds_char *hi, lds_char *lo, int o, f32x4 x) {
+    const float minus = settled(-1.0f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float f = settled(x[e]);
-        h[e] = static_cast<_Float16>(f);
-        l[e] = static_cast<_Float16>(f - static_cast<float>(h[e]));
-    }
+    for (int e = 0; e < 4; ++e) x[e] = settled(x[e]);
+    const f16x4 h = __builtin_convertvector(x, f16x4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(static_cast<float>(h[e]), minus, x[e]);
     *(lds_f16x4 *)(hi + o) = h;
-    *(lds_f16x4 *)(lo + o) = l;
+    *(lds_f16x4 *)(lo + o) = __builtin_convertvector(x, f16x4);
 }
 
 template <int MP, bool kF32>
@@ -930,13 +953,13 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
         const float phi = k == 0 ? sc.phi0 : sc.phi, rho = k == 0 ? sc.rho : 1.0f;
         // A, scaled, as operands: rows bj 16 + (lane & 15) (A is symmetric), columns bi 16 + 4 g ..
         const float alpha = ldexpf(phi * phi, kLogA);
-        float av[kBJ][4];
+        f32x4 av[kBJ];
         if (mine) {
 #pragma unroll
             for (int y = 0; y < kBJ; ++y) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) av[y][e] = alpha * a[y][e];
-                put_split(ah, al, small_at(MP, (bj0 + y) * 16 + (lane & 15), bi * 16 + 4 * g), av[y]);
+                put_split(ah, al, small_four(MP, (bj0 + y) * 16, bi * 16, lane), av[y]);
             }
         }
         __syncthreads();
@@ -959,10 +982,10 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
             const float cc = ldexpf(c.c, -kLogA);
 #pragma unroll
             for (int y = 0; y < kBJ; ++y) {
-                float v[4];
+                f32x4 v;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = c.b * av[y][e] + cc * b[y][e];
-                put_split(ah, al, small_at(MP, (bj0 + y) * 16 + (lane & 15), bi * 16 + 4 * g), v);
+                put_split(ah, al, small_four(MP, (bj0 + y) * 16, bi * 16, lane), v);
             }
         }
         __syncthreads();
@@ -1004,11 +1027,13 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
                 f32x4 v[kAt];
 #pragma unroll
                 for (int y = 0; y < kAt; ++y) {
-                    const int o = small_at(NB, j, (x0 + xs + y) * 16 + 4 * g);
+                    const int o = small_four(NB, r, (x0 + xs + y) * 16, lane);
                     const f16x4 xh = *(lds_f16x4 *)(th + o), xl = *(lds_f16x4 *)(tlo + o);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        v[y][e] = ca * (static_cast<float>(xh[e]) + static_cast<float>(xl[e]));
+                        v[y][e] = __builtin_fmaf(
+                            static_cast<float>(xh[e]), ca,
+                            __builtin_fmaf(static_cast<float>(xl[e]), ca, 0.0f));
                 }
 #pragma unroll
                 for (int q = 0; q < MP / 32; ++q) {
@@ -1037,18 +1062,22 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
                     if (kHeld || r < rows) {
 #pragma unroll
                         for (int y = 0; y < kAt; ++y) {
-                            const float w[4] = {cb * v[y].x, cb * v[y].y, cb * v[y].z, cb * v[y].w};
-                            put_split(th, tlo, small_at(NB, j, (x0 + xs + y) * 16 + 4 * g), w);
+                            f32x4 w;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = cb * v[y][e];
+                            put_split(th, tlo, small_four(NB, r, (x0 + xs + y) * 16, lane), w);
                         }
                     }
                 } else if (j < rows) {
 #pragma unroll
                     for (int y = 0; y < kAt; ++y) {
-                        const int i = (x0 + xs + y) * 16 + 4 * g;
+                        // (not known before: no addresses kept through all iterations)
+                        int i = (x0 + xs + y) * 16 + 4 * g;
+                        asm volatile("" : "+v"(i));
                         uint16_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            w[e] = static_cast<uint16_t>(bf16_rne(cb * v[y][e] * sc.phi));
+                            w[e] = to_bf16(cb * v[y][e] * sc.phi);
                         uint16_t *at = M.out + (M.wide ? static_cast<int64_t>(i) * M.cols + j0 + j
                                                        : static_cast<int64_t>(j0 + j) * M.cols + i);
                         if (quads && i < M.m) {
