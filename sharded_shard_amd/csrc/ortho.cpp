@@ -182,7 +182,7 @@ template <typename F>
 bool few_rows(int32_t id, fsdp::OrthoMat *M, fsdp_ortho_plan *p, F &&take) {
     const int cls = M->mp == 32 ? 0 : M->mp == 64 ? 1 : 2;
     const int32_t nb = fsdp::small_slab(M->mp);
-    const int64_t part = static_cast<int64_t>(M->mp) * M->mp * 4;
+    const int64_t part = static_cast<int64_t>(fsdp::small_part(M->mp)) * 16;
     M->slab = nb;
     if (M->n <= nb) {
         p->one[cls].push_back({id, 0, 0, 0});

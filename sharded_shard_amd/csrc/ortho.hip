@@ -693,11 +693,18 @@ struct Small {
     // with 128 rows the work of one block of threads is long: 16 waves (58 -> 54 us
     // for a 128 x 128 matrix, 326 -> 277 for 32 of 128 x 2048)
     static constexpr int kThreads = MP == 128 ? 1024 : 512, kWaves = kThreads / 64;
-    // blocks of A and B that one wave has: of its row of blocks, bj0 .. + kBJ
+    // 16 x 16 blocks of A and B that one wave has
     static constexpr int kBJ = MP == 128 ? 4 : MP == 64 ? 2 : 1;
     // up to 64 rows a wave sums 32 x 32 of A over one stretch in kStretches
     static constexpr int kStretches = MP == 32 ? 8 : MP == 64 ? 2 : 1;
-    static constexpr int kT = NB * MP * 2, kA = MP * MP * 2;     // bytes of one part in LDS
+    static constexpr int kImage = NB * MP * 2;          // bytes of one part of X
+    // in LDS the low part lies half of the banks further than the high one, so that
+    // a lane's 8 bytes of either, one instruction, are not in the same banks
+    static constexpr int kT = kImage + 128, kA = MP * MP * 2 + 128;
+    // With 128 rows a wave has 32 x 32 of the upper half of A and B, which are
+    // symmetric: ten waves, and the reads of LDS, which bound it, are half of those
+    // of 16 waves with 16 x 64 of all (128 x 128: 43.8 -> 40.6 us).
+    static constexpr bool kUpper = MP == 128;
     // those sums have LDS of their own: no barrier before A takes their place
     static constexpr int kLds = 2 * kT + 2 * kA + (MP == 128 ? 0 : kWaves * 4096);
 };
@@ -780,12 +787,32 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
 
     const OrthoTile tl = tiles[blockIdx.x];
     const OrthoMat M = mats[tl.mat];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
+    const int tid = threadIdx.x;
+    int lane = tid & 63;
+    // nothing that follows from the lane is kept from one phase to the next: all their
+    // addresses together do not fit the registers of 16 waves
+    auto phase = [&]() {
+        if constexpr (MP == 128) asm volatile("" : "+v"(lane));
+    };
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slab = tl.ti, j0 = slab * M.slab;
     const int rows = M.n - j0 < M.slab ? M.n - j0 : M.slab, rows32 = (rows + 31) & ~31;
-    // this wave's blocks of A and B
-    const int bi = MP == 32 ? (wave >> 1) & 1 : wave >> 1, bj0 = (wave & 1) * kBJ;
-    char *image = at(ws, M.t[0]) + static_cast<int64_t>(slab) * 2 * S::kT;
+    // This wave's blocks of A and B, number y: block row bi + (y >> 1) and block column
+    // bj + (y & 1) of the upper half's 32 x 32, otherwise bi and bj + y.
+    int bi, bj;
+    if constexpr (S::kUpper) {
+        // 0 .. 9: rows 0 0 0 0 1 1 1 2 2 3, columns 0 1 2 3 1 2 3 2 3 3
+        const int r = (wave >= 4) + (wave >= 7) + (wave >= 9);
+        bi = 2 * r;
+        bj = 2 * (wave - r * (7 - r) / 2);
+    } else {
+        bi = MP == 32 ? (wave >> 1) & 1 : wave >> 1;
+        bj = (wave & 1) * kBJ;
+    }
+    auto row_of = [&](int y) { return (S::kUpper ? bi + (y >> 1) : bi) * 16; };
+    auto col_of = [&](int y) { return (S::kUpper ? bj + (y & 1) : bj + y) * 16; };
+    const bool mine = S::kUpper ? wave < 10 : MP > 32 || wave < 4;
+    char *image = at(ws, M.t[0]) + static_cast<int64_t>(slab) * 2 * S::kImage;
 
     OrthoScal sc;
     if (mode == kSmallAll || mode == kSmallStart) {
@@ -865,7 +892,7 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
                 *reinterpret_cast<u32x4 *>(smem + at16) =
                     *reinterpret_cast<const u32x4 *>(image + at16);
                 *reinterpret_cast<u32x4 *>(smem + S::kT + at16) =
-                    *reinterpret_cast<const u32x4 *>(image + S::kT + at16);
+                    *reinterpret_cast<const u32x4 *>(image + S::kImage + at16);
             }
     }
     __syncthreads();
@@ -905,7 +932,7 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
             // the stretches in order
 #pragma unroll
             for (int y = 0; y < kBJ; ++y) {
-                const int bj = bj0 + y, of = (bi >> 1) * 2 + (bj >> 1), sub = (bi & 1) * 2 + (bj & 1);
+                const int k = bj + y, of = (bi >> 1) * 2 + (k >> 1), sub = (bi & 1) * 2 + (k & 1);
                 a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int t = 0; t < S::kStretches; ++t)
@@ -915,43 +942,70 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
         } else {
 #pragma unroll
             for (int y = 0; y < kBJ; ++y) a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (!mine) return;
             for (int r = 0; r < rows32; r += 32) {
-                const f16x8 ph = small_cols(th, NB, r, bi * 16, lane);
-                const f16x8 pl = small_cols(tlo, NB, r, bi * 16, lane);
+                f16x8 ph[2], pl[2], qh[2], ql[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    ph[x] = small_cols(th, NB, r, (bi + x) * 16, lane);
+                    pl[x] = small_cols(tlo, NB, r, (bi + x) * 16, lane);
+                    qh[x] = small_cols(th, NB, r, (bj + x) * 16, lane);
+                    ql[x] = small_cols(tlo, NB, r, (bj + x) * 16, lane);
+                }
 #pragma unroll
                 for (int y = 0; y < kBJ; ++y)
-                    a[y] = fine_product(ph, pl, small_cols(th, NB, r, (bj0 + y) * 16, lane),
-                                        small_cols(tlo, NB, r, (bj0 + y) * 16, lane), a[y]);
+                    a[y] = fine_product(ph[y >> 1], pl[y >> 1], qh[y & 1], ql[y & 1], a[y]);
             }
         }
     };
     // parts of A: one 16 x 16 block after the other, a lane's four values together
+    constexpr int kPart = small_part(MP);
     auto part = [&](int k, int y) {
-        return reinterpret_cast<f32x4 *>(at(ws, (k & 1) ? M.b : M.a)) + (bi * nb + bj0 + y) * 64 +
-               lane;
+        return reinterpret_cast<f32x4 *>(at(ws, (k & 1) ? M.b : M.a)) +
+               (S::kUpper ? wave * 4 + y : bi * nb + bj + y) * 64 + lane;
     };
-    const bool mine = MP > 32 || wave < 4;
+    // this wave's blocks, in t by rows of the second index, to their other half
+    auto mirror = [&](lds_char *t) {
+        if constexpr (S::kUpper) {
+            if (bi == bj) return;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                *(lds_f16x8 *)(t + small_block(MP, (bi + x) * 16, bj * 16) +
+                               small_at(MP, lane & 15, 8 * (lane >> 4))) =
+                    small_cols(t, MP, bj * 16, (bi + x) * 16, lane);
+        }
+    };
     if (mode == kSmallAll || mode == kSmallStart) gram();
     if (mode == kSmallStart && mine) {
 #pragma unroll
-        for (int y = 0; y < kBJ; ++y) part(0, y)[static_cast<int64_t>(slab) * MP * MP / 4] = a[y];
+        for (int y = 0; y < kBJ; ++y) part(0, y)[static_cast<int64_t>(slab) * kPart] = a[y];
     }
     const int from = mode == kSmallAll ? 0 : step;
     const int to = mode == kSmallAll ? n_steps : mode == kSmallStart ? 0 : step + 1;
     for (int k = from; k < to; ++k) {
         const OrthoCoef c = coefs[k];
+        phase();
         if (mode != kSmallAll && mine) {
-            // the parts' sum, in order
+            // the parts' sum, in order; eight loads of a lane under way
+            constexpr int kAhead = 8 / kBJ;
 #pragma unroll
-            for (int y = 0; y < kBJ; ++y) {
-                const f32x4 *p = part(k, y);
-                a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-                for (int t = 0; t < M.n_sums; ++t) a[y] += p[static_cast<int64_t>(t) * MP * MP / 4];
+            for (int y = 0; y < kBJ; ++y) a[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int t = 0; t < M.n_sums; t += kAhead) {
+                f32x4 v[kAhead][kBJ];
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+                    for (int y = 0; y < kBJ; ++y)
+                        v[x][y] = part(k, y)[static_cast<int64_t>(t + x < M.n_sums ? t + x : t) * kPart];
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x)
+#pragma unroll
+                    for (int y = 0; y < kBJ; ++y)
+                        if (t + x < M.n_sums) a[y] += v[x][y];
             }
         }
         const float phi = k == 0 ? sc.phi0 : sc.phi, rho = k == 0 ? sc.rho : 1.0f;
-        // A, scaled, as operands: rows bj 16 + (lane & 15) (A is symmetric), columns bi 16 + 4 g ..
+        // A, scaled, as operands: a block's four rows a lane as columns (A is symmetric)
         const float alpha = ldexpf(phi * phi, kLogA);
         f32x4 av[kBJ];
         if (mine) {
@@ -959,8 +1013,10 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
             for (int y = 0; y < kBJ; ++y) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) av[y][e] = alpha * a[y][e];
-                put_split(ah, al, small_four(MP, (bj0 + y) * 16, bi * 16, lane), av[y]);
+                put_split(ah, al, small_four(MP, col_of(y), row_of(y), lane), av[y]);
             }
+            mirror(ah);
+            mirror(al);
         }
         __syncthreads();
         f32x4 b[kBJ];
@@ -969,12 +1025,21 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
             for (int y = 0; y < kBJ; ++y) b[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < MP; q += 32) {
-                const f16x8 ph = small_rows(ah, MP, bi * 16, q, lane);
-                const f16x8 pl = small_rows(al, MP, bi * 16, q, lane);
+                constexpr int kP = S::kUpper ? 2 : 1, kQ = kBJ / kP;
+                f16x8 ph[kP], pl[kP], qh[kQ], ql[kQ];
+#pragma unroll
+                for (int x = 0; x < kP; ++x) {
+                    ph[x] = small_rows(ah, MP, (bi + x) * 16, q, lane);
+                    pl[x] = small_rows(al, MP, (bi + x) * 16, q, lane);
+                }
+#pragma unroll
+                for (int x = 0; x < kQ; ++x) {
+                    qh[x] = small_rows(ah, MP, (bj + x) * 16, q, lane);
+                    ql[x] = small_rows(al, MP, (bj + x) * 16, q, lane);
+                }
 #pragma unroll
                 for (int y = 0; y < kBJ; ++y)
-                    b[y] = fine_product(ph, pl, small_rows(ah, MP, (bj0 + y) * 16, q, lane),
-                                        small_rows(al, MP, (bj0 + y) * 16, q, lane), b[y]);
+                    b[y] = fine_product(ph[y / kQ], pl[y / kQ], qh[y % kQ], ql[y % kQ], b[y]);
             }
         }
         __syncthreads();
@@ -985,10 +1050,13 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
                 f32x4 v;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = c.b * av[y][e] + cc * b[y][e];
-                put_split(ah, al, small_four(MP, (bj0 + y) * 16, bi * 16, lane), v);
+                put_split(ah, al, small_four(MP, col_of(y), row_of(y), lane), v);
             }
+            mirror(ah);
+            mirror(al);
         }
         __syncthreads();
+        phase();
         // X = a X + B X: a wave takes 16 columns j at a time, which no other wave reads or writes
         const bool last = k + 1 == n_steps;
         const float ca = ldexpf(c.a, kLogA), cb = ldexpf(rho, -kLogA);
@@ -1071,9 +1139,7 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
                 } else if (j < rows) {
 #pragma unroll
                     for (int y = 0; y < kAt; ++y) {
-                        // (not known before: no addresses kept through all iterations)
-                        int i = (x0 + xs + y) * 16 + 4 * g;
-                        asm volatile("" : "+v"(i));
+                        const int i = (x0 + xs + y) * 16 + 4 * (lane >> 4);
                         uint16_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -1096,11 +1162,12 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
         }
         __syncthreads();
         if (last) break;
+        phase();
         gram();
         if (mode == kSmallStep && mine) {
 #pragma unroll
             for (int y = 0; y < kBJ; ++y)
-                part(k + 1, y)[static_cast<int64_t>(slab) * MP * MP / 4] = a[y];
+                part(k + 1, y)[static_cast<int64_t>(slab) * kPart] = a[y];
         }
     }
     if (mode == kSmallStart || mode == kSmallStep) {
@@ -1110,7 +1177,7 @@ __global__ __launch_bounds__(Small<MP>::kThreads) void ortho_small_kernel(
                 const int at16 = q * NB * 64 + o;
                 *reinterpret_cast<u32x4 *>(image + at16) =
                     *reinterpret_cast<const u32x4 *>(smem + at16);
-                *reinterpret_cast<u32x4 *>(image + S::kT + at16) =
+                *reinterpret_cast<u32x4 *>(image + S::kImage + at16) =
                     *reinterpret_cast<const u32x4 *>(smem + S::kT + at16);
             }
     }
@@ -1123,7 +1190,7 @@ __global__ __launch_bounds__(kBlock) void ortho_sums_kernel(const OrthoTile *__r
                                                             void *ws, int32_t step) {
     const OrthoTile tl = tiles[blockIdx.x];
     const OrthoMat M = mats[tl.mat];
-    const int64_t size = static_cast<int64_t>(M.mp) * M.mp / 4;
+    const int64_t size = small_part(M.mp);
     f32x4 *p = reinterpret_cast<f32x4 *>(at(ws, (step & 1) ? M.b : M.a)) + tl.ti * kBlock +
                threadIdx.x;
     f32x4 v = p[0];

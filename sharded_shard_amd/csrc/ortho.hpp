@@ -55,6 +55,8 @@ struct OrthoCoef {
 // 128 rows, worked on in slabs of so many columns.
 constexpr int32_t kSmallMax = 128;
 constexpr int32_t small_rows_of(int32_t m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
+// fours of a slab's part of X X^T: the upper 32 x 32 blocks of 128 rows, or all
+constexpr int32_t small_part(int32_t mp) { return mp == 128 ? 10 * 256 : mp * mp / 4; }
 constexpr int32_t small_slab(int32_t mp) { return mp == 128 ? 128 : mp == 64 ? 416 : 896; }
 // What a launch does: all steps (one slab), the start, one step, the last step.
 enum { kSmallAll = 0, kSmallStart = 1, kSmallStep = 2, kSmallLast = 3 };
