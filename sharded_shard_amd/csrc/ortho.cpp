@@ -110,8 +110,14 @@ void spread(std::vector<fsdp::OrthoTile> *tiles) {
     }
 }
 
-// Bytes of parts of A that a block sums by itself.
-constexpr int64_t kSumsInBlock = 192 << 10;
+// Bytes of parts of A that a block sums by itself: more with few matrices, whose
+// blocks wait for a launch less, fewer with many, whose blocks all read them
+// (64 x 4096, 192 and 384 KB: one matrix 76 and 69 us, 8 87 and 82, 16 103 and 150).
+int64_t sums_in_block(const fsdp_ortho_plan &p) {
+    int32_t few = 0;
+    for (const fsdp::OrthoMat &M : p.mats) few += M.m <= fsdp::kSmallMax;
+    return few <= 8 ? 384 << 10 : 192 << 10;
+}
 
 // Tile sides and the parts of X X^T's sum: what a model of a launch's time says,
 // in clocks.  A CU takes `per` clocks for each element of a tile's sum, and a
@@ -179,7 +185,7 @@ void choose(fsdp_ortho_plan *p) {
 // A matrix of few rows: its slabs; true if it needs no norm of its own (one
 // slab: the block that works on it takes it).
 template <typename F>
-bool few_rows(int32_t id, fsdp::OrthoMat *M, fsdp_ortho_plan *p, F &&take) {
+bool few_rows(int32_t id, fsdp::OrthoMat *M, int64_t most, fsdp_ortho_plan *p, F &&take) {
     const int cls = M->mp == 32 ? 0 : M->mp == 64 ? 1 : 2;
     const int32_t nb = fsdp::small_slab(M->mp);
     const int64_t part = static_cast<int64_t>(fsdp::small_part(M->mp)) * 16;
@@ -190,7 +196,7 @@ bool few_rows(int32_t id, fsdp::OrthoMat *M, fsdp_ortho_plan *p, F &&take) {
     }
     // shorter slabs as long as every block can sum their parts by itself
     auto count = [&](int32_t slab) { return (M->n + slab - 1) / slab; };
-    while (M->slab > 128 && count(round_up(M->slab / 2, 32)) * part <= kSumsInBlock)
+    while (M->slab > 128 && count(round_up(M->slab / 2, 32)) * part <= most)
         M->slab = static_cast<int32_t>(round_up(M->slab / 2, 32));
     const int32_t slabs = count(M->slab);
     M->t[0] = take(static_cast<int64_t>(slabs) * nb * M->mp * 4);
@@ -198,7 +204,7 @@ bool few_rows(int32_t id, fsdp::OrthoMat *M, fsdp_ortho_plan *p, F &&take) {
     M->b = take(slabs * part);
     for (int32_t s = 0; s < slabs; ++s) p->slabs[cls].push_back({id, s, 0, 0});
     M->n_sums = slabs;
-    if (slabs * part > kSumsInBlock) {
+    if (slabs * part > most) {
         M->n_sums = 1;
         for (int32_t t = 0; t < part / 16 / 256; ++t) p->sums.push_back({id, t, slabs, 0});
     }
@@ -212,11 +218,12 @@ void layout(fsdp_ortho_plan *p) {
         off += round_up(bytes, 256);
         return at;
     };
+    const int64_t most = sums_in_block(*p);
     for (size_t i = 0; i < p->mats.size(); ++i) {
         fsdp::OrthoMat &M = p->mats[i];
         const int32_t id = static_cast<int32_t>(i);
         const int64_t total = static_cast<int64_t>(M.rows) * M.cols;
-        if (M.m <= fsdp::kSmallMax && few_rows(id, &M, p, take)) continue;
+        if (M.m <= fsdp::kSmallMax && few_rows(id, &M, most, p, take)) continue;
         M.n_parts = static_cast<int32_t>(std::max<int64_t>(
             1, std::min<int64_t>(fsdp::kOrthoParts, total / fsdp::kOrthoPartMin)));
         M.parts = take(M.n_parts * 8);

@@ -690,8 +690,8 @@ template <int MP>
 struct Small {
     static constexpr int NB = small_slab(MP);           // columns of a slab, at most
     static constexpr int nb = MP / 16;                  // 16 x 16 blocks a side
-    // with 128 rows the work of one block of threads is long: 16 waves (58 -> 54 us
-    // for a 128 x 128 matrix, 326 -> 277 for 32 of 128 x 2048)
+    // with 128 rows the work of one block of threads is long: 16 waves (with 8 a
+    // 128 x 128 matrix took 7 % longer, 32 of 128 x 2048 18 %)
     static constexpr int kThreads = MP == 128 ? 1024 : 512, kWaves = kThreads / 64;
     // 16 x 16 blocks of A and B that one wave has
     static constexpr int kBJ = MP == 128 ? 4 : MP == 64 ? 2 : 1;
@@ -711,9 +711,10 @@ struct Small {
 
 // Element (row, col .. + 4 or 8) in LDS panels of 32 columns with `rows` rows; a
 // row's 16-byte chunk sits at its index xor a number that the row's place among
-// four fours gives: 0, 2, 1, 3.  Reads along rows of 16 bytes a lane, the products'
-// results of 8 bytes in 16 rows and the transposing reads below all hit 64 banks
-// then (with 0, 0, 2, 2 the results took 16 LDS cycles for 4: 37 % of all).
+// four fours gives: 0, 3, 2, 1.  Reads along rows of 16 bytes a lane, the products'
+// results of 8 bytes in 16 rows and the transposing reads below all spread over the
+// 64 banks then (with 0, 0, 2, 2 a quarter of all LDS cycles were conflicts, with
+// 0, 2, 1, 3 those of the reads along rows).
 __device__ __forceinline__ int small_at(int rows, int row, int col) {
     return (col >> 5) * rows * 64 + row * 64 +
            ((((col >> 3) & 3) ^ (-(row >> 2) & 3)) * 16) + (col & 7) * 2;
@@ -738,9 +739,7 @@ __device__ __forceinline__ f16x8 small_rows(const lds_char *t, int rows, int row
                                 small_at(rows, lane & 15, 8 * (lane >> 4)));
 }
 
-// Operand: 16 columns from col0, 32 rows (the sum) from row0.  The sum's order is
-// free as long as both operands have it: lanes 16 g .. + 16 take fours 0, 1, 4, 5
-// of the rows and then fours 2, 3, 6, 7, so that two of them hit all banks.
+// Operand: 16 columns from col0, 32 rows (the sum) from row0.
 __device__ __forceinline__ f16x8 small_cols(lds_char *t, int rows, int row0, int col0, int lane) {
     const int k = (lane >> 4) * 8 + ((lane >> 2) & 3), col = (col0 & 16) + (lane & 3) * 4;
     t += small_block(rows, row0, col0);
