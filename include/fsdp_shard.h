@@ -586,7 +586,8 @@ fsdp_status fsdp_muon_reduce_momentum(const fsdp_plan *plan, const uint16_t *rs_
  *           the bound full tensors (every rank orthogonalised every matrix)
  *   ag_in   [S] bf16 copy-in as fsdp_pack_allgather writes it, or NULL for
  *           none; must not overlap upd, scales or the bound tensors
- *   scales  device array of n_params fp32 factors, or NULL for 1
+ *   scales  device array of n_params fp32 factors, or NULL for 1; must not
+ *           overlap the bound master shards
  * Needs FSDP_ROLE_MASTER, and FSDP_ROLE_FULL where upd is NULL.
  * Errors: FSDP_E_INVAL (null hparams, lr or weight_decay not finite, overlap),
  *         FSDP_E_ALIGN, FSDP_E_STATE, FSDP_E_HIP. */
@@ -649,6 +650,9 @@ fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *plan, const void *const *in, uint16
  *              workspace bytes; its contents need not be kept between calls.
  *              Executions that share a workspace must follow one another
  *              (one stream, or events between them)
+ * It does not synchronise and may be captured into a graph, whose replays read
+ * the plan's tables and the workspace: they work on what is bound at that
+ * time, and both must outlive them.
  * Errors: FSDP_E_INVAL (null plan; null, small or overlapping workspace),
  *         FSDP_E_ALIGN, FSDP_E_STATE (not bound, another device), FSDP_E_HIP. */
 fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *plan, void *workspace,

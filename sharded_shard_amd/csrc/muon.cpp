@@ -128,6 +128,9 @@ fsdp_status fsdp_muon_update(const fsdp_plan *p, const uint16_t *upd, uint16_t *
     if ((reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
         return set_error(FSDP_E_ALIGN, std::string(call) + ": scales not 4-byte aligned");
     const int64_t n_scales = static_cast<int64_t>(p->L.entries.size()) * 4;
+    if (scales != nullptr &&
+        (s = check_apart(p, scales, n_scales, FSDP_ROLE_MASTER, call, "scales")) != FSDP_OK)
+        return s;
     if (upd != nullptr) {
         if ((s = fsdp::check_segment(p, upd, call, "upd")) != FSDP_OK ||
             (s = check_apart(p, upd, segment_bytes(p), roles, call, "upd")) != FSDP_OK)

@@ -87,7 +87,12 @@ class Orthogonalizer:
 
     def execute(self, stream=None) -> None:
         if self.workspace is None:
-            self.allocate()
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream)
+            # of the stream that works in it: memory that torch frees on its current
+            # stream may still be written there
+            with torch.cuda.stream(stream):
+                self.allocate()
         capi.fsdp_ortho_execute(self.plan, self.workspace, stream=stream)
 
     def close(self) -> None:
@@ -296,7 +301,7 @@ class ShardedGroup:
                        eps: float = 1e-7, stream=None) -> Orthogonalizer:
         """An Orthogonalizer bound, in place, to the full matrices of ``params``
         (all by default; one rank's share where each rank works on its own)."""
-        idx = range(len(self.shapes)) if params is None else params
+        idx = range(len(self.shapes)) if params is None else list(params)
         o = Orthogonalizer([(self.rows[i], self.cols[i]) for i in idx], coeffs, eps)
         o.bind([self.full_view(i) for i in idx], stream=stream)
         return o

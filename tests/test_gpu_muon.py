@@ -272,6 +272,7 @@ def test_refusals_leave_the_state_alone():
             (E.FSDP_E_INVAL, lambda: g.muon_update(None, g.full_flat, 0.1, 0.0)),
             (E.FSDP_E_INVAL, lambda: g.muon_update(seg, None, float("inf"), 0.0)),
             (E.FSDP_E_ALIGN, lambda: g.muon_update(seg, None, 0.1, 0.0, scales=odd)),
+            (E.FSDP_E_INVAL, lambda: g.muon_update(seg, None, 0.1, 0.0, scales=g.master_flat)),
             (E.FSDP_E_ALIGN, lambda: g.muon_update(odd, None, 0.1, 0.0))):
         with pytest.raises(capi.FsdpError) as ei:
             call()

@@ -256,6 +256,39 @@ def test_refusals_on_the_device():
     o.close()
 
 
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_first_execution_on_another_stream_takes_memory_of_that_stream(as_handle):
+    """A block that torch freed on its current stream may still be in use there."""
+    u = matrix((300, 500), 1).to(DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with Orthogonalizer([(300, 500)]) as o:
+        o.bind([u], [torch.empty_like(u)])
+        torch.cuda.empty_cache()
+        freed = torch.empty(o.workspace_bytes, dtype=torch.uint8, device=DEV)
+        was = freed.data_ptr()
+        del freed
+        o.execute(stream=s.cuda_stream if as_handle else s)
+        assert o.workspace.data_ptr() != was
+        torch.cuda.synchronize()
+        first = o._bound[1][0].clone()
+        o.execute()
+        torch.cuda.synchronize()
+        assert torch.equal(first, o._bound[1][0])
+
+
+def test_parameters_of_a_group_from_any_iterable():
+    g = ShardedGroup([(8, 16), (12, 4)], 1, 0, optimizer="muon")
+    with g.orthogonalizer(i for i in (1, 0)) as o:
+        assert o.shapes == [(12, 4), (8, 16)]
+        o.execute()
+        torch.cuda.synchronize()
+    with pytest.raises(capi.FsdpError) as ei:        # the same matrix twice
+        g.orthogonalizer([0, 0])
+    assert ei.value.status == capi.FSDP_E_INVAL
+    g.close()
+
+
 def test_injected_launch_fault_reaches_the_caller(monkeypatch):
     u = matrix((8, 16), 0).to(DEV)
     with Orthogonalizer([(8, 16)]) as o:
