@@ -481,31 +481,47 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
 #pragma unroll
             for (int k = 0; k < kLoadsQ; ++k) fill_q(s, k);
         }
-        if constexpr (kSym) {
-#pragma unroll
-            for (int x = 0; x < FM; ++x)
-#pragma unroll
-                for (int y = 0; y < FN; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        } else {
-            // the sums start from a X, so that its loads overlap the first stages'
+        // Pair n of a X: two 16 x 16 blocks, rows 8 g .. + 8 of one column j a lane.
+        auto load_x = [&](int n, f16x8 &hi, f16x8 &lo) {
+            const int x = n / FN * 2, y = n % FN;
+            // of one panel, through its range: past the matrix, and of a low part
+            // that there is not, zeros
+            const int at32 = (i0 + wm * WTM) / 32 + x / 2;
+            const int j = j0 + wn * WTN + (y >> 1) * 32 + perm_row(lane & 15, y & 1);
+            const int64_t panel = static_cast<int64_t>(at32) * M.np * 64;
+            const uint32_t n32 = at32 < M.mp / 32 ? static_cast<uint32_t>(M.np) * 64u : 0u;
+            const uint32_t o = static_cast<uint32_t>(j) * 64u + 16u * g;
+            hi = __builtin_bit_cast(f16x8, bload16<0>(T + panel, o, n32));
+            lo = __builtin_bit_cast(
+                f16x8, bload16<0>(at(ws, M.lo) + panel, o, when & kHigh ? 0u : n32));
+        };
+        auto add_x = [&](int n, const f16x8 &hi, const f16x8 &lo) {
             const float ca = ldexpf(coef.a, kLogA);
+            const int x = n / FN * 2, y = n % FN;
 #pragma unroll
-            for (int x = 0; x < FM; x += 2)
+            for (int e = 0; e < 8; ++e)
+                acc[x + (e >> 2)][y][e & 3] +=
+                    ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e]));
+        };
+        // a X: where a CU has one block, whose loads of it nothing else covers, two pairs
+        // at a time in eight turns along the sum (two 1024 x 8192: 511 -> 490 us, a
+        // decoder block's 15.3 -> 15.1 ms); as the sums' start where blocks share a CU
+        // or the sum is short.  A border's wait counts the loads younger than a stage's;
+        // these between only make it longer.
+        constexpr int kPairs = FM / 2 * FN, kTurns = kPairs / 2;
+        constexpr bool kSpread = !kSym && BM == 256;
+        const bool spread = kSpread && steps >= 4 + 2 * kTurns;
 #pragma unroll
-                for (int y = 0; y < FN; ++y) {
-                    const int i = i0 + wm * WTM + x * 16 + 8 * g;
-                    const int j = j0 + wn * WTN + (y >> 1) * 32 + perm_row(lane & 15, y & 1);
-                    f16x8 hi{}, lo{};
-                    if (i < M.mp && j < M.np) {
-                        const int64_t o = panel_at(M.np, j, i) >> 3;
-                        hi = reinterpret_cast<const f16x8 *>(T)[o];
-                        if (!(when & kHigh)) lo = reinterpret_cast<const f16x8 *>(at(ws, M.lo))[o];
-                    }
+        for (int x = 0; x < FM; ++x)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[x + (e >> 2)][y][e & 3] =
-                            ca * (static_cast<float>(hi[e]) + static_cast<float>(lo[e]));
-                }
+            for (int y = 0; y < FN; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!kSym && !spread) {
+#pragma unroll
+            for (int n = 0; n < kPairs; ++n) {
+                f16x8 hi, lo;
+                load_x(n, hi, lo);
+                add_x(n, hi, lo);
+            }
         }
         border<0>();
 #pragma unroll
@@ -552,6 +568,24 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
         // loads younger than the next stage's: NST - 3 stages and this one's first
         constexpr Int<kLoads *(NST - 3) + kLoadsP> kWait{};
         int s = 0;
+        if constexpr (kSpread) {
+            if (spread) {
+#pragma unroll
+                for (int t = 0; t < kTurns; ++t) {
+                    f16x8 hi[2], lo[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) load_x(2 * t + k, hi[k], lo[k]);
+                    const int end = (steps - NST) / 2 * (t + 1) / kTurns * 2;
+                    do {
+                        stage(kWait, Int<2>{}, 0, s);
+                        stage(kWait, Int<2>{}, 1, s + 1);
+                        s += 2;
+                    } while (s < end);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) add_x(2 * t + k, hi[k], lo[k]);
+                }
+            }
+        }
         for (; s + NST < steps; s += 2) {
             stage(kWait, Int<2>{}, 0, s);
             stage(kWait, Int<2>{}, 1, s + 1);

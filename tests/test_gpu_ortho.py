@@ -171,6 +171,31 @@ def test_long_sum_and_offsets():
         close(run([u])[0], u)
 
 
+# counts at which a plan takes other tiles for its products: X X^T and A A in
+# 128, 192 and 256, B X in 128, 192 and 256 with its term a X before and along
+# the sum, X X^T in parts
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape,count", [((139, 140), 60), ((1040, 1037), 12), ((677, 680), 40),
+                                         ((257, 260), 60), ((440, 523), 40), ((797, 800), 16),
+                                         ((900, 7900), 2)], ids=str)
+def test_every_tile_with_edges(shape, count, dtype):
+    """One wide and one tall matrix, the others of the plan copies of them: equal
+    shapes and inputs give equal bits."""
+    r, c = shape
+    us = [matrix(shape, 11, "falling", dtype), matrix((c, r), 12, "noise", dtype)]
+    ins = [u.to(DEV) for u in us] * (count // 2)
+    outs = [torch.full(u.shape, 7.0, dtype=torch.bfloat16, device=DEV) for u in ins]
+    with Orthogonalizer([u.shape for u in ins]) as o:
+        o.bind(ins, outs)
+        o.allocate(torch.full((o.workspace_bytes,), 0xFF, dtype=torch.uint8, device=DEV))
+        o.execute()
+        torch.cuda.synchronize()
+    for u, x in zip(us, outs):
+        close(x, u)
+    for i, x in enumerate(outs):
+        assert torch.equal(x, outs[i % 2]), i
+
+
 def test_captured_execution_replays_like_an_eager_one():
     shapes = [(150, 260), (20, 30), (260, 150)]
     mats = [matrix(s, i, "falling").to(DEV) for i, s in enumerate(shapes)]
