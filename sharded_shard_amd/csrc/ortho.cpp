@@ -237,8 +237,9 @@ void layout(fsdp_ortho_plan *p) {
         M.lo = take(x);
         M.a = take(s);
         M.b = take(s);
-        for (int32_t j = 0; j < M.np / 64; ++j)
-            for (int32_t k = 0; k < M.mp / 64; ++k) p->init.push_back({id, k, j, 0});
+        for (int32_t j = 0; j < M.np / 64; j += fsdp::kInitPieces)
+            for (int32_t k = 0; k < M.mp / 64; ++k)
+                p->init.push_back({id, k, j, std::min(fsdp::kInitPieces, M.np / 64 - j)});
     }
     choose(p);
     // the matrices with the longest sums first, so that short tiles come last

@@ -179,38 +179,51 @@ __device__ __forceinline__ OrthoScal scalars(double norm, double eps, int32_t gr
     return s;
 }
 
-// X^T's 64 x 64 piece (rows 64 tj of n, columns 64 ti of m), eight neighbouring
-// values a thread and turn: of a tall U as they lie, of a wide one turned over in
-// LDS.  A bf16 input times 2^k is an fp16 value but for what lies under 2^-26 of
-// the norm (2^-37 of the norm at most is lost there); an fp32 input leaves a low
-// part.
+// Four rows of 16 columns: lane l of a 16-lane group reads 4 neighbouring
+// columns (8 bytes at t) of row l >> 2, and gets column l of the 16 that lanes
+// 0 to 3 read, of those 4 rows.  (restrict: with aliasing facts on the read the
+// compiler does not wait for every load to LDS that is under way before it;
+// the borders wait for those that matter.)
+__device__ __forceinline__ s16x4 read_tr(lds_char *__restrict__ t) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)t);
+}
+
+// X^T's 64 x 64 pieces tj .. + part of n for piece ti of m, one after the other, the
+// next one's values under way: the norm's parts are summed once for all of them.
+// Eight neighbouring values a thread and turn: of a tall U as they lie, of a wide one
+// turned over by transposing LDS reads.  A bf16 input times 2^k is an fp16 value but
+// for what lies under 2^-26 of the norm (2^-37 of the norm at most is lost there);
+// an fp32 input leaves a low part.
 template <bool kF32>
 __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__restrict__ tiles,
                                                             const OrthoMat *__restrict__ mats,
                                                             void *ws, double eps, int32_t growth) {
-    constexpr int kParts = kF32 ? 2 : 1;
-    // rows of 64 halves and 8 more: a turned row's reads start in other banks
-    __shared__ __attribute__((aligned(16))) _Float16 buf[kParts][64][72];
+    constexpr int kParts = kF32 ? 2 : 1, kPitch = 72;
+    // two pieces in turn: one barrier a piece
+    __shared__ __attribute__((aligned(16))) _Float16 buf[2][kParts][64 * kPitch];
     const OrthoTile tl = tiles[blockIdx.x];
     const OrthoMat M = mats[tl.mat];
-    const int r0 = (M.wide ? tl.ti : tl.tj) * 64, c0 = (M.wide ? tl.tj : tl.ti) * 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const bool vec = (lo32(M.in) & 15u) == 0 && (M.cols & 7) == 0;
-    // the values leave before the norm's parts are summed
     float x[2][8];
+    auto load = [&](int piece) {
+        const int r0 = (M.wide ? tl.ti : piece) * 64, c0 = (M.wide ? piece : tl.ti) * 64;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int u = t * kBlock + threadIdx.x, r = r0 + (u >> 3), c = c0 + (u & 7) * 8;
-        const int64_t o = static_cast<int64_t>(r) * M.cols + c;
+        for (int t = 0; t < 2; ++t) {
+            const int u = t * kBlock + threadIdx.x, r = r0 + (u >> 3), c = c0 + (u & 7) * 8;
+            const int64_t o = static_cast<int64_t>(r) * M.cols + c;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[t][e] = 0.0f;
-        if (r < M.rows && c + 8 <= M.cols) {
-            load_in8<kF32>(M.in, o, vec, x[t]);
-        } else if (r < M.rows) {
+            for (int e = 0; e < 8; ++e) x[t][e] = 0.0f;
+            if (r < M.rows && c + 8 <= M.cols) {
+                load_in8<kF32>(M.in, o, vec, x[t]);
+            } else if (r < M.rows) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < M.cols) x[t][e] = load_in<kF32>(M.in, o + e);
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < M.cols) x[t][e] = load_in<kF32>(M.in, o + e);
+            }
         }
-    }
+    };
+    load(tl.tj);
     const double *parts = reinterpret_cast<const double *>(at(ws, M.parts));
     double s = 0.0;
     for (int i = threadIdx.x; i < M.n_parts; i += kBlock) s += parts[i];
@@ -222,40 +235,52 @@ __global__ __launch_bounds__(kBlock) void ortho_init_kernel(const OrthoTile *__r
         *reinterpret_cast<OrthoScal *>(at(ws, M.scal)) = sc;
     f16x8 *hi = reinterpret_cast<f16x8 *>(at(ws, M.t[0]));
     f16x8 *lo = reinterpret_cast<f16x8 *>(at(ws, M.lo));
+    for (int piece = tl.tj; piece < tl.tj + tl.part; ++piece) {
+        f16x8 h[2], l[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int u = t * kBlock + threadIdx.x, y = u >> 3, c = (u & 7) * 8;
-        f16x8 h, l;
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float f = fine ? settled(ldexpf(x[t][e], k)) : 0.0f;
-            h[e] = static_cast<_Float16>(f);
-            l[e] = static_cast<_Float16>(f - static_cast<float>(h[e]));
+            for (int e = 0; e < 8; ++e) {
+                const float f = fine ? settled(ldexpf(x[t][e], k)) : 0.0f;
+                h[t][e] = static_cast<_Float16>(f);
+                l[t][e] = static_cast<_Float16>(f - static_cast<float>(h[t][e]));
+            }
+        if (piece + 1 < tl.tj + tl.part) load(piece + 1);
+        if (!M.wide) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int u = t * kBlock + threadIdx.x, y = u >> 3, c = (u & 7) * 8;
+                const int64_t o = panel_at(M.np, piece * 64 + y, tl.ti * 64 + c) >> 3;
+                hi[o] = h[t];
+                if constexpr (kF32) lo[o] = l[t];
+            }
+            continue;
         }
-        if (M.wide) {
-            *reinterpret_cast<f16x8 *>(&buf[0][y][c]) = h;
-            if constexpr (kF32) *reinterpret_cast<f16x8 *>(&buf[kParts - 1][y][c]) = l;
-        } else {
-            const int64_t o = panel_at(M.np, tl.tj * 64 + y, tl.ti * 64 + c) >> 3;
-            hi[o] = h;
-            if constexpr (kF32) lo[o] = l;
+        _Float16(&now)[kParts][64 * kPitch] = buf[piece & 1];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int u = t * kBlock + threadIdx.x, o = (u >> 3) * kPitch + (u & 7) * 8;
+            *reinterpret_cast<f16x8 *>(&now[0][o]) = h[t];
+            if constexpr (kF32) *reinterpret_cast<f16x8 *>(&now[kParts - 1][o]) = l[t];
         }
-    }
-    if (!M.wide) return;
-    __syncthreads();
+        __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        // row y of X^T, its columns c .. + 8; a wave's lanes take 64 rows
-        const int u = t * kBlock + threadIdx.x, y = u & 63, c = (u >> 6) * 8;
-        const int64_t o = panel_at(M.np, tl.tj * 64 + y, tl.ti * 64 + c) >> 3;
-        f16x8 v;
+        for (int t = 0; t < 2; ++t) {
+            // 16 rows y of X^T, 32 of its columns: 1 KB that a wave writes whole
+            const int y = wave * 16, c = t * 32 + (lane >> 4) * 8;
+            const int from = (c + ((lane >> 2) & 3)) * kPitch + y + (lane & 3) * 4;
+            const int64_t o = panel_at(M.np, piece * 64 + y + (lane & 15), tl.ti * 64 + c) >> 3;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = buf[0][c + e][y];
-        hi[o] = v;
-        if constexpr (kF32) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = buf[kParts - 1][c + e][y];
-            lo[o] = v;
+            for (int part = 0; part < kParts; ++part) {
+                lds_char *b = (lds_char *)&now[part][from];
+                union {
+                    s16x4 q[2];
+                    f16x8 f;
+                } v;
+                v.q[0] = read_tr(b);
+                v.q[1] = read_tr(b + 4 * kPitch * 2);
+                (part == 0 ? hi : lo)[o] = v.f;
+            }
         }
     }
 }
@@ -316,15 +341,6 @@ __device__ __forceinline__ void fill_cols(lds_char *dst, const char *src, uint32
 // Operand of 16 rows and 32 elements of the sum: this lane's row, its 8.
 __device__ __forceinline__ f16x8 read_rows(const lds_char *t, int row, int lane) {
     return *(const lds_f16x8 *)(t + row * 64 + ((lane >> 4) ^ swz_row(row)) * 16);
-}
-
-// Four rows of 16 columns: lane l of a 16-lane group reads 4 neighbouring
-// columns (8 bytes at t) of row l >> 2, and gets column l of the 16 that lanes
-// 0 to 3 read, of those 4 rows.  (restrict: with aliasing facts on the read the
-// compiler does not wait for every load to LDS that is under way before it;
-// the borders wait for those that matter.)
-__device__ __forceinline__ s16x4 read_tr(lds_char *__restrict__ t) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)t);
 }
 
 // The operand from a tile with the sum over rows, of 16 neighbouring columns

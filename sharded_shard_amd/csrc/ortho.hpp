@@ -19,6 +19,9 @@ constexpr int32_t kOrthoPad = 128;
 constexpr int32_t kOrthoParts = 256;
 // elements per partial sum: at least this many
 constexpr int64_t kOrthoPartMin = 16384;
+// 64 x 64 pieces that one block of the start lays out: two 1024 x 8192 matrices 17.4,
+// 14.5, 14.1 and 16.7 us with 1, 2, 4 and 8, a decoder block's seven 179, 171, 175, 177
+constexpr int32_t kInitPieces = 2;
 
 // Per matrix, read on the device; offsets are bytes into the workspace.
 struct OrthoMat {
@@ -44,7 +47,7 @@ struct OrthoScal {
 struct OrthoTile {
     int32_t mat;
     int32_t ti, tj;
-    int32_t part;        // of a split sum: this part's place among all
+    int32_t part;        // of a split sum: this part's place among all; start: pieces
 };
 
 struct OrthoCoef {
@@ -65,7 +68,7 @@ enum { kSmallAll = 0, kSmallStart = 1, kSmallStep = 2, kSmallLast = 3 };
 hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              bool f32, hipStream_t st);
 // The scaled X^T (for fp32 inputs the low part too) and the scalars; tiles: 64 x
-// 64 pieces of [np][mp].  growth: log2 of the most that the iterations can
+// 64 pieces of [np][mp], `part` of them from (tj, ti) on.  growth: log2 of the most that the iterations can
 // magnify a singular value.
 hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              bool f32, double eps, int32_t growth, hipStream_t st);

@@ -106,14 +106,19 @@ hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *
         for (int64_t at : {M.t[0], M.t[1], M.lo}) touch(ws, at, x);
         touch(ws, M.scal, sizeof(OrthoScal));
     }
-    return record(harness::kInit, 64, tiles, n);
+    // each piece that a block lays out, as a tile of its own
+    std::vector<OrthoTile> pieces;
+    for (int64_t i = 0; i < n; ++i)
+        for (int32_t k = 0; k < tiles[i].part; ++k)
+            pieces.push_back({tiles[i].mat, tiles[i].ti, tiles[i].tj + k, 0});
+    return record(harness::kInit, 64, pieces.data(), static_cast<int64_t>(pieces.size()));
 }
 
 hipError_t launch_ortho_small(int32_t mp, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
                               void *ws, bool f32, int32_t mode, int32_t step, int32_t n_steps,
                               const OrthoCoef *coefs, double, int32_t, hipStream_t) {
     touch(coefs, 0, n_steps * sizeof(OrthoCoef));
-    const int64_t part = static_cast<int64_t>(mp) * mp * 4;
+    const int64_t part = static_cast<int64_t>(small_part(mp)) * 16;
     for (int64_t i = 0; i < n; ++i) {
         const OrthoMat &M = mats[tiles[i].mat];
         if (mode == kSmallAll || mode == kSmallStart) touch_in(M, f32);
