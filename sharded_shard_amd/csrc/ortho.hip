@@ -131,20 +131,21 @@ __global__ __launch_bounds__(kBlock) void ortho_norm_kernel(const OrthoTile *__r
     const bool vec = (lo32(M.in) & 15u) == 0;
     double s[4] = {0.0, 0.0, 0.0, 0.0};
     for (int64_t i = lo + threadIdx.x; i < hi; i += 4 * kBlock) {
+        // past the end the first eight again, which count nothing: no branch lies
+        // between the loads
         float x[4][8];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (i + t * kBlock < hi) {
-                load_in8<kF32>(M.in, (i + t * kBlock) * 8, vec, x[t]);
-            } else {
+        for (int t = 0; t < 4; ++t)
+            load_in8<kF32>(M.in, (i + t * kBlock < hi ? i + t * kBlock : lo) * 8, vec, x[t]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[t][e] = 0.0f;
+        for (int t = 0; t < 4; ++t) {
+            const bool in = i + t * kBlock < hi;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double d = in ? x[t][e] : 0.0f;
+                s[t] = __builtin_fma(d, d, s[t]);       // the product is exact
             }
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[t] += static_cast<double>(x[t][e]) * x[t][e];
     }
     if (tl.ti == M.n_parts - 1 && eights * 8 + threadIdx.x < total) {
         const double x = load_in<kF32>(M.in, eights * 8 + threadIdx.x);

@@ -15,8 +15,9 @@
 namespace fsdp {
 
 constexpr int32_t kOrthoPad = 128;
-// at most this many partial sums of squares per matrix
-constexpr int32_t kOrthoParts = 256;
+// at most this many partial sums of squares per matrix (a decoder block's seven:
+// 105 us; 256 of them 116)
+constexpr int32_t kOrthoParts = 512;
 // elements per partial sum: at least this many
 constexpr int64_t kOrthoPartMin = 16384;
 // 64 x 64 pieces that one block of the start lays out: two 1024 x 8192 matrices 17.4,

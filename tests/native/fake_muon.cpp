@@ -141,7 +141,7 @@ hipError_t launch_ortho_sums(const OrthoTile *tiles, int64_t n, const OrthoMat *
                              int32_t step, hipStream_t) {
     for (int64_t i = 0; i < n; ++i) {
         const OrthoMat &M = mats[tiles[i].mat];
-        const int64_t part = static_cast<int64_t>(M.mp) * M.mp * 4;
+        const int64_t part = static_cast<int64_t>(small_part(M.mp)) * 16;
         for (int64_t k = 0; k < tiles[i].tj; ++k)
             touch(ws, ((step & 1) ? M.b : M.a) + k * part + tiles[i].ti * 4096, 4096);
     }
