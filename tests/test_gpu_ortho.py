@@ -171,6 +171,32 @@ def test_long_sum_and_offsets():
         close(run([u])[0], u)
 
 
+@pytest.mark.parametrize("tall", [False, True])
+def test_more_than_2_to_31_elements(tall):
+    """U = [V V .. V], k times: X X^T is V's, so the result is V's over sqrt(k), here
+    16.  Both sides are within the tolerance of the exact one."""
+    v = matrix((2100, 4096), 4, "falling")
+    want = run([v])[0].float()
+    k, n = 256, 2100 * 4096 * 256
+    assert n > 2 ** 31
+    u = torch.empty(n, dtype=torch.bfloat16, device=DEV)
+    d = v.to(DEV)
+    if tall:
+        d, want = d.t().contiguous(), want.t().contiguous()
+        u.view(k, 4096, 2100).copy_(d)
+    else:
+        u.view(2100, k, 4096).copy_(d[:, None])
+    out = torch.zeros_like(u)
+    with Orthogonalizer([(4096 * k, 2100) if tall else (2100, 4096 * k)]) as o:
+        o.bind([u], [out])
+        o.execute()
+        torch.cuda.synchronize()
+    norm = want.norm().item()
+    for i in range(k):
+        x = out.view(k, 4096, 2100)[i] if tall else out.view(2100, k, 4096)[:, i]
+        assert (x.float() * 16 - want).norm().item() <= 4 * HALF * norm, i
+
+
 # counts at which a plan takes other tiles for its products: X X^T and A A in
 # 128, 192 and 256, B X in 128, 192 and 256 with its term a X before and along
 # the sum, X X^T in parts
