@@ -635,13 +635,16 @@ fsdp_status fsdp_ortho_plan_info(const fsdp_ortho_plan *plan, int32_t *n_mats,
 /* in, out: host arrays of n_mats device pointers to contiguous [rows, cols]
  * matrices (any pointer where the matrix is empty): in bf16 or fp32
  * (FSDP_DTYPE_*), out bf16, each aligned to its element.  An output may share
- * memory with its own input, and with nothing else of the plan.  Uploads the
- * plan's tables on `stream` and waits for it, and for the device before it
- * replaces them.  A rejected call keeps the previous binding; a HIP failure
- * during the upload leaves the plan unbound.
+ * memory with its own input, and with nothing else of the plan.  The first bind
+ * sets the plan's in_dtype: captured executions hold the kernels for it, so a
+ * later bind may name other memory, apart from the workspaces of captured
+ * executions, but no other dtype.  Uploads the plan's tables on `stream` and
+ * waits for it, and for the device before it replaces them.  A rejected call
+ * keeps the previous binding; a HIP failure during the upload leaves the plan
+ * unbound.
  * Errors: FSDP_E_INVAL (null pointer of a non-empty matrix, overlap),
  *         FSDP_E_UNSUPPORTED (dtype), FSDP_E_ALIGN, FSDP_E_STATE (bound on
- *         another device), FSDP_E_NOMEM, FSDP_E_HIP. */
+ *         another device or with another dtype), FSDP_E_NOMEM, FSDP_E_HIP. */
 fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *plan, const void *const *in, uint16_t *const *out,
                             int32_t in_dtype, void *stream);
 

@@ -22,7 +22,8 @@ struct fsdp_ortho_plan {
     int32_t n_mats = 0, growth = 0;
     double eps = 0.0;
     int64_t ws_bytes = 0;
-    bool bound = false, f32 = false;
+    bool bound = false;
+    bool f32 = false, typed = false;        // inputs' dtype, set by the first bind
     int device = -1;
     char *dmem = nullptr;                   // mats, then the tile tables
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;  // bytes of the bound matrices
@@ -364,6 +365,11 @@ fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *p, const void *const *in, uint16_t 
         return set_error(FSDP_E_INVAL, "fsdp_ortho_bind: null plan or array");
     if (in_dtype != FSDP_DTYPE_BF16 && in_dtype != FSDP_DTYPE_F32)
         return set_error(FSDP_E_UNSUPPORTED, "fsdp_ortho_bind: in_dtype must be BF16 or F32");
+    // Captured executions read addresses from the tables but hold the kernels of
+    // the dtype they were captured with: inputs of another size an element would
+    // be read past their end.
+    if (p->typed && p->f32 != (in_dtype == FSDP_DTYPE_F32))
+        return set_error(FSDP_E_STATE, "fsdp_ortho_bind: plan already bound to inputs of another dtype");
     const uintptr_t esize = in_dtype == FSDP_DTYPE_F32 ? 4 : 2;
     struct Span {
         uintptr_t lo, hi;
@@ -437,6 +443,7 @@ fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *p, const void *const *in, uint16_t 
     p->mats = std::move(mats);
     p->spans = std::move(merged);
     p->f32 = in_dtype == FSDP_DTYPE_F32;
+    p->typed = true;
     p->bound = true;
     return FSDP_OK;
 } catch (...) {

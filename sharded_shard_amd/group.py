@@ -61,7 +61,9 @@ class Orthogonalizer:
 
     def bind(self, ins, outs=None, stream=None) -> None:
         """ins: [rows, cols] GPU tensors, all bf16 (or their int16 bits) or all
-        fp32; outs: bf16 (or int16) ones, by default the bf16 inputs themselves."""
+        fp32; outs: bf16 (or int16) ones, by default the bf16 inputs themselves.
+        Binding again names other memory, which replays of a captured execution
+        work on from then on; the inputs' dtype stays that of the first bind."""
         outs = ins if outs is None else outs
         if len(ins) != len(self.shapes) or len(outs) != len(self.shapes):
             raise ValueError("one input and one output per matrix")

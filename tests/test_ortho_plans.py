@@ -1,0 +1,40 @@
+"""Orthogonalisation plans without a GPU: what they refuse, and the host code of
+several binds under AddressSanitizer and UndefinedBehaviorSanitizer."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+
+NATIVE = os.path.join(ROOT, "tests", "native")
+CSRC = os.path.join(ROOT, "sharded_shard_amd", "csrc")
+ROCM_INCLUDE = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
+
+
+def _harness(tmp_path, sources):
+    """Build the sources with the library's host code under sanitizers and run them."""
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.isdir(os.path.join(ROCM_INCLUDE, "hip")):
+        pytest.skip("needs g++ and the HIP headers")
+    out = str(tmp_path / "harness")
+    srcs = [os.path.join(NATIVE, f) for f in sources]
+    srcs += [os.path.join(CSRC, f) for f in ("capi.cpp", "plan.cpp", "reshard.cpp", "host_adamw.cpp",
+                                             "muon.cpp", "ortho.cpp")]
+    cmd = [gxx, "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer",
+           "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
+           "-ffp-contract=off", "-D__HIP_PLATFORM_AMD__", "-I" + ROCM_INCLUDE,
+           "-Wall", "-Wextra", "-Wno-unused-parameter", *srcs, "-pthread", "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-4000:]
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0:exitcode=23",
+               UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
+    env.pop("FSDP_FAULT", None)
+    r = subprocess.run([out], capture_output=True, text=True, timeout=900, env=env)
+    assert r.returncode == 0, (r.stdout[-2000:], r.stderr[-6000:])
+    assert "ALL OK" in r.stdout
+
+
+def test_a_plan_keeps_the_dtype_of_its_first_bind(tmp_path):
+    _harness(tmp_path, ["ortho_plan_harness.cpp", "fake_hip.cpp", "fake_launch.cpp", "fake_muon.cpp"])
