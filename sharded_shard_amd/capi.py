@@ -684,12 +684,13 @@ def fsdp_ortho_plan_create(rows, cols, coeffs, eps: float = 1e-7):
     n = len(rows)
     if len(cols) != n:
         raise ValueError("rows and cols differ in length")
-    flat = [float(x) for abc in coeffs for x in abc]
-    if len(flat) != 3 * len(coeffs):
+    steps = [[float(x) for x in abc] for abc in coeffs]
+    if any(len(abc) != 3 for abc in steps):
         raise ValueError("coeffs: three numbers per step")
+    flat = [x for abc in steps for x in abc]
     out = _P()
     _check(lib.fsdp_ortho_plan_create((_i64 * max(1, n))(*rows), (_i64 * max(1, n))(*cols), n,
-                                      (ctypes.c_double * max(1, len(flat)))(*flat), len(coeffs),
+                                      (ctypes.c_double * max(1, len(flat)))(*flat), len(steps),
                                       eps, ctypes.byref(out)), "fsdp_ortho_plan_create")
     return out
 

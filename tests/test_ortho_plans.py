@@ -10,6 +10,9 @@ from conftest import ROOT
 
 NATIVE = os.path.join(ROOT, "tests", "native")
 CSRC = os.path.join(ROOT, "sharded_shard_amd", "csrc")
+capi = pytest.importorskip("sharded_shard_amd.capi")
+NS = [(3.4445, -4.7750, 2.0315)] * 5
+
 ROCM_INCLUDE = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
 
 
@@ -38,3 +41,13 @@ def _harness(tmp_path, sources):
 
 def test_a_plan_keeps_the_dtype_of_its_first_bind(tmp_path):
     _harness(tmp_path, ["ortho_plan_harness.cpp", "fake_hip.cpp", "fake_launch.cpp", "fake_muon.cpp"])
+
+
+def test_every_step_has_three_coefficients():
+    """Steps of other lengths whose numbers happen to make whole threes as well."""
+    for bad in ([(1.5, -0.5), (0.0, 1.5, -0.5, 0.0)], [(1.5, -0.5, 0.0, 1.5, -0.5, 0.0), ()],
+                [(1.0, 2.0)], [NS[0], (1.5,), (-0.5, 0.0, 1.5, -0.5, 0.0)]):
+        with pytest.raises(ValueError, match="three"):
+            capi.fsdp_ortho_plan_create([4], [8], bad)
+    # any iterable of steps of any iterables
+    capi.fsdp_ortho_plan_destroy(capi.fsdp_ortho_plan_create([4], [8], (iter(c) for c in NS)))
