@@ -620,7 +620,7 @@ typedef struct fsdp_ortho_plan fsdp_ortho_plan;
  *   coeffs      host array of 3 * n_steps: a, b, c of each step; n_steps in
  *               [1, 64].  Starting from singular values in [0, 1], no step may
  *               take one past 4, nor |b s^2 + c s^4| past 16 (the range of the
- *               scaled products)
+ *               scaled products), from 2% more than the steps before it give
  *   eps         finite, >= 0
  * Errors: FSDP_E_INVAL, FSDP_E_UNSUPPORTED (sides, n_steps, the range of the
  *         coefficients), FSDP_E_NOMEM. */

@@ -63,6 +63,11 @@ void extremes(double a, double b, double c, double top, double *f, double *g, do
     }
 }
 
+// Every step is held to the range with singular values of 2% more than the steps
+// before it can give, for what the products round.  That room is not handed on:
+// 2% a step would add up, and a steep step multiplies it.
+constexpr double kSpare = 1.02;
+
 fsdp_status check_coeffs(const double *coeffs, int32_t n_steps, fsdp_ortho_plan *p) {
     double top = 1.0, growth = 0.0;
     for (int32_t k = 0; k < n_steps; ++k) {
@@ -70,14 +75,15 @@ fsdp_status check_coeffs(const double *coeffs, int32_t n_steps, fsdp_ortho_plan 
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
             return set_error(FSDP_E_INVAL, "fsdp_ortho_plan_create: coefficient of step " +
                                                std::to_string(k) + " is not finite");
-        double f, g, q;
-        extremes(a, b, c, top * 1.02, &f, &g, &q);
+        double f, g, q, f0, g0, q0;
+        extremes(a, b, c, top * kSpare, &f, &g, &q);
         if (!(f <= kMaxSigma) || !(g <= kMaxB))
             return set_error(FSDP_E_UNSUPPORTED,
                              "fsdp_ortho_plan_create: the coefficients of step " +
                                  std::to_string(k) +
                                  " take a singular value past 4 or b s^2 + c s^4 past 16");
-        top = f;
+        extremes(a, b, c, top, &f0, &g0, &q0);
+        top = f0;
         growth += std::max(0.0, std::log2(std::max(q, 1e-30)));
         p->coef.push_back({static_cast<float>(a), static_cast<float>(b), static_cast<float>(c)});
     }

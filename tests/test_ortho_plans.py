@@ -51,3 +51,29 @@ def test_every_step_has_three_coefficients():
             capi.fsdp_ortho_plan_create([4], [8], bad)
     # any iterable of steps of any iterables
     capi.fsdp_ortho_plan_destroy(capi.fsdp_ortho_plan_create([4], [8], (iter(c) for c in NS)))
+
+
+def _tops(coeffs):
+    """The largest singular value after each step, from any in [0, 1]."""
+    import numpy as np
+    s, out = np.linspace(0.0, 1.0, 200001), []
+    for a, b, c in coeffs:
+        s = np.abs(a * s + b * s ** 3 + c * s ** 5)
+        out.append(s.max())
+    return out
+
+
+def test_steep_schedules_are_accepted_as_far_as_the_range_allows():
+    """The room that a step leaves for rounding is its own: handed on from step
+    to step it refused schedules that stay far inside the range."""
+    steep = [(8.205, -22.90, 16.46), (4.066, -2.861, 0.518)]
+    assert max(_tops(steep)) < 2.1
+    for coeffs in (steep, steep + [(1.0, 0.0, 0.0)] * 40, [(2.0, 0, 0), (1.95, 0, 0)] + [(1.0, 0, 0)] * 20):
+        assert max(_tops(coeffs)) < 4.0
+        capi.fsdp_ortho_plan_destroy(capi.fsdp_ortho_plan_create([4], [8], coeffs))
+    # the second's 2 * 1.97 * 1.02 is 4.02
+    for coeffs in ([(2.0, 0, 0), (2.0, 0, 0)], [(2.0, 0, 0), (1.97, 0, 0)] + [(1.0, 0, 0)] * 20,
+                   [(4.0, 0, 0)], steep + [(2.3, 0, 0)], [(1.0, 0, 0)] * 9 + [(4.1, 0, 0)]):
+        with pytest.raises(capi.FsdpError) as ei:
+            capi.fsdp_ortho_plan_create([4], [8], coeffs)
+        assert ei.value.status == capi.FSDP_E_UNSUPPORTED
