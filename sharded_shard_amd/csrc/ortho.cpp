@@ -43,15 +43,14 @@ int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 // and of |f(s) / s|, from the ends and the places where a derivative is 0.
 void extremes(double a, double b, double c, double top, double *f, double *g, double *q) {
     std::vector<double> t = {0.0, top * top};      // values of s^2
-    if (c != 0.0) {
-        t.push_back(-b / (2.0 * c));
-        const double d = 9.0 * b * b - 20.0 * a * c;
-        if (d >= 0.0) {
-            t.push_back((-3.0 * b + std::sqrt(d)) / (10.0 * c));
-            t.push_back((-3.0 * b - std::sqrt(d)) / (10.0 * c));
-        }
-    } else if (b != 0.0) {
-        t.push_back(-a / (3.0 * b));
+    if (c != 0.0) t.push_back(-b / (2.0 * c));
+    // a + 3 b t + 5 c t^2 = 0: the root of the sum without cancellation, and the
+    // other from their product a / (5 c), which is right for a vanishing c too
+    const double d = 9.0 * b * b - 20.0 * a * c;
+    if (d >= 0.0) {
+        const double r = -0.5 * (3.0 * b + std::copysign(std::sqrt(d), b));
+        if (c != 0.0) t.push_back(r / (5.0 * c));
+        if (r != 0.0) t.push_back(a / r);
     }
     *f = *g = *q = 0.0;
     for (double s2 : t) {

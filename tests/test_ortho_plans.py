@@ -77,3 +77,14 @@ def test_steep_schedules_are_accepted_as_far_as_the_range_allows():
         with pytest.raises(capi.FsdpError) as ei:
             capi.fsdp_ortho_plan_create([4], [8], coeffs)
         assert ei.value.status == capi.FSDP_E_UNSUPPORTED
+
+
+@pytest.mark.parametrize("c", [1e-12, -1e-12, 1e-17, -1e-17, 1e-200, -1e-300, 5e-324])
+def test_a_vanishing_fifth_order_term_does_not_hide_a_maximum(c):
+    """15 s - 15 s^3 reaches 5.8 at s = 0.58 and returns to 0 at 1; so it does with
+    c s^5 too small to count."""
+    with pytest.raises(capi.FsdpError) as ei:
+        capi.fsdp_ortho_plan_create([4], [8], [(15.0, -15.0, c)])
+    assert ei.value.status == capi.FSDP_E_UNSUPPORTED
+    # the same shape within the range: 2.6 at its largest
+    capi.fsdp_ortho_plan_destroy(capi.fsdp_ortho_plan_create([4], [8], [(6.8, -6.8, c)]))
