@@ -705,6 +705,10 @@ def fsdp_ortho_plan_info(plan):
 
 def fsdp_ortho_bind(plan, ins, outs, in_dtype: int = FSDP_DTYPE_BF16, stream=None) -> None:
     """ins, outs: one tensor or address per matrix."""
+    if plan is not None and getattr(plan, "value", 1) is not None:
+        n = fsdp_ortho_plan_info(plan)[0]
+        if len(ins) != n or len(outs) != n:
+            raise ValueError(f"{len(ins)} inputs and {len(outs)} outputs for a plan of {n} matrices")
     _check(lib.fsdp_ortho_bind(plan, _ptr_array(ins), _ptr_array(outs), in_dtype,
                                stream_handle(stream)), "fsdp_ortho_bind")
 

@@ -88,3 +88,16 @@ def test_a_vanishing_fifth_order_term_does_not_hide_a_maximum(c):
     assert ei.value.status == capi.FSDP_E_UNSUPPORTED
     # the same shape within the range: 2.6 at its largest
     capi.fsdp_ortho_plan_destroy(capi.fsdp_ortho_plan_create([4], [8], [(6.8, -6.8, c)]))
+
+
+def test_bind_needs_an_address_for_every_matrix():
+    """The C call reads n_mats of each array."""
+    p = capi.fsdp_ortho_plan_create([5, 0, 7], [7, 4, 3], NS)
+    ins, outs = [0x10000, 0, 0x20000], [0x30000, 0, 0x40001]
+    for a, b in ((ins[:2], outs), (ins, outs[:1]), ([], []), (ins + [0x50000], outs + [0x60000])):
+        with pytest.raises(ValueError, match="3 matrices"):
+            capi.fsdp_ortho_bind(p, a, b, stream=0)
+    with pytest.raises(capi.FsdpError) as ei:      # whole lists go on to the C checks
+        capi.fsdp_ortho_bind(p, ins, outs, stream=0)
+    assert ei.value.status == capi.FSDP_E_ALIGN
+    capi.fsdp_ortho_plan_destroy(p)
