@@ -1294,9 +1294,11 @@ hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const
     else if (tile == 128)
         ortho_product_kernel<KIND, 128, 128, 2, 2>
             <<<grid, 256, 0, st>>>(tiles, mats, ws, src, when, split, c);
-    else
+    else if (tile == 64)
         ortho_product_kernel<KIND, 64, 64, 2, 2>
             <<<grid, 256, 0, st>>>(tiles, mats, ws, src, when, split, c);
+    else
+        return hipErrorInvalidValue;
     return hipGetLastError();
 }
 

@@ -81,7 +81,8 @@ hipError_t launch_ortho_small(int32_t mp, const OrthoTile *tiles, int64_t n, con
 // tiles: (matrix, 256 x 4 elements of it, number of parts).
 hipError_t launch_ortho_sums(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              int32_t step, hipStream_t st);
-// The products; tile: 256, 128 or 64 rows and columns of a tile.
+// The products; tile: 256, 192, 128 or 64 rows and columns of a tile, any other
+// is hipErrorInvalidValue.
 // A = X X^T, tiles (ti >= tj) of the lower triangle; src: which high part is
 // read.  With split > 1 every tile comes split times (its part its place among
 // all parts), and join has each once, with its first part.

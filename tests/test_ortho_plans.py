@@ -101,3 +101,17 @@ def test_bind_needs_an_address_for_every_matrix():
         capi.fsdp_ortho_bind(p, ins, outs, stream=0)
     assert ei.value.status == capi.FSDP_E_ALIGN
     capi.fsdp_ortho_plan_destroy(p)
+
+
+def test_product_launchers_refuse_a_tile_that_they_do_not_have():
+    """Before anything is launched: an unknown side ran as 64 x 64 tiles."""
+    import ctypes
+    gram = getattr(capi.lib, "_ZN4fsdp17launch_ortho_gramEiPKNS_9OrthoTileElS2_liPKNS_8OrthoMatEPvibP12ihipStream_t")
+    gram.restype = ctypes.c_int
+    gram.argtypes = [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                     ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_bool,
+                     ctypes.c_void_p]
+    hip_error_invalid_value = 1
+    for side in (0, 32, 96, 160, 512, -64):
+        for split in (1, 2):
+            assert gram(side, None, 1, None, 1, split, None, None, 0, True, None) == hip_error_invalid_value
