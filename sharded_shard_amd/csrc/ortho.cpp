@@ -280,6 +280,21 @@ void layout(fsdp_ortho_plan *p) {
     spread(&p->apply);
 }
 
+// A launch has less than 2^32 threads.
+bool fits_launches(const fsdp_ortho_plan &p) {
+    auto fits = [](const std::vector<fsdp::OrthoTile> &v, int32_t threads) {
+        return v.size() * static_cast<uint64_t>(threads) < (uint64_t{1} << 32);
+    };
+    bool ok = fits(p.norm, 256) && fits(p.init, 256) && fits(p.sums, 256) &&
+              fits(p.gram, fsdp::product_threads(p.t_gram)) &&
+              fits(p.poly, fsdp::product_threads(p.t_poly)) &&
+              fits(p.apply, fsdp::product_threads(p.t_apply));
+    for (int c = 0; c < 3; ++c)
+        ok = ok && fits(p.one[c], fsdp::small_threads(32 << c)) &&
+             fits(p.slabs[c], fsdp::small_threads(32 << c));
+    return ok;
+}
+
 // The device tables in their order: matrices, coefficients, tiles.
 struct Table {
     const void *src;
@@ -340,8 +355,7 @@ fsdp_status fsdp_ortho_plan_create(const int64_t *rows, const int64_t *cols, int
             p->index.push_back(i);
         }
         if (s == FSDP_OK) layout(p);
-        const size_t most = size_t{1} << 30;
-        if (s == FSDP_OK && (p->apply.size() > most || p->gram.size() > most || p->init.size() > most))
+        if (s == FSDP_OK && !fits_launches(*p))
             s = set_error(FSDP_E_UNSUPPORTED, "fsdp_ortho_plan_create: too many tiles for one launch");
         if (s != FSDP_OK) {
             delete p;

@@ -741,9 +741,7 @@ template <int MP>
 struct Small {
     static constexpr int NB = small_slab(MP);           // columns of a slab, at most
     static constexpr int nb = MP / 16;                  // 16 x 16 blocks a side
-    // with 128 rows the work of one block of threads is long: 16 waves (with 8 a
-    // 128 x 128 matrix took 7 % longer, 32 of 128 x 2048 18 %)
-    static constexpr int kThreads = MP == 128 ? 1024 : 512, kWaves = kThreads / 64;
+    static constexpr int kThreads = small_threads(MP), kWaves = kThreads / 64;
     // 16 x 16 blocks of A and B that one wave has
     static constexpr int kBJ = MP == 128 ? 4 : MP == 64 ? 2 : 1;
     // up to 64 rows a wave sums 32 x 32 of A over one stretch in kStretches
@@ -1277,8 +1275,6 @@ hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *
 
 namespace {
 
-// 256 x 256 by eight waves and 192 x 192 by twelve, one block a CU; 128 x 128 and
-// 64 x 64 by four, two and five blocks a CU
 template <int KIND>
 hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
                           void *ws, int32_t src, int32_t when, int32_t split, OrthoCoef c,
@@ -1287,16 +1283,16 @@ hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const
     const unsigned grid = static_cast<unsigned>(n);
     if (tile == 256)
         ortho_product_kernel<KIND, 256, 256, 2, 4>
-            <<<grid, 512, 0, st>>>(tiles, mats, ws, src, when, split, c);
+            <<<grid, product_threads(256), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 192)
         ortho_product_kernel<KIND, 192, 192, 6, 2>
-            <<<grid, 768, 0, st>>>(tiles, mats, ws, src, when, split, c);
+            <<<grid, product_threads(192), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 128)
         ortho_product_kernel<KIND, 128, 128, 2, 2>
-            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, when, split, c);
+            <<<grid, product_threads(128), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 64)
         ortho_product_kernel<KIND, 64, 64, 2, 2>
-            <<<grid, 256, 0, st>>>(tiles, mats, ws, src, when, split, c);
+            <<<grid, product_threads(64), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else
         return hipErrorInvalidValue;
     return hipGetLastError();

@@ -62,8 +62,18 @@ constexpr int32_t small_rows_of(int32_t m) { return m <= 32 ? 32 : m <= 64 ? 64 
 // fours of a slab's part of X X^T: the upper 32 x 32 blocks of 128 rows, or all
 constexpr int32_t small_part(int32_t mp) { return mp == 128 ? 10 * 256 : mp * mp / 4; }
 constexpr int32_t small_slab(int32_t mp) { return mp == 128 ? 128 : mp == 64 ? 416 : 896; }
+// with 128 rows the work of one block of threads is long: 16 waves (with 8 a
+// 128 x 128 matrix took 7 % longer, 32 of 128 x 2048 18 %)
+constexpr int32_t small_threads(int32_t mp) { return mp == 128 ? 1024 : 512; }
 // What a launch does: all steps (one slab), the start, one step, the last step.
 enum { kSmallAll = 0, kSmallStart = 1, kSmallStep = 2, kSmallLast = 3 };
+
+// Threads of a block of a product with tiles of this side: 256 x 256 by eight
+// waves and 192 x 192 by twelve, one block a CU; 128 x 128 and 64 x 64 by four,
+// two and five blocks a CU.
+constexpr int32_t product_threads(int32_t tile) {
+    return tile == 256 ? 512 : tile == 192 ? 768 : 256;
+}
 
 // Partial sums of squares; tiles: (matrix, part).
 hipError_t launch_ortho_norm(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,

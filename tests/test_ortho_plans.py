@@ -115,3 +115,12 @@ def test_product_launchers_refuse_a_tile_that_they_do_not_have():
     for side in (0, 32, 96, 160, 512, -64):
         for split in (1, 2):
             assert gram(side, None, 1, None, 1, split, None, None, 0, True, None) == hip_error_invalid_value
+
+
+def test_plans_past_a_launch_are_refused():
+    """A launch has less than 2^32 threads: 65536 x 2^20 elements are 2^23 blocks of
+    256 at the start, two such matrices are one too many."""
+    capi.fsdp_ortho_plan_destroy(capi.fsdp_ortho_plan_create([1 << 16], [1 << 20], NS[:1]))
+    with pytest.raises(capi.FsdpError, match="too many tiles") as ei:
+        capi.fsdp_ortho_plan_create([1 << 16] * 2, [1 << 20] * 2, NS[:1])
+    assert ei.value.status == capi.FSDP_E_UNSUPPORTED
