@@ -255,8 +255,9 @@ void reduce_momentum(hipStream_t st, const PackTile *tiles, int64_t n, const Dev
     // Rows in flight and elements a block, from a sweep over both for 1 to 64
     // ranks.  From 16 ranks a wave a block, two rows at a time: 64 ranks 6.4 TB/s
     // (5.95 with four rows, 4.5 with one row and 2048 elements for four waves);
-    // misaligned 4.5 (3.9).  Below, as many rows as divide N, in fewer elements
-    // the more rows there are: 8 ranks 5.9 TB/s (5.4 with one row and 2048
+    // misaligned 4.5 (3.9).  Below, three rows at a time where three divide N,
+    // else four from four ranks on, the N mod 4 that are left one by one, in fewer
+    // elements the more ranks there are: 8 ranks 5.9 TB/s (5.4 with one row and 2048
     // elements), 6 ranks 5.95 (5.45); misaligned rows two at a time, 5.3 TB/s at 6
     // ranks (5.0 with one, 5.1 with three).
     const int64_t most = 6144 / N;

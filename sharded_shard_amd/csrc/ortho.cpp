@@ -128,8 +128,8 @@ int64_t sums_in_block(const fsdp_ortho_plan &p) {
 // Tile sides and the parts of X X^T's sum: what a model of a launch's time says,
 // in clocks.  A CU takes `per` clocks for each element of a tile's sum, and a
 // tile no less than `alone` however many CUs are idle; measured on products of
-// 256 to 4096 rows (256: 46 clocks where every CU has a tile; 128: 13 each and
-// 16 alone; 64: 6 and 11).  Larger tiles read their operands less often, smaller
+// 256 to 4096 rows (256: 46 clocks where every CU has a tile; 192: 34; 128: 13 each
+// and 16 alone; 64: 6 and 11).  Larger tiles read their operands less often, smaller
 // ones fill the CUs where there are few: one 4096 x 4096 matrix's a X + B X takes
 // 150 us in 256 x 256 tiles and 165 in 128 x 128, one 2048 x 2048's 31 and 12; two
 // such matrices' X X^T (272 tiles of 256) 135 and 105.  A split sum costs a launch
