@@ -46,8 +46,12 @@ class Orthogonalizer:
     """Newton-Schulz orthogonalisation of a list of full matrices, many shapes
     in one call; ``bind`` names the matrices, ``execute`` enqueues the work.
 
-    The workspace is allocated on first use, or the caller's: several of them
-    may share one whose executions follow each other.
+    The workspace is allocated on first use, or the caller's.  Executions that
+    share one must follow each other, on one stream or with events between
+    them: those of one Orthogonalizer, of several with the same workspace, and
+    replays of executions captured into graphs.  A captured execution keeps the
+    workspace that it was captured with; that and the Orthogonalizer must
+    outlive its replays.
     """
 
     def __init__(self, shapes: Sequence[Sequence[int]], coeffs=NS_COEFFS, eps: float = 1e-7):
@@ -81,6 +85,11 @@ class Orthogonalizer:
         self._bound = (list(ins), list(outs))
 
     def allocate(self, workspace: Optional[torch.Tensor] = None, device: str = "cuda") -> None:
+        """Use ``workspace``, or new memory of the current stream.  One that was
+        there before is let go of once the device has finished with it."""
+        if self.workspace is not None:
+            # executions on any stream may be under way in it
+            torch.cuda.synchronize(self.workspace.device)
         if workspace is None:
             workspace = torch.empty(max(self.workspace_bytes, 1), dtype=torch.uint8, device=device)
         if workspace.numel() * workspace.element_size() < self.workspace_bytes:

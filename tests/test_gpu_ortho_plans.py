@@ -73,3 +73,27 @@ def test_replays_follow_the_binding_and_its_dtype_stays(dtype):
         assert torch.equal(x, y)
     del graph
     o.close()
+
+
+def test_a_workspace_is_replaced_after_the_executions_in_it():
+    """Memory let go of while another stream still works in it would be handed out
+    again."""
+    u, = matrices([(300, 500)], 4)
+    out, = empty([u.shape])
+    want, = alone([u])
+    side = torch.cuda.Stream()
+    with Orthogonalizer([u.shape]) as o:
+        o.bind([u], [out])
+        o.allocate()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        o.execute(stream=side)
+        assert not side.query()
+        o.allocate(torch.empty(o.workspace_bytes, dtype=torch.uint8, device=DEV))
+        assert side.query()
+        assert torch.equal(out, want)
+        out.fill_(7.0)
+        o.execute()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
