@@ -603,9 +603,8 @@ fsdp_status fsdp_muon_update(const fsdp_plan *plan, const uint16_t *upd, uint16_
  * which maps every singular value s to a s + b s^3 + c s^5, step by step, and
  * leaves the singular vectors.  The norm is summed in fp64.  The products take
  * fp16 operands (scaled by powers of two) and add in fp32, the term a X takes X
- * to 22 bits: the result is within about 2e-3 of the exact iterate before its
- * rounding to bf16 (relative, in the 2-norm, for the default coefficients).  A
- * matrix that holds a NaN or an infinity becomes NaN throughout; one of zeros
+ * to 22 bits; how many parts the operands have is the plan's choice
+ * (fsdp_ortho_plan_set_products).  A matrix that holds a NaN or an infinity becomes NaN throughout; one of zeros
  * stays zero (with eps > 0).  A plan gives the same bits every time; which other
  * matrices a plan has may change how a matrix's fp32 sums are split, and so its
  * last bits, but never by what those hold.
@@ -631,6 +630,28 @@ fsdp_status fsdp_ortho_plan_create(const int64_t *rows, const int64_t *cols, int
 /* The number of matrices, and the bytes of workspace an execution needs. */
 fsdp_status fsdp_ortho_plan_info(const fsdp_ortho_plan *plan, int32_t *n_mats,
                                  int64_t *workspace_bytes);
+
+/* The operands of the products of matrices with more than 128 rows (the smaller
+ * side); up to 128 rows they always have both parts.  Errors are those of the
+ * result before its rounding to bf16, relative, in the 2-norm, for the default
+ * coefficients.
+ *   FSDP_ORTHO_FP16    the default: X, A and B rounded to fp16 once for each
+ *           product.  Where these roundings are independent of each other, as for
+ *           gradients, noise and falling spectra, the result is within 2e-3.
+ *           Where many entries have the same magnitude they add up: to 8e-3 for
+ *           a constant, signs of rank one, repeated or orthonormal rows or an
+ *           identity, 1.7e-2 for two constants in blocks (the largest found).
+ *           All roundings at their largest would be 3.2e-2 for a matrix of rank
+ *           one.
+ *   FSDP_ORTHO_FP16X2  a high and a low fp16 part of each, 22 bits, in three
+ *           products for each one: within 1e-4 on every matrix.  An execution
+ *           takes 2.3 to 2.9 times as long, and the workspace grows by a half
+ *           to 0.6 of its size.
+ * Changes the plan's workspace bytes.
+ * Errors: FSDP_E_INVAL (null plan), FSDP_E_UNSUPPORTED (products),
+ *         FSDP_E_STATE (after a bind), FSDP_E_NOMEM. */
+enum { FSDP_ORTHO_FP16 = 0, FSDP_ORTHO_FP16X2 = 1 };
+fsdp_status fsdp_ortho_plan_set_products(fsdp_ortho_plan *plan, int32_t products);
 
 /* in, out: host arrays of n_mats device pointers to contiguous [rows, cols]
  * matrices (any pointer where the matrix is empty): in bf16 or fp32

@@ -35,6 +35,8 @@ FSDP_ROLE_FULL_FP8 = 128
 
 FSDP_DTYPE_BF16 = 0
 FSDP_DTYPE_F32 = 1
+FSDP_ORTHO_FP16 = 0
+FSDP_ORTHO_FP16X2 = 1
 
 FSDP_STEP_WRITE_GRAD = 1
 FSDP_STEP_UNFUSED = 2
@@ -157,6 +159,7 @@ _SIGS = {
                                       ctypes.POINTER(ctypes.c_double), _i32, ctypes.c_double,
                                       ctypes.POINTER(_P)]),
     "fsdp_ortho_plan_info": (_i32, [_P, ctypes.POINTER(_i32), ctypes.POINTER(_i64)]),
+    "fsdp_ortho_plan_set_products": (_i32, [_P, _i32]),
     "fsdp_ortho_bind": (_i32, [_P, _PP, _PP, _i32, _P]),
     "fsdp_ortho_execute": (_i32, [_P, _P, _i64, _P]),
     "fsdp_ortho_plan_destroy": (None, [_P]),
@@ -701,6 +704,11 @@ def fsdp_ortho_plan_info(plan):
     _check(lib.fsdp_ortho_plan_info(plan, ctypes.byref(n), ctypes.byref(b)),
            "fsdp_ortho_plan_info")
     return n.value, b.value
+
+
+def fsdp_ortho_plan_set_products(plan, products: int) -> None:
+    """FSDP_ORTHO_FP16 or FSDP_ORTHO_FP16X2, before the first bind."""
+    _check(lib.fsdp_ortho_plan_set_products(plan, products), "fsdp_ortho_plan_set_products")
 
 
 def fsdp_ortho_bind(plan, ins, outs, in_dtype: int = FSDP_DTYPE_BF16, stream=None) -> None:

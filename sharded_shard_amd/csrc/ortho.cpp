@@ -19,6 +19,7 @@ struct fsdp_ortho_plan {
     std::vector<fsdp::OrthoTile> norm, init, gram, join, poly, apply;
     std::vector<fsdp::OrthoTile> one[3], slabs[3], sums;    // few rows: 32, 64, 128
     int32_t t_gram = 128, t_poly = 128, t_apply = 128, split = 1;   // tiles' sides, parts of X X^T
+    bool fine = false;                      // both parts of every operand above 128 rows too
     int32_t n_mats = 0, growth = 0;
     double eps = 0.0;
     int64_t ws_bytes = 0;
@@ -151,7 +152,7 @@ double clocks(const fsdp_ortho_plan &p, Product what, const Tile &tile, int32_t 
         if (M.m <= fsdp::kSmallMax) continue;
         const double a = (M.mp + tile.side - 1) / tile.side, b = (M.np + tile.side - 1) / tile.side;
         const double n = what == kBX ? a * b : a * (a + 1) / 2;
-        const double sum = static_cast<double>(what == kXXT ? M.np : M.mp) / split;
+        const double sum = (p.fine ? 3.0 : 1.0) * (what == kXXT ? M.np : M.mp) / split;
         work += n * split * sum;
         tiles += n;
         shortest = std::min(shortest, sum);
@@ -243,6 +244,11 @@ void layout(fsdp_ortho_plan *p) {
         M.lo = take(x);
         M.a = take(s);
         M.b = take(s);
+        if (p->fine) {
+            M.lo2 = take(x);
+            M.al = take(s);
+            M.bl = take(s);
+        }
         for (int32_t j = 0; j < M.np / 64; j += fsdp::kInitPieces)
             for (int32_t k = 0; k < M.mp / 64; ++k)
                 p->init.push_back({id, k, j, std::min(fsdp::kInitPieces, M.np / 64 - j)});
@@ -378,6 +384,30 @@ fsdp_status fsdp_ortho_plan_info(const fsdp_ortho_plan *p, int32_t *n_mats,
     return FSDP_OK;
 }
 
+fsdp_status fsdp_ortho_plan_set_products(fsdp_ortho_plan *p, int32_t products) try {
+    const char *call = "fsdp_ortho_plan_set_products";
+    if (p == nullptr) return set_error(FSDP_E_INVAL, std::string(call) + ": null plan");
+    if (products != FSDP_ORTHO_FP16 && products != FSDP_ORTHO_FP16X2)
+        return set_error(FSDP_E_UNSUPPORTED, std::string(call) + ": products must be FP16 or FP16X2");
+    if (p->dmem != nullptr)
+        return set_error(FSDP_E_STATE, std::string(call) + ": plan already bound");
+    fsdp_ortho_plan next;
+    next.mats = p->mats;
+    next.index = p->index;
+    next.coef = p->coef;
+    next.n_mats = p->n_mats;
+    next.growth = p->growth;
+    next.eps = p->eps;
+    next.fine = products == FSDP_ORTHO_FP16X2;
+    layout(&next);
+    if (!fits_launches(next))
+        return set_error(FSDP_E_UNSUPPORTED, std::string(call) + ": too many tiles for one launch");
+    *p = std::move(next);
+    return FSDP_OK;
+} catch (...) {
+    return set_error(FSDP_E_NOMEM, "fsdp_ortho_plan_set_products: host allocation failed");
+}
+
 fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *p, const void *const *in, uint16_t *const *out,
                             int32_t in_dtype, void *stream) try {
     if (p == nullptr || (p->n_mats > 0 && (in == nullptr || out == nullptr)))
@@ -411,6 +441,7 @@ fsdp_status fsdp_ortho_bind(fsdp_ortho_plan *p, const void *const *in, uint16_t 
         spans.push_back({b, b + n * 2, true, i});
         mats[k].in = in[i];
         mats[k].out = out[i];
+        mats[k].low = in_dtype == FSDP_DTYPE_F32 ? 1 : 0;
     }
     std::sort(spans.begin(), spans.end(), [](const Span &x, const Span &y) { return x.lo < y.lo; });
     // an output may share memory with its own input only: pairs that overlap
@@ -506,6 +537,7 @@ fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *p, void *workspace, int64_
                           *poly = tiles(6), *apply = tiles(7), *sums = tiles(14);
     auto count = [](const std::vector<fsdp::OrthoTile> &v) { return static_cast<int64_t>(v.size()); };
     const int32_t n_steps = static_cast<int32_t>(p->coef.size());
+    const int32_t fine = p->fine ? fsdp::kTileFine : 0;
     auto run = [&](const std::vector<fsdp::OrthoTile> &v, auto &&launch) {
         if (v.empty() || e != hipSuccess) return;
         e = fsdp::injected_fault();
@@ -541,16 +573,17 @@ fsdp_status fsdp_ortho_execute(const fsdp_ortho_plan *p, void *workspace, int64_
         });
         small(last ? fsdp::kSmallLast : fsdp::kSmallStep, static_cast<int32_t>(k));
         run(p->gram, [&] {
-            return fsdp::launch_ortho_gram(p->t_gram, gram, count(p->gram), join, count(p->join),
+            return fsdp::launch_ortho_gram(p->t_gram | fine, gram, count(p->gram), join, count(p->join),
                                            p->split, mats, workspace, src, k == 0, st);
         });
         run(p->poly, [&] {
-            return fsdp::launch_ortho_poly(p->t_poly, poly, count(p->poly), mats, workspace,
+            return fsdp::launch_ortho_poly(p->t_poly | fine, poly, count(p->poly), mats, workspace,
                                            p->coef[k], st);
         });
         run(p->apply, [&] {
-            return fsdp::launch_ortho_apply(p->t_apply, apply, count(p->apply), mats, workspace, src,
-                                            k == 0, k == 0 && !p->f32, last, p->coef[k], st);
+            return fsdp::launch_ortho_apply(p->t_apply | fine, apply, count(p->apply), mats,
+                                            workspace, src, k == 0, k == 0 && !p->f32, last,
+                                            p->coef[k], st);
         });
     }
     return e == hipSuccess ? FSDP_OK : hip_error(e, (std::string(call) + ": launch").c_str());

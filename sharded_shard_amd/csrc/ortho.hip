@@ -15,7 +15,17 @@
 // one of low rank (relative, in the 2-norm; bf16 1e-2 to 0.2).  The term a X
 // therefore takes X as a high and a low fp16 part (22 bits); the products,
 // which vanish with the singular value, take the high part.  That leaves 3e-4
-// to 2e-3, below the 1.7e-3 of rounding the result to bf16 itself or near it.
+// to 2e-3 on gradients, noise and falling spectra, where the roundings of X, A
+// and B are independent of each other: below the 1.7e-3 of rounding the result
+// to bf16 itself or near it.  Where many entries have the same magnitude their
+// roundings are the same, and add up: 2e-3 to 8e-3 on constants, signs of rank
+// one, repeated or orthonormal rows and identities, 1.7e-2 on two constants in
+// blocks.
+//
+// A plan may therefore have its products made of both parts of every operand,
+// in three terms (high high, low high, high low), like those of few rows below:
+// 22 bits throughout, 1e-6 to 3e-5 off on all of these, in 2.3 to 2.9 times the
+// time (a decoder block's seven matrices 39.1 ms for 14.7).
 //
 // Layout.  Only X^T is stored.  X = a X + B X is then a product of rows with
 // rows (rows of B, rows of X^T), and A sums over rows of X^T, whose tiles the
@@ -398,7 +408,11 @@ __device__ __forceinline__ void border() {
 // old stage in registers (lgkmcnt) and its loads of the next one landed
 // (vmcnt: those after it may be under way); past the barrier the next stage
 // may be read and the old one overwritten.
-template <int KIND, int BM, int BN, int WM, int WN>
+//
+// kFine: operands as high and low parts.  The sum is three times as long, over
+// (high, high), (low, high) and (high, low) parts one after the other: the terms
+// differ only in the memory that a stage is filled from.
+template <int KIND, int BM, int BN, int WM, int WN, bool kFine>
 __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const OrthoTile *__restrict__ tiles, const OrthoMat *__restrict__ mats, void *ws, int32_t src,
     int32_t when, int32_t split, OrthoCoef coef) {
@@ -422,6 +436,8 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
     const int g = lane >> 4;
     const OrthoScal sc = *reinterpret_cast<const OrthoScal *>(at(ws, M.scal));
     const char *T = at(ws, src ? M.t[1] : M.t[0]);
+    // X's low part: in place where nothing but a X reads it
+    const char *L = at(ws, kFine && src ? M.lo2 : M.lo);
 
     f32x4 acc[FM][FN];
     if constexpr (KIND == kGramJoin) {
@@ -440,6 +456,34 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                 for (int y = 0; y < FN; ++y) acc[x][y] += part[(x * FN + y) * 64 * WAVES];
         }
     } else {
+        // stages of the sum, or of this part's stretch of it, a multiple of four: of
+        // one term, and of all
+        int term = (kXXT ? M.np : M.mp) / kBK, steps;
+        const char *TH = T, *TL = L;
+        if constexpr (KIND == kGramPart) {
+            const int units = term / NST, k = tl.part % split;
+            const int from = units * k / split, to = units * (k + 1) / split;
+            TH += static_cast<int64_t>(from) * NST * 2048;
+            TL += static_cast<int64_t>(from) * NST * 2048;
+            term = (to - from) * NST;
+        }
+        steps = term;
+        if constexpr (kFine) {
+            // before the first iteration a bf16 input has no low part
+            const bool high = KIND != kPoly && (when & kFirst) && !M.low;
+            steps = term * (!high ? 3 : kXXT ? 1 : 2);
+        }
+        // The part of an operand that stage s is filled from, and its stage within the
+        // term; second: the low part's turn.
+        auto source = [&](const char *high, const char *low, int second, int &s) {
+            if constexpr (kFine) {
+                const int t = (s >= term) + (s >= 2 * term);
+                s -= t * term;
+                return t == second ? low : high;
+            } else {
+                return high;
+            }
+        };
         // load k of this wave's kLoadsP of stage s's rows i, or of its kLoadsQ of the rows j
         auto fill_p = [&](int s, int k) {
             lds_char *b = lds + (s & (NST - 1)) * kStage;
@@ -448,9 +492,11 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                 // rows of X^T are the sum, columns i and j
                 const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
                 const int at = i0 / 32, n = M.mp / 32 - at < BM / 32 ? M.mp / 32 - at : BM / 32;
-                fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
+                const char *X = source(TH, TL, 1, s);
+                fill_cols(b, X + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
             } else {
-                const char *A = at(ws, KIND == kPoly ? M.a : M.b);
+                const char *A = source(at(ws, KIND == kPoly ? M.a : M.b),
+                                       at(ws, KIND == kPoly ? M.al : M.bl), 1, s);
                 const int n = M.mp - i0 < BM ? M.mp - i0 : BM;
                 fill_rows(b, A + (static_cast<int64_t>(s) * M.mp + i0) * 64, n * 64u, u, lane);
             }
@@ -461,9 +507,11 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
             if constexpr (kXXT) {
                 const uint32_t panel = static_cast<uint32_t>(M.np) * 64u;
                 const int at = j0 / 32, n = M.mp / 32 - at < BN / 32 ? M.mp / 32 - at : BN / 32;
-                fill_cols(b, T + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
+                const char *X = source(TH, TL, 2, s);
+                fill_cols(b, X + static_cast<int64_t>(at) * panel, n * panel, panel, s, u, lane);
             } else {
-                const char *A = KIND == kPoly ? at(ws, M.a) : T;
+                const char *A = source(KIND == kPoly ? at(ws, M.a) : T,
+                                       KIND == kPoly ? at(ws, M.al) : L, 2, s);
                 const int rq = KIND == kPoly ? M.mp : M.np, n = rq - j0 < BN ? rq - j0 : BN;
                 fill_rows(b, A + (static_cast<int64_t>(s) * rq + j0) * 64, n * 64u, u, lane);
             }
@@ -483,14 +531,6 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
             else q[set][y] = read_rows(t, base + perm_row(lane & 15, y & 1), lane);
         };
 
-        // stages of the sum, or of this part's stretch of it: a multiple of four
-        int steps = (kXXT ? M.np : M.mp) / kBK;
-        if constexpr (KIND == kGramPart) {
-            const int units = steps / NST, k = tl.part % split;
-            const int from = units * k / split, to = units * (k + 1) / split;
-            T += static_cast<int64_t>(from) * NST * 2048;
-            steps = (to - from) * NST;
-        }
 #pragma unroll
         for (int s = 0; s < NST - 1; ++s) {
 #pragma unroll
@@ -510,7 +550,7 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
             const uint32_t o = static_cast<uint32_t>(j) * 64u + 16u * g;
             hi = __builtin_bit_cast(f16x8, bload16<0>(T + panel, o, n32));
             lo = __builtin_bit_cast(
-                f16x8, bload16<0>(at(ws, M.lo) + panel, o, when & kHigh ? 0u : n32));
+                f16x8, bload16<0>(L + panel, o, when & kHigh ? 0u : n32));
         };
         auto add_x = [&](int n, const f16x8 &hi, const f16x8 &lo) {
             const float ca = ldexpf(coef.a, kLogA);
@@ -646,36 +686,59 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                 col[b] = kXXT ? 16 * b + (lane & 15) : perm_row(lane & 15, b);
                 row[b] = kXXT ? 16 * b + 4 * g : 8 * g + 4 * b;
             }
-            char *C = at(ws, kXXT ? M.a : M.b);
+            char *C = at(ws, kXXT ? M.a : M.b), *CL = at(ws, kXXT ? M.al : M.bl);
+            Half8 low[2];               // of A and B
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 float t[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] = alpha * acc[x + (e >> 2)][y + b][e & 3];
                 const int64_t o = panel_at(kSym ? M.mp : M.np, jb + col[b], ib + row[0]);
-                if constexpr (kXXT) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[b].f[e] = static_cast<_Float16>(t[e]);
-                    s16x4 *c = reinterpret_cast<s16x4 *>(C) + (o >> 2);
-                    c[0] = v[b].q[0];
-                    c[4] = v[b].q[1];
-                } else if constexpr (KIND == kPoly) {
-                    const f16x8 old = reinterpret_cast<const f16x8 *>(at(ws, M.a))[o >> 3];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[b].f[e] =
-                            static_cast<_Float16>(coef.b * static_cast<float>(old[e]) + t[e]);
-                    reinterpret_cast<f16x8 *>(C)[o >> 3] = v[b].f;
-                } else if constexpr (KIND == kApply) {
-                    f16x8 lo;
+                auto halves = [&](f16x8 &hi, f16x8 &lo) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float f = settled(t[e]);
-                        v[b].f[e] = static_cast<_Float16>(f);
-                        lo[e] = static_cast<_Float16>(f - static_cast<float>(v[b].f[e]));
+                        hi[e] = static_cast<_Float16>(f);
+                        lo[e] = static_cast<_Float16>(f - static_cast<float>(hi[e]));
                     }
+                };
+                if constexpr (kXXT) {
+                    auto put = [&](char *to, const Half8 &h) {
+                        s16x4 *c = reinterpret_cast<s16x4 *>(to) + (o >> 2);
+                        c[0] = h.q[0];
+                        c[4] = h.q[1];
+                    };
+                    if constexpr (kFine) {
+                        halves(v[b].f, low[b].f);
+                        put(CL, low[b]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[b].f[e] = static_cast<_Float16>(t[e]);
+                    }
+                    put(C, v[b]);
+                } else if constexpr (KIND == kPoly) {
+                    const f16x8 old = reinterpret_cast<const f16x8 *>(at(ws, M.a))[o >> 3];
+                    if constexpr (kFine) {
+                        const f16x8 rest = reinterpret_cast<const f16x8 *>(at(ws, M.al))[o >> 3];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            t[e] = coef.b * (static_cast<float>(old[e]) + static_cast<float>(rest[e])) +
+                                   t[e];
+                        halves(v[b].f, low[b].f);
+                        reinterpret_cast<f16x8 *>(CL)[o >> 3] = low[b].f;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[b].f[e] =
+                                static_cast<_Float16>(coef.b * static_cast<float>(old[e]) + t[e]);
+                    }
+                    reinterpret_cast<f16x8 *>(C)[o >> 3] = v[b].f;
+                } else if constexpr (KIND == kApply) {
+                    f16x8 lo;
+                    halves(v[b].f, lo);
                     reinterpret_cast<f16x8 *>(at(ws, src ? M.t[0] : M.t[1]))[o >> 3] = v[b].f;
-                    reinterpret_cast<f16x8 *>(at(ws, M.lo))[o >> 3] = lo;
+                    // other blocks read all of a low part that is an operand
+                    reinterpret_cast<f16x8 *>(at(ws, kFine && !src ? M.lo2 : M.lo))[o >> 3] = lo;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -684,7 +747,7 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
             }
             // the block turned over, through 2 KB of LDS: row ib + (lane & 31), its
             // columns 16 t + 8 (lane >> 5) .. + 8 in v[t]
-            if ((kSym && tl.ti != tl.tj) || (KIND == kLast && M.wide)) {
+            auto turn = [&](Half8(&v)[2]) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -697,15 +760,23 @@ __global__ __launch_bounds__(64 * WM *WN) void ortho_product_kernel(
                     v[t].q[0] = read_tr(a);
                     v[t].q[1] = read_tr(a + 4 * 64);
                 }
-            }
+            };
+            if ((kSym && tl.ti != tl.tj) || (KIND == kLast && M.wide)) turn(v);
             const int tr = ib + (lane & 31);
             if constexpr (kSym) {
                 // a tile off the diagonal is its mirror image's values too
                 if (tl.ti != tl.tj) {
+                    auto mirror = [&](char *to, const Half8(&v)[2]) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        reinterpret_cast<f16x8 *>(
-                            C)[panel_at(M.mp, tr, jb + 16 * t + 8 * (lane >> 5)) >> 3] = v[t].f;
+                        for (int t = 0; t < 2; ++t)
+                            reinterpret_cast<f16x8 *>(
+                                to)[panel_at(M.mp, tr, jb + 16 * t + 8 * (lane >> 5)) >> 3] = v[t].f;
+                    };
+                    mirror(C, v);
+                    if constexpr (kFine) {
+                        turn(low);
+                        mirror(CL, low);
+                    }
                 }
             } else if constexpr (KIND == kLast) {
                 // the row and the first of 8 neighbouring columns of the output
@@ -1275,27 +1346,36 @@ hipError_t launch_ortho_init(const OrthoTile *tiles, int64_t n, const OrthoMat *
 
 namespace {
 
-template <int KIND>
-hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
+template <int KIND, bool kFine>
+hipError_t launch_tiles(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
                           void *ws, int32_t src, int32_t when, int32_t split, OrthoCoef c,
                           hipStream_t st) {
     if (n == 0) return hipSuccess;
     const unsigned grid = static_cast<unsigned>(n);
     if (tile == 256)
-        ortho_product_kernel<KIND, 256, 256, 2, 4>
+        ortho_product_kernel<KIND, 256, 256, 2, 4, kFine>
             <<<grid, product_threads(256), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 192)
-        ortho_product_kernel<KIND, 192, 192, 6, 2>
+        ortho_product_kernel<KIND, 192, 192, 6, 2, kFine>
             <<<grid, product_threads(192), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 128)
-        ortho_product_kernel<KIND, 128, 128, 2, 2>
+        ortho_product_kernel<KIND, 128, 128, 2, 2, kFine>
             <<<grid, product_threads(128), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else if (tile == 64)
-        ortho_product_kernel<KIND, 64, 64, 2, 2>
+        ortho_product_kernel<KIND, 64, 64, 2, 2, kFine>
             <<<grid, product_threads(64), 0, st>>>(tiles, mats, ws, src, when, split, c);
     else
         return hipErrorInvalidValue;
     return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t launch_product(int32_t tile, const OrthoTile *tiles, int64_t n, const OrthoMat *mats,
+                          void *ws, int32_t src, int32_t when, int32_t split, OrthoCoef c,
+                          hipStream_t st) {
+    if (tile & kTileFine)
+        return launch_tiles<KIND, true>(tile & ~kTileFine, tiles, n, mats, ws, src, when, split, c, st);
+    return launch_tiles<KIND, false>(tile, tiles, n, mats, ws, src, when, split, c, st);
 }
 
 }  // namespace

@@ -3,7 +3,8 @@
 // Per matrix the workspace holds, for m = the smaller and n = the larger side
 // padded to mp and np (multiples of kOrthoPad, padding zero), X^T as fp16 high
 // and low parts ([np][mp]; the high part twice, read and written by turns) and
-// the m x m products A and B in fp16.  Where m is at most kSmallMax, and X has
+// the m x m products A and B in fp16; a fine plan has a low part of A and of B too,
+// and both parts of X^T twice.  Where m is at most kSmallMax, and X has
 // more columns than a block holds, it has the slabs' X^T, high and low, and two
 // sets of the slabs' parts of A in fp32.
 #pragma once
@@ -30,6 +31,7 @@ struct OrthoMat {
     uint16_t *out;       // [rows, cols] bf16
     int64_t t[2], lo;    // X^T: high parts, low part
     int64_t a, b;        // A, B
+    int64_t lo2, al, bl; // fine plans: the low part's other place, low parts of A and B
     int64_t parts;       // partial sums of squares (double), n_parts of them
     int64_t scal;        // float[4], see OrthoScal
     int64_t sums;        // fp32 parts of split sums, the plan's
@@ -37,6 +39,7 @@ struct OrthoMat {
     int32_t m, n, mp, np;
     int32_t n_parts, wide;  // wide: rows <= cols, X = U; else X = U^T
     int32_t n_sums, slab;   // few rows: parts of A that every block sums, columns of a slab
+    int32_t low, reserved;  // low: the start leaves a low part (fp32 inputs); set by bind
 };
 
 // What one init pass leaves for the products: the true X is phi0 times the
@@ -91,8 +94,9 @@ hipError_t launch_ortho_small(int32_t mp, const OrthoTile *tiles, int64_t n, con
 // tiles: (matrix, 256 x 4 elements of it, number of parts).
 hipError_t launch_ortho_sums(const OrthoTile *tiles, int64_t n, const OrthoMat *mats, void *ws,
                              int32_t step, hipStream_t st);
-// The products; tile: 256, 192, 128 or 64 rows and columns of a tile, any other
-// is hipErrorInvalidValue.
+// The products; tile: 256, 192, 128 or 64 rows and columns of a tile, plus kTileFine
+// for operands of two parts; any other is hipErrorInvalidValue.
+constexpr int32_t kTileFine = 1 << 12;
 // A = X X^T, tiles (ti >= tj) of the lower triangle; src: which high part is
 // read.  With split > 1 every tile comes split times (its part its place among
 // all parts), and join has each once, with its first part.

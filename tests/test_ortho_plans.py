@@ -16,7 +16,7 @@ NS = [(3.4445, -4.7750, 2.0315)] * 5
 ROCM_INCLUDE = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")
 
 
-def _harness(tmp_path, sources):
+def _harness(tmp_path, sources, host=("muon.cpp",)):
     """Build the sources with the library's host code under sanitizers and run them."""
     gxx = shutil.which("g++")
     if gxx is None or not os.path.isdir(os.path.join(ROCM_INCLUDE, "hip")):
@@ -24,7 +24,7 @@ def _harness(tmp_path, sources):
     out = str(tmp_path / "harness")
     srcs = [os.path.join(NATIVE, f) for f in sources]
     srcs += [os.path.join(CSRC, f) for f in ("capi.cpp", "plan.cpp", "reshard.cpp", "host_adamw.cpp",
-                                             "muon.cpp", "ortho.cpp")]
+                                             "ortho.cpp") + tuple(host)]
     cmd = [gxx, "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer",
            "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
            "-ffp-contract=off", "-D__HIP_PLATFORM_AMD__", "-I" + ROCM_INCLUDE,
@@ -41,6 +41,23 @@ def _harness(tmp_path, sources):
 
 def test_a_plan_keeps_the_dtype_of_its_first_bind(tmp_path):
     _harness(tmp_path, ["ortho_plan_harness.cpp", "fake_hip.cpp", "fake_launch.cpp", "fake_muon.cpp"])
+
+
+def test_plans_with_two_part_operands(tmp_path):
+    _harness(tmp_path, ["ortho_fine_harness.cpp", "fake_hip.cpp", "fake_launch.cpp"], host=())
+
+
+def test_products_are_named():
+    from sharded_shard_amd.group import Orthogonalizer
+    plans = [Orthogonalizer([(300, 400), (20, 30)], products=p) for p in ("fp16", "fp16x2")]
+    assert plans[0].workspace_bytes < plans[1].workspace_bytes
+    with pytest.raises(ValueError, match="fp16x2"):
+        Orthogonalizer([(300, 400)], products="fp32")
+    with pytest.raises(capi.FsdpError) as ei:
+        capi.fsdp_ortho_plan_set_products(plans[0].plan, -1)
+    assert ei.value.status == capi.FSDP_E_UNSUPPORTED
+    few = [Orthogonalizer([(100, 4000)], products=p) for p in ("fp16", "fp16x2")]
+    assert few[0].workspace_bytes == few[1].workspace_bytes
 
 
 def test_every_step_has_three_coefficients():
