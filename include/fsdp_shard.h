@@ -633,16 +633,16 @@ fsdp_status fsdp_ortho_plan_info(const fsdp_ortho_plan *plan, int32_t *n_mats,
 
 /* The operands of the products of matrices with more than 128 rows (the smaller
  * side); up to 128 rows they always have both parts.  Errors are those of the
- * result before its rounding to bf16, relative, in the 2-norm, for the default
- * coefficients.
+ * result before its rounding to bf16, relative, in the Frobenius norm, for the
+ * default coefficients.
  *   FSDP_ORTHO_FP16    the default: X, A and B rounded to fp16 once for each
  *           product.  Where these roundings are independent of each other, as for
- *           gradients, noise and falling spectra, the result is within 2e-3.
- *           Where many entries have the same magnitude they add up: to 8e-3 for
- *           a constant, signs of rank one, repeated or orthonormal rows or an
- *           identity, 1.7e-2 for two constants in blocks (the largest found).
- *           All roundings at their largest would be 3.2e-2 for a matrix of rank
- *           one.
+ *           gradients, noise and falling spectra, the result is within 2e-3 (3e-3
+ *           where all but a few rows, or most entries, are zero).  Where many
+ *           entries have the same magnitude they add up: to 8e-3 for a constant,
+ *           signs of rank one, repeated or orthonormal rows or an identity,
+ *           1.7e-2 for two constants in blocks (the largest found).  All
+ *           roundings at their largest would be 3.2e-2 for a matrix of rank one.
  *   FSDP_ORTHO_FP16X2  a high and a low fp16 part of each, 22 bits, in three
  *           products for each one: within 1e-4 on every matrix.  An execution
  *           takes 2.3 to 2.9 times as long, and the workspace grows by a half

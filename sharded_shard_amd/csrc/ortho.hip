@@ -12,7 +12,7 @@
 // singular value is still small is multiplied by a in every iteration, 3.4445^5
 // = 485 times in all, and so is whatever rounding X adds to it: with X held in
 // fp16 alone the result was 3.5e-3 off for a falling spectrum and 2.7e-2 for
-// one of low rank (relative, in the 2-norm; bf16 1e-2 to 0.2).  The term a X
+// one of low rank (relative, in the Frobenius norm; bf16 1e-2 to 0.2).  The term a X
 // therefore takes X as a high and a low fp16 part (22 bits); the products,
 // which vanish with the singular value, take the high part.  That leaves 3e-4
 // to 2e-3 on gradients, noise and falling spectra, where the roundings of X, A

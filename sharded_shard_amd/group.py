@@ -100,7 +100,7 @@ class Orthogonalizer:
     def allocate(self, workspace: Optional[torch.Tensor] = None, device: str = "cuda") -> None:
         """Use ``workspace``, or new memory of the current stream.  One that was
         there before is let go of once the device has finished with it."""
-        if self.workspace is not None:
+        if self.workspace is not None and self.workspace.is_cuda:
             # executions on any stream may be under way in it
             torch.cuda.synchronize(self.workspace.device)
         if workspace is None:

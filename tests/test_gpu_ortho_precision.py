@@ -3,7 +3,7 @@ and of two, on matrices whose roundings are independent and on ones whose
 roundings add up.
 
 Tolerance.  Let x be the result before its rounding to bf16, w the exact iterate
-and |x - w| <= e |w| in the 2-norm.  bf16(x) is the nearest value to x, so no
+and |x - w| <= e |w| in the Frobenius norm.  bf16(x) is the nearest value to x, so no
 element of it is further from x than bf16(w)'s is, and |bf16(x) - w| <= |bf16(w) -
 w| + 2 |x - w|: the first term is known from w, the second is at most 2 e |w|.
 
@@ -71,6 +71,11 @@ def matrix(shape, seed, kind, dtype):
     elif kind == "orthonormal":
         q = torch.linalg.qr(rand(max(r, c), min(r, c)))[0]
         x = q if r >= c else q.T
+    elif kind == "few":                  # rows that are not zero
+        x = torch.zeros(r, c, dtype=torch.float64)
+        x[:7] = rand(7, c)
+    elif kind == "sparse":
+        x = rand(r, c) * (torch.rand(r, c, generator=g, dtype=torch.float64) < 0.01)
     elif kind == "identity":
         x = torch.eye(r, c, dtype=torch.float64)
     else:                                # two constants in blocks
@@ -117,7 +122,7 @@ SHAPES = [(139, 140), (257, 260), (260, 257), (353, 356), (200, 333), (1024, 512
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("kind", KINDS + ["few", "sparse"])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "%dx%d" % s)
 def test_two_parts_are_right_on_every_matrix(shape, kind, dtype):
     u = matrix(shape, sum(shape), kind, dtype)
@@ -234,3 +239,32 @@ def test_two_parts_in_place_and_captured():
             b.execute()
             torch.cuda.synchronize()
         del graph
+
+
+@pytest.mark.parametrize("kind", ["noise", "falling", "blocks", "signs"])
+@pytest.mark.parametrize("shape", [(20, 30), (20, 2000), (2000, 31), (50, 400), (33, 1000), (1000, 64),
+                                   (128, 128), (97, 100), (100, 2000), (2000, 128), (70, 20000)],
+                         ids=lambda s: "%dx%d" % s)
+def test_fp32_inputs_of_few_rows(shape, kind):
+    """One slab and several of each of the three classes: 32, 64 and 128 rows."""
+    u = matrix(shape, sum(shape), kind, torch.float32)
+    err, rounding, norm = errors(run([u], "fp16")[0], u)
+    assert err <= rounding + 2 * FINE * norm
+
+
+# plans whose X X^T is split into parts in tiles of 256 and of 192
+@pytest.mark.parametrize("shape,count,products", [((1178, 6738), 5, "fp16"), ((1052, 5818), 6, "fp16"),
+                                                  ((2087, 1933), 2, "fp16x2"), ((1035, 1905), 6, "fp16x2")],
+                         ids=str)
+def test_split_sums_in_the_larger_tiles(shape, count, products):
+    r, c = shape
+    us = [matrix(shape, 13, "falling", torch.bfloat16), matrix((c, r), 14, "noise", torch.bfloat16)]
+    outs = run([us[i % 2] for i in range(count)], products)
+    for u, x in zip(us, outs):
+        err, rounding, norm = errors(x, u)
+        if products == "fp16":
+            assert err <= math.hypot(rounding, 4 * U * norm), u.shape
+        else:
+            assert err <= rounding + 2 * FINE * norm, u.shape
+    for i, x in enumerate(outs):
+        assert torch.equal(x, outs[i % 2]), i
