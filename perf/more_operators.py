@@ -1,0 +1,446 @@
+"""Training in 8 bits on Shard(0) parameter groups: what is timed and compared.
+
+Matrices are held in 8-bit floating point with a power of two for each block of 128: a block whose largest finite
+magnitude is a gets the smallest power s = 2^(byte - 127) with a <= fmax s (fmax 448 for e4m3, 57344 for e5m2; byte 0
+where nothing is left), and x is held as the code nearest to x / s, ties to even.  Blocks are 1 x 128 ("rows"),
+128 x 1 ("cols") or 128 x 128 ("tiles").  Three operators:
+
+* ``copy-in``: this rank's fp32 shards to its 8-bit all-gather segment, zeros in the padding.  Blocks are 128 x 128 of
+  the full matrix; the bytes of a rank's part of them come first (a collective takes their maximum over ranks), then
+  the codes.
+* ``checkpoint``: a matrix of activations or gradients to 8 bits, along rows (the operand of a product over columns),
+  along columns (what the weight gradient reads), or both in one pass; and back to 16 bits.
+* ``product``: y = x W^T, dx = dy W and dW = dy^T x of such matrices, 32-bit sums, rounded to bf16 or added to an
+  fp32 accumulator.
+
+``linear`` is a layer's whole step with them: y and, from the 8-bit checkpoint of x, dx and dW.
+
+``run`` computes them with elementary torch operations in 32 bits, or, where ``own`` is set, through the package's
+entry points; ``exact`` in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+FMAX = {"e4m3": 448.0, "e5m2": 57344.0}
+TYPE = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+# The matrices of the repository's workloads.
+PROBE = "32x16,4x32"
+BLOCK = "4096x4096*4,14336x4096*2,4096x14336"
+EXPERTS = "1408x2048*32,2048x1408*16,64x2048,1x2048"
+
+
+def listed():
+    return [
+        # the two-layer probe: a few hundred elements, all latency
+        {"name": "copy-in probe", "op": "copy-in", "shapes": PROBE, "world": 2, "rank": 0, "align": 1},
+        # one decoder block on 8 ranks
+        {"name": "copy-in block n8", "op": "copy-in", "shapes": BLOCK, "world": 8, "rank": 3, "align": 8},
+        # ragged experts on 6 ranks: blocks that two ranks share, short last chunks, empty pieces
+        {"name": "copy-in experts n6", "op": "copy-in", "shapes": EXPERTS, "world": 6, "rank": 5, "align": 1},
+        # one token on its way into a projection
+        {"name": "save one row", "op": "checkpoint", "rows": 1, "cols": 4096, "how": "rows", "fmt": "e4m3",
+         "f32": False},
+        # a batch of tokens: the operand of the forward product and the checkpoint for the backward pass
+        {"name": "save both 8192", "op": "checkpoint", "rows": 8192, "cols": 4096, "how": "both", "fmt": "e4m3",
+         "f32": False},
+        # an expert's ragged share of the tokens, back to 16 bits
+        {"name": "restore 4097x1408", "op": "checkpoint", "rows": 4097, "cols": 1408, "how": "restore cols",
+         "fmt": "e5m2", "f32": False},
+        # one token through an up projection: its weights are read, all else is small
+        {"name": "product one row", "op": "product", "form": "forward", "tokens": 1, "n": 14336, "k": 4096,
+         "fmt": "e4m3", "f32": False},
+        # a batch through the same projection
+        {"name": "product forward 8192", "op": "product", "form": "forward", "tokens": 8192, "n": 14336, "k": 4096,
+         "fmt": "e4m3", "f32": False},
+        # gradient of a down projection's input
+        {"name": "product input grad 8192", "op": "product", "form": "input", "tokens": 8192, "n": 4096, "k": 14336,
+         "fmt": "e5m2", "f32": False},
+        # gradient of a square projection's weights, added to the fp32 accumulator
+        {"name": "product weight grad 8191", "op": "product", "form": "weight", "tokens": 8191, "n": 4096, "k": 4096,
+         "fmt": "e4m3", "f32": True},
+        # one expert with the tokens that the router gave it
+        {"name": "linear expert 333", "op": "linear", "tokens": 333, "n": 1408, "k": 2048, "fmt": "e5m2",
+         "f32": False},
+        # a square projection of a decoder block
+        {"name": "linear square 8192", "op": "linear", "tokens": 8192, "n": 4096, "k": 4096, "fmt": "e4m3",
+         "f32": True},
+    ]
+
+
+def _log(rng, lo, hi):
+    """A whole number in [lo, hi], spread evenly over its logarithm."""
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def _width(rng, lo, hi):
+    """A matrix's side: a multiple of 64 more often than not, as the framework's are."""
+    n = _log(rng, lo, hi)
+    return n if rng.random() < 0.4 else -(-n // 64) * 64
+
+
+def draw(rng):
+    """One more case: any operator, from a few elements to a decoder block's."""
+    op = rng.choice(("copy-in", "checkpoint", "product", "product", "linear"))
+    fmt = rng.choice(("e4m3", "e4m3", "e5m2"))
+    if op == "copy-in":
+        world = rng.choice((1, 2, 4, 6, 8, 8, 16))
+        shapes = []
+        for _ in range(rng.randint(1, 4)):
+            cols, times = _width(rng, 1, 8192), rng.randint(1, 3)
+            most = 12_000_000 * world // (times * cols)       # elements of a rank's piece
+            shapes.append("%dx%d*%d" % (_log(rng, 1, max(1, min(8192, most))), cols, times))
+        return {"op": op, "shapes": ",".join(shapes), "world": world, "rank": rng.randrange(world),
+                "align": rng.choice((1, 8))}
+    if op == "checkpoint":
+        how = rng.choice(("rows", "cols", "both", "tiles", "restore rows", "restore cols", "restore tiles"))
+        return {"op": op, "rows": _log(rng, 1, 8192), "cols": _width(rng, 1, 4096), "how": how, "fmt": fmt,
+                "f32": rng.random() < 0.3}
+    tokens, n, k = _log(rng, 1, 8192), _width(rng, 16, 8192), _width(rng, 16, 8192)
+    f32 = rng.random() < 0.4
+    if op == "linear":
+        return {"op": op, "tokens": tokens, "n": n, "k": min(k, 4096), "fmt": fmt, "f32": f32}
+    return {"op": op, "form": rng.choice(("forward", "input", "weight")), "tokens": tokens, "n": n, "k": k,
+            "fmt": fmt, "f32": f32}
+
+
+# ---- inputs --------------------------------------------------------------------
+
+
+def _shapes(case):
+    out = []
+    for part in case["shapes"].split(","):
+        dims, _, times = part.partition("*")
+        r, c = dims.split("x")
+        out += [(int(r), int(c))] * int(times or 1)
+    return out
+
+
+def _pieces(case):
+    """This rank's piece of each matrix, as the group lays it out: (its rows, the first of them, the matrix's rows,
+    columns, elements in the segment, offset in the flat shards); then the segment's length, that of the flat shards
+    and the number of blocks.  Shards start at multiples of 64 elements."""
+    world, rank, align = case["world"], case["rank"], case["align"]
+    out, seg, flat, blocks = [], 0, 0, 0
+    for r, c in _shapes(case):
+        chunk = -(-r // world)
+        first = min(rank * chunk, r)
+        n = min((rank + 1) * chunk, r) - first
+        size = -(-chunk * c // align) * align
+        out.append((n, first, r, c, size, flat))
+        seg, flat, blocks = seg + size, flat + -(-n * c // 64) * 64, blocks + -(-r // 128) * -(-c // 128)
+    return out, seg, max(flat, 1), blocks
+
+
+def _activations(gen, rows, cols):
+    """Tokens of different size, and one channel in a hundred that stands out."""
+    x = torch.randn(rows, cols, generator=gen, device="cuda")
+    x *= torch.exp(0.5 * torch.randn(rows, 1, generator=gen, device="cuda"))
+    return x * (1 + 20 * (torch.rand(cols, generator=gen, device="cuda") < 0.01))
+
+
+def _gradients(gen, rows, cols):
+    """Small, and of very different size from token to token."""
+    x = torch.randn(rows, cols, generator=gen, device="cuda")
+    return x * (1e-4 * torch.exp(torch.randn(rows, 1, generator=gen, device="cuda")))
+
+
+def _weights(gen, rows, cols):
+    return 0.02 * torch.randn(rows, cols, generator=gen, device="cuda")
+
+
+def _held(x, how, fmt):
+    """x in 8 bits, as the package holds it."""
+    codes, scales = _quantized(x, how, fmt)
+    state = {"codes": codes, "scales": scales, "how": how, "fmt": fmt, "shape": tuple(x.shape)}
+    if own:
+        from sharded_shard_amd.q8 import Q8
+        state["q"] = Q8.empty(x.shape, how, fmt)
+        state["q"].codes_view().copy_(codes.view(torch.uint8))
+        state["q"].scales_view().copy_(scales)
+    return state
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    state = {"case": case}
+    if case["op"] == "copy-in":
+        pieces, seg, flat, blocks = _pieces(case)
+        state["pieces"] = pieces
+        state["p"] = 0.02 * torch.randn(flat, generator=gen, device="cuda")
+        # rows of different size: neighbouring blocks have different scales
+        state["p"] *= torch.exp(torch.randn(-(-flat // 512), 1, generator=gen, device="cuda")).expand(
+            -1, 512).reshape(-1)[:flat]
+        state["ag_in"] = torch.empty(seg, dtype=torch.uint8, device="cuda")
+        state["scales"] = torch.empty(blocks, dtype=torch.uint8, device="cuda")
+        if own:
+            from sharded_shard_amd.group import ShardedGroup
+            group = ShardedGroup(_shapes(case), case["world"], case["rank"], case["align"], bind=False)
+            group.master_flat = state["p"]
+            group.bind()
+            state["group"] = group
+        return state
+    if case["op"] == "checkpoint":
+        make = _gradients if case["fmt"] == "e5m2" else _activations
+        x = make(gen, case["rows"], case["cols"])
+        if case["how"].startswith("restore"):
+            state["held"] = _held(x, case["how"].split()[1], case["fmt"])
+        else:
+            state["x"] = x if case["f32"] else x.to(torch.bfloat16)
+        return state
+    t, n, k = case["tokens"], case["n"], case["k"]
+    if case["op"] == "linear":
+        state["x"] = _activations(gen, t, k).to(torch.bfloat16)
+        state["dy"] = _gradients(gen, t, n).to(torch.bfloat16)
+        state["w"] = _held(_weights(gen, n, k), "tiles", "e4m3")
+        state["dw"] = _gradients(gen, n, k) if case["f32"] else torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+        if own:
+            from sharded_shard_amd.q8 import Linear8
+            state["layer"] = Linear8(state["w"]["q"], grad_format=case["fmt"])
+        return state
+    if case["form"] == "forward":
+        state["a"] = _held(_activations(gen, t, k), "rows", case["fmt"])
+        state["b"] = _held(_weights(gen, n, k), "tiles", "e4m3")
+        shape = t, n
+    elif case["form"] == "input":
+        state["a"] = _held(_gradients(gen, t, n), "rows", case["fmt"])
+        state["b"] = _held(_weights(gen, n, k), "tiles", "e4m3")
+        shape = t, k
+    else:
+        state["a"] = _held(_gradients(gen, t, n), "cols", case["fmt"])
+        state["b"] = _held(_activations(gen, t, k), "cols", "e4m3")
+        shape = n, k
+    # an accumulator that holds other microbatches' sums, or a result of its own
+    state["out"] = _gradients(gen, *shape) if case["f32"] else torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    return state
+
+
+# ---- the plain forms -----------------------------------------------------------
+
+
+def _grid(x, top, how):
+    """x with `top` rows of zeros above it, filled up to whole blocks: [block rows, rows, block columns, columns]."""
+    r, c = (128 if how != "rows" else 1), (128 if how != "cols" else 1)
+    rows, cols = -(-(x.shape[0] + top) // r), -(-x.shape[1] // c)
+    full = torch.zeros(rows * r, cols * c, dtype=torch.float32, device=x.device)
+    full[top:top + x.shape[0], :x.shape[1]] = x
+    return full.view(rows, r, cols, c)
+
+
+def _bytes(grid, fmt):
+    """The scales' bytes of blocks, from the largest magnitude a = m 2^e, 1/2 <= m < 1: fmax is 7/8 of a power of two."""
+    a = grid.abs().amax((1, 3))
+    m, e = torch.frexp(a)
+    byte = e.long() - (9 if fmt == "e4m3" else 16) + (m > 0.875) + 127
+    return torch.where(a > 0, byte, 0).clamp_(min=0).to(torch.uint8)
+
+
+def _power(byte, sign=1):
+    return torch.exp2((byte.double() - 127) * sign).float()
+
+
+def _codes(grid, byte, fmt):
+    x = grid * _power(byte, -1)[:, None, :, None]
+    return x.to(TYPE[fmt]).view(grid.shape[0] * grid.shape[1], -1)
+
+
+def _quantized(x, how, fmt):
+    """Codes [rows, columns], and bytes: [blocks along a row, rows], [blocks along a column, columns] or those of tiles."""
+    grid = _grid(x, 0, how)
+    byte = _bytes(grid, fmt)
+    codes = _codes(grid, byte, fmt).view(torch.uint8)[:x.shape[0], :x.shape[1]].contiguous().view(TYPE[fmt])
+    return codes, byte.mT.contiguous() if how == "rows" else byte
+
+
+def _values(codes, scales, how):
+    """What codes stand for."""
+    s = _power(scales)
+    s = s.mT if how == "rows" else s
+    rows, cols = codes.shape
+    s = s if how == "rows" else s.repeat_interleave(128, 0)[:rows]
+    return codes.float() * (s if how == "cols" else s.repeat_interleave(128, 1)[:, :cols])
+
+
+def _of(held):
+    return _values(held["codes"], held["scales"], held["how"])
+
+
+def _copy_in(state):
+    grids = [_grid(state["p"][at:at + n * c].view(n, c), first % 128, "tiles")
+             for n, first, _, c, _, at in state["pieces"]]
+    bytes_ = [_bytes(g, "e4m3") for g in grids]
+    # the blocks above and below this rank's rows are other ranks'
+    all_bytes = [b for q, own_ in zip(state["pieces"], bytes_)
+                 for b in (own_.new_zeros(q[1] // 128 * own_.shape[1] if q[0] else -(-q[2] // 128) * -(-q[3] // 128)),
+                           own_.reshape(-1) if q[0] else own_.new_zeros(0),
+                           own_.new_zeros((-(-q[2] // 128) - q[1] // 128 - own_.shape[0]) * own_.shape[1]
+                                          if q[0] else 0))]
+    codes = [c for q, g, b in zip(state["pieces"], grids, bytes_)
+             for c in (_codes(g, b, "e4m3").view(torch.uint8)[q[1] % 128:q[1] % 128 + q[0], :q[3]].reshape(-1),
+                       b.new_zeros(q[4] - q[0] * q[3]))]
+    torch.cat(all_bytes, out=state["scales"])
+    torch.cat(codes, out=state["ag_in"])
+
+
+def _checkpoint(state):
+    case = state["case"]
+    if case["how"].startswith("restore"):
+        return _of(state["held"]).to(torch.float32 if case["f32"] else torch.bfloat16)
+    return [_quantized(state["x"], how, case["fmt"]) for how in _ways(case["how"])]
+
+
+def _ways(how):
+    return ("rows", "cols") if how == "both" else (how,)
+
+
+def _result(x, out, add):
+    """x rounded into `out`, or added to it."""
+    return out.add_(x) if add else out.copy_(x)
+
+
+def _product(state):
+    a, b = _of(state["a"]), _of(state["b"])
+    form = state["case"]["form"]
+    c = a @ b.mT if form == "forward" else a @ b if form == "input" else a.mT @ b
+    return _result(c, state["out"], state["case"]["f32"])
+
+
+def _linear(state):
+    fmt, w = state["case"]["fmt"], _of(state["w"])
+    x, dy = state["x"], state["dy"]
+    y = _values(*_quantized(x, "rows", "e4m3"), "rows") @ w.mT
+    dx = _values(*_quantized(dy, "rows", fmt), "rows") @ w
+    dw = _values(*_quantized(dy, "cols", fmt), "cols").mT @ _values(*_quantized(x, "cols", "e4m3"), "cols")
+    return y.to(torch.bfloat16), dx.to(torch.bfloat16), _result(dw, state["dw"], state["case"]["f32"])
+
+
+def run(state):
+    case = state["case"]
+    if case["op"] == "copy-in":
+        if own:
+            state["group"].block_scales(state["scales"])
+            state["group"].pack_fp8_blocks(state["ag_in"], state["scales"])
+        else:
+            _copy_in(state)
+        return state["ag_in"].view(torch.float8_e4m3fn), state["scales"]
+    if not own:
+        return {"checkpoint": _checkpoint, "product": _product, "linear": _linear}[case["op"]](state)
+    from sharded_shard_amd import q8
+    if case["op"] == "checkpoint":
+        if case["how"].startswith("restore"):
+            return q8.dequantize(state["held"]["q"], torch.float32 if case["f32"] else torch.bfloat16)
+        held = q8.quantize(state["x"], case["how"], case["fmt"])
+        return [(q.codes_view().view(TYPE[case["fmt"]]), q.scales_view())
+                for q in (held if case["how"] == "both" else (held,))]
+    if case["op"] == "product":
+        return q8.product(state["a"]["q"], state["b"]["q"], trans_a=case["form"] == "weight",
+                          trans_b=case["form"] == "forward", out=state["out"], accumulate=case["f32"])
+    y = state["layer"].forward(state["x"])
+    dx = state["layer"].backward(state["dy"], state["dw"], accumulate=case["f32"])
+    return y, dx, state["dw"]
+
+
+# ---- what a pass has to do, and what it has to give ----------------------------
+
+
+def _held_bytes(rows, cols, how):
+    return rows * cols + {"rows": rows * -(-cols // 128), "cols": -(-rows // 128) * cols,
+                          "tiles": -(-rows // 128) * -(-cols // 128)}[how]
+
+
+def work(case):
+    if case["op"] == "copy-in":
+        pieces, seg, _, blocks = _pieces(case)
+        valid = sum(p[0] * p[3] for p in pieces)
+        return {"bytes": 4 * valid + seg + blocks, "flops": 2 * valid}
+    if case["op"] == "checkpoint":
+        n, wide = case["rows"] * case["cols"], 4 if case["f32"] else 2
+        how = case["how"].split()[-1]
+        return {"bytes": n * wide + sum(_held_bytes(case["rows"], case["cols"], h) for h in _ways(how)),
+                "flops": 2 * n}
+    t, n, k = case["tokens"], case["n"], case["k"]
+    if case["op"] == "linear":
+        return {"bytes": 4 * t * k + 4 * t * n + _held_bytes(n, k, "tiles") + n * k * (8 if case["f32"] else 2),
+                "flops": 6 * t * n * k}
+    form = case["form"]
+    a = _held_bytes(t, k if form == "forward" else n, "cols" if form == "weight" else "rows")
+    b = _held_bytes(t, k, "cols") if form == "weight" else _held_bytes(n, k, "tiles")
+    out = {"forward": t * n, "input": t * k, "weight": n * k}[form]
+    return {"bytes": a + b + out * (8 if case["f32"] else 2), "flops": 2 * t * n * k}
+
+
+def _nearest(v, fmt):
+    """The 8-bit value nearest to v in 64 bits, |v| at most fmax: steps of 2^-3 (2^-2) of a binade, ties to even."""
+    bits, low = (3, -6) if fmt == "e4m3" else (2, -14)
+    binade = torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -200)))
+    binade -= (torch.exp2(binade) > v.abs()).double()      # log2 may round up to a whole number
+    step = torch.exp2(binade.clamp(min=low) - bits)
+    return torch.round(v / step) * step
+
+
+def _exponents(a, fmt):
+    """The smallest e >= -127 with a <= fmax 2^e."""
+    e = torch.ceil(torch.log2(a / FMAX[fmt])).nan_to_num(neginf=-127.0)
+    e += (a > FMAX[fmt] * torch.exp2(e)).double()          # log2 may be off at a whole number
+    e -= (a <= FMAX[fmt] * torch.exp2(e - 1)).double()
+    return e.clamp(min=-127)
+
+
+def _exact_held(x, how, fmt, top=0):
+    """Codes, exponents of the blocks, and the values, in 64 bits; block rows are counted from `top` rows above x."""
+    x = x.double()
+    r = torch.arange(top, top + x.shape[0], device=x.device) // (1 if how == "rows" else 128)
+    c = torch.arange(x.shape[1], device=x.device) // (1 if how == "cols" else 128)
+    shape = int(r[-1]) + 1, int(c[-1]) + 1
+    a = torch.zeros(shape[0], x.shape[1], dtype=torch.float64, device=x.device)
+    a.index_reduce_(0, r, x.abs(), "amax")
+    b = torch.zeros(shape, dtype=torch.float64, device=x.device).index_reduce_(1, c, a, "amax")
+    e = _exponents(b, fmt)
+    s = torch.exp2(e)[r][:, c]
+    code = _nearest(x / s, fmt)
+    return code, e, code * s
+
+
+def exact(case, seed):
+    state = prepare(case, seed)
+    if case["op"] == "copy-in":
+        codes, exps = [], []
+        for n, first, rows, c, size, at in state["pieces"]:
+            e = torch.full((-(-rows // 128), -(-c // 128)), -127.0, dtype=torch.float64, device="cuda")
+            if n:
+                code, got, _ = _exact_held(state["p"][at:at + n * c].view(n, c), "tiles", "e4m3", first % 128)
+                e[first // 128:first // 128 + len(got)] = got
+                codes.append(code.reshape(-1))
+            codes.append(torch.zeros(size - n * c, dtype=torch.float64, device="cuda"))
+            exps.append(e.reshape(-1))
+        return torch.cat(codes), (torch.cat(exps) + 127).to(torch.uint8)
+    if case["op"] == "checkpoint":
+        if case["how"].startswith("restore"):
+            return _exact_values(state["held"])
+        out = []
+        for how in _ways(case["how"]):
+            code, e, _ = _exact_held(state["x"], how, case["fmt"])
+            out.append((code, ((e.mT if how == "rows" else e) + 127).to(torch.uint8)))
+        return out
+    add = 1.0 if case["f32"] else 0.0
+    if case["op"] == "product":
+        a, b = _exact_values(state["a"]), _exact_values(state["b"])
+        c = a @ (b.T if case["form"] == "forward" else b) if case["form"] != "weight" else a.T @ b
+        return c + (state["out"].double() if add else 0.0)
+    fmt, w = case["fmt"], _exact_values(state["w"])
+    x, dy = state["x"], state["dy"]
+    y = _exact_held(x, "rows", "e4m3")[2] @ w.T
+    dx = _exact_held(dy, "rows", fmt)[2] @ w
+    dw = _exact_held(dy, "cols", fmt)[2].T @ _exact_held(x, "cols", "e4m3")[2]
+    return y, dx, dw + (state["dw"].double() if add else 0.0)
+
+
+def _exact_values(held):
+    codes, scales, how = held["codes"].double(), held["scales"].double(), held["how"]
+    r = torch.arange(codes.shape[0], device="cuda") // (1 if how == "rows" else 128)
+    c = torch.arange(codes.shape[1], device="cuda") // (1 if how == "cols" else 128)
+    e = (scales.T if how == "rows" else scales)[r][:, c]
+    return codes * torch.exp2(e - 127)
