@@ -10,8 +10,7 @@ where nothing is left), and x is held as the code nearest to x / s, ties to even
   the codes.
 * ``checkpoint``: a matrix of activations or gradients to 8 bits, along rows (the operand of a product over columns),
   along columns (what the weight gradient reads), or both in one pass; and back to 16 bits.
-* ``product``: y = x W^T, dx = dy W and dW = dy^T x of such matrices, 32-bit sums, rounded to bf16 or added to an
-  fp32 accumulator.
+* ``product``: y = x W^T, dx = dy W and dW = dy^T x of such matrices, 32-bit sums, rounded once to bf16.
 
 ``linear`` is a layer's whole step with them: y and, from the 8-bit checkpoint of x, dx and dW.
 
@@ -52,22 +51,20 @@ def listed():
          "fmt": "e5m2", "f32": False},
         # one token through an up projection: its weights are read, all else is small
         {"name": "product one row", "op": "product", "form": "forward", "tokens": 1, "n": 14336, "k": 4096,
-         "fmt": "e4m3", "f32": False},
+         "fmt": "e4m3"},
         # a batch through the same projection
         {"name": "product forward 8192", "op": "product", "form": "forward", "tokens": 8192, "n": 14336, "k": 4096,
-         "fmt": "e4m3", "f32": False},
+         "fmt": "e4m3"},
         # gradient of a down projection's input
         {"name": "product input grad 8192", "op": "product", "form": "input", "tokens": 8192, "n": 4096, "k": 14336,
-         "fmt": "e5m2", "f32": False},
-        # gradient of a square projection's weights, added to the fp32 accumulator
+         "fmt": "e5m2"},
+        # gradient of a square projection's weights
         {"name": "product weight grad 8191", "op": "product", "form": "weight", "tokens": 8191, "n": 4096, "k": 4096,
-         "fmt": "e4m3", "f32": True},
+         "fmt": "e4m3"},
         # one expert with the tokens that the router gave it
-        {"name": "linear expert 333", "op": "linear", "tokens": 333, "n": 1408, "k": 2048, "fmt": "e5m2",
-         "f32": False},
+        {"name": "linear expert 333", "op": "linear", "tokens": 333, "n": 1408, "k": 2048, "fmt": "e5m2"},
         # a square projection of a decoder block
-        {"name": "linear square 8192", "op": "linear", "tokens": 8192, "n": 4096, "k": 4096, "fmt": "e4m3",
-         "f32": True},
+        {"name": "linear square 8192", "op": "linear", "tokens": 8192, "n": 4096, "k": 4096, "fmt": "e4m3"},
     ]
 
 
@@ -100,11 +97,10 @@ def draw(rng):
         return {"op": op, "rows": _log(rng, 1, 8192), "cols": _width(rng, 1, 4096), "how": how, "fmt": fmt,
                 "f32": rng.random() < 0.3}
     tokens, n, k = _log(rng, 1, 8192), _width(rng, 16, 8192), _width(rng, 16, 8192)
-    f32 = rng.random() < 0.4
     if op == "linear":
-        return {"op": op, "tokens": tokens, "n": n, "k": min(k, 4096), "fmt": fmt, "f32": f32}
+        return {"op": op, "tokens": tokens, "n": n, "k": min(k, 4096), "fmt": fmt}
     return {"op": op, "form": rng.choice(("forward", "input", "weight")), "tokens": tokens, "n": n, "k": k,
-            "fmt": fmt, "f32": f32}
+            "fmt": fmt}
 
 
 # ---- inputs --------------------------------------------------------------------
@@ -196,7 +192,7 @@ def prepare(case, seed):
         state["x"] = _activations(gen, t, k).to(torch.bfloat16)
         state["dy"] = _gradients(gen, t, n).to(torch.bfloat16)
         state["w"] = _held(_weights(gen, n, k), "tiles", "e4m3")
-        state["dw"] = _gradients(gen, n, k) if case["f32"] else torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+        state["dw"] = torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
         if own:
             from sharded_shard_amd.q8 import Linear8
             state["layer"] = Linear8(state["w"]["q"], grad_format=case["fmt"])
@@ -213,8 +209,7 @@ def prepare(case, seed):
         state["a"] = _held(_gradients(gen, t, n), "cols", case["fmt"])
         state["b"] = _held(_activations(gen, t, k), "cols", "e4m3")
         shape = n, k
-    # an accumulator that holds other microbatches' sums, or a result of its own
-    state["out"] = _gradients(gen, *shape) if case["f32"] else torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    state["out"] = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
     return state
 
 
@@ -296,16 +291,11 @@ def _ways(how):
     return ("rows", "cols") if how == "both" else (how,)
 
 
-def _result(x, out, add):
-    """x rounded into `out`, or added to it."""
-    return out.add_(x) if add else out.copy_(x)
-
-
 def _product(state):
     a, b = _of(state["a"]), _of(state["b"])
     form = state["case"]["form"]
     c = a @ b.mT if form == "forward" else a @ b if form == "input" else a.mT @ b
-    return _result(c, state["out"], state["case"]["f32"])
+    return state["out"].copy_(c)
 
 
 def _linear(state):
@@ -314,7 +304,7 @@ def _linear(state):
     y = _values(*_quantized(x, "rows", "e4m3"), "rows") @ w.mT
     dx = _values(*_quantized(dy, "rows", fmt), "rows") @ w
     dw = _values(*_quantized(dy, "cols", fmt), "cols").mT @ _values(*_quantized(x, "cols", "e4m3"), "cols")
-    return y.to(torch.bfloat16), dx.to(torch.bfloat16), _result(dw, state["dw"], state["case"]["f32"])
+    return y.to(torch.bfloat16), dx.to(torch.bfloat16), state["dw"].copy_(dw)
 
 
 def run(state):
@@ -337,9 +327,9 @@ def run(state):
                 for q in (held if case["how"] == "both" else (held,))]
     if case["op"] == "product":
         return q8.product(state["a"]["q"], state["b"]["q"], trans_a=case["form"] == "weight",
-                          trans_b=case["form"] == "forward", out=state["out"], accumulate=case["f32"])
+                          trans_b=case["form"] == "forward", out=state["out"])
     y = state["layer"].forward(state["x"])
-    dx = state["layer"].backward(state["dy"], state["dw"], accumulate=case["f32"])
+    dx = state["layer"].backward(state["dy"], state["dw"])
     return y, dx, state["dw"]
 
 
@@ -363,13 +353,13 @@ def work(case):
                 "flops": 2 * n}
     t, n, k = case["tokens"], case["n"], case["k"]
     if case["op"] == "linear":
-        return {"bytes": 4 * t * k + 4 * t * n + _held_bytes(n, k, "tiles") + n * k * (8 if case["f32"] else 2),
+        return {"bytes": 4 * t * k + 4 * t * n + _held_bytes(n, k, "tiles") + 2 * n * k,
                 "flops": 6 * t * n * k}
     form = case["form"]
     a = _held_bytes(t, k if form == "forward" else n, "cols" if form == "weight" else "rows")
     b = _held_bytes(t, k, "cols") if form == "weight" else _held_bytes(n, k, "tiles")
     out = {"forward": t * n, "input": t * k, "weight": n * k}[form]
-    return {"bytes": a + b + out * (8 if case["f32"] else 2), "flops": 2 * t * n * k}
+    return {"bytes": a + b + 2 * out, "flops": 2 * t * n * k}
 
 
 def _nearest(v, fmt):
@@ -425,17 +415,15 @@ def exact(case, seed):
             code, e, _ = _exact_held(state["x"], how, case["fmt"])
             out.append((code, ((e.mT if how == "rows" else e) + 127).to(torch.uint8)))
         return out
-    add = 1.0 if case["f32"] else 0.0
     if case["op"] == "product":
         a, b = _exact_values(state["a"]), _exact_values(state["b"])
-        c = a @ (b.T if case["form"] == "forward" else b) if case["form"] != "weight" else a.T @ b
-        return c + (state["out"].double() if add else 0.0)
+        return a @ (b.T if case["form"] == "forward" else b) if case["form"] != "weight" else a.T @ b
     fmt, w = case["fmt"], _exact_values(state["w"])
     x, dy = state["x"], state["dy"]
     y = _exact_held(x, "rows", "e4m3")[2] @ w.T
     dx = _exact_held(dy, "rows", fmt)[2] @ w
     dw = _exact_held(dy, "cols", fmt)[2].T @ _exact_held(x, "cols", "e4m3")[2]
-    return y, dx, dw + (state["dw"].double() if add else 0.0)
+    return y, dx, dw
 
 
 def _exact_values(held):
