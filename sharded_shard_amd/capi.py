@@ -35,6 +35,12 @@ FSDP_ROLE_FULL_FP8 = 128
 
 FSDP_DTYPE_BF16 = 0
 FSDP_DTYPE_F32 = 1
+FSDP_Q8_E4M3 = 0
+FSDP_Q8_E5M2 = 1
+FSDP_Q8_TENSOR = 0
+FSDP_Q8_ROWS = 1
+FSDP_Q8_COLS = 2
+FSDP_Q8_TILES = 3
 FSDP_ORTHO_FP16 = 0
 FSDP_ORTHO_FP16X2 = 1
 
@@ -81,6 +87,13 @@ class MuonHparams(ctypes.Structure):
                 ("weight_decay", ctypes.c_double), ("nesterov", _i32), ("reserved", _i32)]
 
 
+class Q8Struct(ctypes.Structure):
+    """fsdp_q8_t: a matrix in 8 bits with a power of two for each block of 128."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("divisor", ctypes.c_void_p), ("rows", _i64), ("cols", _i64), ("ld", _i64),
+                ("pitch", _i64), ("format", _i32), ("blocks", _i32)]
+
+
 class FsdpError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} [{status}]")
@@ -102,6 +115,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
+_Q8 = ctypes.POINTER(Q8Struct)
 
 _SIGS = {
     "fsdp_abi_version": (_i32, []),
@@ -163,6 +177,13 @@ _SIGS = {
     "fsdp_ortho_bind": (_i32, [_P, _PP, _PP, _i32, _P]),
     "fsdp_ortho_execute": (_i32, [_P, _P, _i64, _P]),
     "fsdp_ortho_plan_destroy": (None, [_P]),
+    "fsdp_q8_quantize": (_i32, [_P, _i32, _i64, _Q8, _Q8, _P]),
+    "fsdp_q8_dequantize": (_i32, [_Q8, _P, _i32, _i64, _P]),
+    "fsdp_q8_product_workspace": (_i32, [_Q8, _i32, _Q8, _i32, ctypes.POINTER(_i64)]),
+    "fsdp_q8_product": (_i32, [_Q8, _i32, _Q8, _i32, _P, _i64, _P, _i64, _P]),
+    "fsdp_plan_block_scales": (_i32, [_P, _i32, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
+    "fsdp_block_scales_shard": (_i32, [_P, _P, _P]),
+    "fsdp_pack_allgather_fp8_blocks": (_i32, [_P, _P, _P, _P]),
     "fsdp_check_stream": (_i32, [_P]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -732,6 +753,64 @@ def fsdp_ortho_execute(plan, workspace, workspace_bytes=None, stream=None) -> No
 
 def fsdp_ortho_plan_destroy(plan) -> None:
     lib.fsdp_ortho_plan_destroy(plan)
+
+
+# ---- 8-bit matrices ------------------------------------------------------------------
+
+def fsdp_q8_quantize(x, dtype: int, ldx: int, a: Q8Struct, b=None, stream=None) -> None:
+    """x: an address, or a tensor whose layout the caller has checked."""
+    _check(lib.fsdp_q8_quantize(addr(x), dtype, ldx, ctypes.byref(a),
+                                ctypes.byref(b) if b is not None else None,
+                                stream_handle(stream)), "fsdp_q8_quantize")
+
+
+def fsdp_q8_dequantize(q: Q8Struct, out, dtype: int, ldo: int, stream=None) -> None:
+    _check(lib.fsdp_q8_dequantize(ctypes.byref(q), addr(out), dtype, ldo, stream_handle(stream)),
+           "fsdp_q8_dequantize")
+
+
+def fsdp_q8_product_workspace(a: Q8Struct, trans_a: int, b: Q8Struct, trans_b: int) -> int:
+    n = _i64()
+    _check(lib.fsdp_q8_product_workspace(ctypes.byref(a), trans_a, ctypes.byref(b), trans_b,
+                                         ctypes.byref(n)), "fsdp_q8_product_workspace")
+    return n.value
+
+
+def fsdp_q8_product(a: Q8Struct, trans_a: int, b: Q8Struct, trans_b: int, out, ldo: int,
+                    workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """workspace: a tensor, or an address of workspace_bytes bytes."""
+    if hasattr(workspace, "data_ptr"):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+        workspace = _dev(workspace, 0, "workspace")
+    _check(lib.fsdp_q8_product(ctypes.byref(a), trans_a, ctypes.byref(b), trans_b, addr(out), ldo,
+                               addr(workspace), workspace_bytes, stream_handle(stream)),
+           "fsdp_q8_product")
+
+
+def fsdp_plan_block_scales(plan, i: int):
+    """(offset, total): where parameter i's block scales start, and the bytes of all."""
+    o, t = _i64(), _i64()
+    _check(lib.fsdp_plan_block_scales(plan, i, ctypes.byref(o), ctypes.byref(t)),
+           "fsdp_plan_block_scales")
+    return o.value, t.value
+
+
+def _scales_dev(plan, scales) -> int:
+    ok = _dims(plan) is not None
+    return _dev(scales, fsdp_plan_block_scales(plan, 0)[1], "scales") if ok else addr(scales)
+
+
+def fsdp_block_scales_shard(plan, scales, stream=None) -> None:
+    _check(lib.fsdp_block_scales_shard(plan, _scales_dev(plan, scales), stream_handle(stream)),
+           "fsdp_block_scales_shard")
+
+
+def fsdp_pack_allgather_fp8_blocks(plan, ag_in, scales, stream=None) -> None:
+    d = _dims(plan)
+    a = _dev(ag_in, d[1], "ag_in") if d else addr(ag_in)
+    _check(lib.fsdp_pack_allgather_fp8_blocks(plan, a, _scales_dev(plan, scales),
+                                              stream_handle(stream)),
+           "fsdp_pack_allgather_fp8_blocks")
 
 
 def fsdp_check_stream(stream=None) -> None:

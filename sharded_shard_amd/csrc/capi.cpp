@@ -109,11 +109,12 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     const size_t n = p->L.entries.size();
     std::vector<int64_t> own;
     for (const fsdp_shard_entry_t &t : p->L.entries) own.push_back(t.row_begin * t.cols);
+    const fsdp::Blocks blocks = fsdp::blocks_of(p->L);
     struct Table {
         void **dst;
         const void *src;
         size_t bytes;
-    } tabs[8] = {
+    } tabs[10] = {
         {reinterpret_cast<void **>(&p->d_entries), nullptr, n * sizeof(fsdp::DevEntry)},
         {reinterpret_cast<void **>(&p->d_pack), p->L.pack.data(),
          p->L.pack.size() * sizeof(fsdp::PackTile)},
@@ -128,6 +129,10 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
         {reinterpret_cast<void **>(&p->d_full), p->L.full.data(),
          p->L.full.size() * sizeof(fsdp::EwTile)},
         {reinterpret_cast<void **>(&p->d_own), own.data(), own.size() * sizeof(int64_t)},
+        {reinterpret_cast<void **>(&p->d_blocks), blocks.entries.data(),
+         blocks.entries.size() * sizeof(fsdp::BlockEntry)},
+        {reinterpret_cast<void **>(&p->d_cells), blocks.cells.data(),
+         blocks.cells.size() * sizeof(fsdp::BlockCell)},
     };
     const bool first = p->dmem == nullptr;
     if (first) {
@@ -151,7 +156,7 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     // (hot calls then fail with FSDP_E_STATE) rather than half-updated.
     const int32_t prev = p->bound;
     p->bound = 0;
-    const int n_tabs = p->tiles_uploaded ? 1 : 8;
+    const int n_tabs = p->tiles_uploaded ? 1 : 10;
     for (int k = 0; k < n_tabs; ++k) {
         if (tabs[k].bytes == 0) continue;
         const void *src = k == 0 ? static_cast<const void *>(ents.data()) : tabs[k].src;
@@ -161,6 +166,8 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     e = hipStreamSynchronize(st);
     if (e != hipSuccess) return hip_fail(e, (c + ": upload").c_str());
     p->tiles_uploaded = true;
+    p->n_cells = static_cast<int64_t>(blocks.cells.size());
+    p->n_block_scales = blocks.total;
     p->host_entries = std::move(ents);
     p->bound = prev | roles;
     return FSDP_OK;

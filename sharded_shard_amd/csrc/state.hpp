@@ -10,6 +10,7 @@
 
 #include "../../include/fsdp_shard.h"
 #include "plan.hpp"
+#include "q8.hpp"
 
 struct fsdp_plan {
     fsdp::Layout L;
@@ -26,6 +27,9 @@ struct fsdp_plan {
     fsdp::EwTile *d_adamw = nullptr;
     fsdp::EwTile *d_full = nullptr;
     int64_t *d_own = nullptr;     // per parameter: element offset of this rank's rows
+    fsdp::BlockEntry *d_blocks = nullptr;   // per parameter: its 128 x 128 blocks
+    fsdp::BlockCell *d_cells = nullptr;     // this rank's part of each block
+    int64_t n_cells = 0, n_block_scales = 0;
 };
 
 namespace fsdp {

@@ -160,6 +160,7 @@ class ShardedGroup:
             capi.fsdp_plan_destroy(self.plan)
             raise
         self.S, self.V, self.F = self.info.S, self.info.V, self.info.F
+        self.n_block_scales = capi.fsdp_plan_block_scales(self.plan, 0)[1]
         self.device = torch.device(device)
         offs, o = [], 0
         for e in self.entries:
@@ -274,6 +275,23 @@ class ShardedGroup:
 
     def unpack_fp8(self, ag_out, stream=None) -> None:
         capi.fsdp_unpack_allgather_fp8(self.plan, ag_out, stream)
+
+    def block_scales(self, out, stream=None) -> None:
+        """This rank's scale byte of every 128 x 128 block into ``out`` [n_block_scales]
+        (uint8); the maximum over ranks is what ``pack_fp8_blocks`` takes."""
+        capi.fsdp_block_scales_shard(self.plan, out, stream)
+
+    def pack_fp8_blocks(self, ag_in, scales, stream=None) -> None:
+        capi.fsdp_pack_allgather_fp8_blocks(self.plan, ag_in, scales, stream)
+
+    def full_q8(self, i: int, scales):
+        """Parameter i's gathered FP8 matrix with its blocks' ``scales`` [n_block_scales],
+        for ``q8.product`` and ``q8.Linear8``."""
+        from .q8 import Q8
+        at = capi.fsdp_plan_block_scales(self.plan, i)[0]
+        down, across = -(-self.rows[i] // 128), -(-self.cols[i] // 128)
+        return Q8(self.full_fp8_view(i), scales[at:at + down * across].view(down, across),
+                  "tiles", "e4m3")
 
     def amax(self, out, stream=None) -> None:
         capi.fsdp_amax_shard(self.plan, out, stream)
