@@ -69,42 +69,54 @@ __device__ __forceinline__ int spread(int r) {
 
 constexpr uint32_t kPastAll = 0x7FFFFFF0u;
 
-__device__ __forceinline__ void load_lds(const char *base, uint32_t nbytes, uint32_t voff,
-                                         lds_char *to) {
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, nbytes, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, voff, 0, 0, 0);
-}
+// This wave's share of an operand's image, W rows (or columns) of results and one
+// step of the sum: loads of 1 KB each straight into LDS, every WAVES-th one.  Rows,
+// columns and elements past the matrix become zeros, whole 16 bytes at a time.
+template <bool kCol, int W, bool kSpread, int WAVES>
+struct Filler {
+    static constexpr int kLoads = W / 8 / WAVES;
+    static_assert(W / 8 % WAVES == 0 && WAVES % 2 == 0, "whole loads; chunks the same for all");
+    const char *base;
+    uint32_t voff, ld, nbytes;      // of load 0 and element 0; rows past the matrix lie past nbytes
+    int K, chunk;
 
-// Load u (1 KB) of an operand's image for the step from element k0 of the sum.
-// Rows, columns and elements past the matrix become zeros, whole 16 bytes at a
-// time.
-template <bool kCol, int W, bool kSpread>
-__device__ __forceinline__ void fill(lds_char *dst, const Operand &O, int i0, int k0, int K, int u,
-                                     int lane) {
-    if constexpr (!kCol) {
-        const int rho = 8 * u + (lane >> 3), c = (lane & 7) ^ swz_row(rho);
-        const int row = kSpread ? spread(rho) : rho, left = O.n - i0;
-        const bool in = row < left && k0 + 16 * c < K;
-        const uint32_t voff = static_cast<uint32_t>(row) * static_cast<uint32_t>(O.ld) + k0 + 16 * c;
-        const int rows = left < W ? left : W;
-        const uint32_t nbytes =
-            static_cast<uint32_t>(rows - 1) * static_cast<uint32_t>(O.ld) + ((K + 15) & ~15);
-        load_lds(O.codes + static_cast<int64_t>(i0) * O.ld, nbytes, in ? voff : kPastAll,
-                 dst + u * 1024);
-    } else {
-        constexpr int kChunks = W / 16, kRows = 1024 / W;
-        const int k = u * kRows + lane / kChunks, c = lane % kChunks ^ swz_col<W>(k);
+    __device__ __forceinline__ Filler(const Operand &O, int i0, int K_, int wave, int lane)
+        : ld(static_cast<uint32_t>(O.ld)), K(K_) {
         const int left = O.n - i0;
-        const bool in = k0 + k < K && 16 * c < left;
-        const uint32_t voff = static_cast<uint32_t>(k) * static_cast<uint32_t>(O.ld) + 16 * c;
-        const int rows = K - k0 < kBK ? K - k0 : kBK;
-        const uint32_t nbytes =
-            static_cast<uint32_t>(rows - 1) * static_cast<uint32_t>(O.ld) + ((left + 15) & ~15);
-        load_lds(O.codes + static_cast<int64_t>(k0) * O.ld + i0, nbytes, in ? voff : kPastAll,
-                 dst + u * 1024);
+        if constexpr (!kCol) {
+            const int rho = 8 * wave + (lane >> 3);
+            chunk = 16 * ((lane & 7) ^ swz_row(rho));
+            voff = static_cast<uint32_t>(kSpread ? spread(rho) : rho) * ld + chunk;
+            base = O.codes + static_cast<int64_t>(i0) * O.ld;
+            nbytes = static_cast<uint32_t>((left < W ? left : W) - 1) * ld + ((K + 15) & ~15);
+        } else {
+            constexpr int kChunks = W / 16, kRows = 1024 / W;
+            const int k = wave * kRows + lane / kChunks, c = 16 * (lane % kChunks ^ swz_col<W>(k));
+            chunk = 0;
+            voff = c < left ? static_cast<uint32_t>(k) * ld + c : kPastAll;
+            base = O.codes + i0;
+            nbytes = static_cast<uint32_t>((left + 15) & ~15);
+        }
     }
-}
+    // load t of step s
+    __device__ __forceinline__ void load(lds_char *image, int s, int t, int wave) const {
+        const int k0 = s * kBK;
+        const char *b = base;
+        uint32_t n = nbytes, o;
+        if constexpr (!kCol) {
+            const int rows = kSpread ? spread(t * 8 * WAVES) : t * 8 * WAVES;
+            o = k0 + chunk < K ? voff + (static_cast<uint32_t>(rows) * ld + k0) : kPastAll;
+        } else {
+            b += static_cast<int64_t>(k0) * ld;
+            n += static_cast<uint32_t>((K - k0 < kBK ? K - k0 : kBK) - 1) * ld;
+            o = voff + static_cast<uint32_t>(t * WAVES * (1024 / W)) * ld;
+        }
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(b), 0, n, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r, (lds_void *)(image + (t * WAVES + wave) * 1024), 16, o, 0, 0, 0);
+    }
+};
 
 // 16 rows (results) and 128 elements of the sum: lane l has row l & 15 and the
 // 16-byte chunks l >> 4 and 4 + (l >> 4) of it, whichever form it comes from.
@@ -146,18 +158,6 @@ __device__ __forceinline__ i32x8 read_cols(lds_char *t, int col0, int lane) {
 // scales
 // ---------------------------------------------------------------------------
 
-// Scales of step kb for four results from i, i a multiple of 4.
-template <bool kCol>
-__device__ __forceinline__ uint32_t load_scales(const Operand &O, int kb, int i) {
-    if (O.blocks == FSDP_Q8_TENSOR || i >= O.n) return 0x7F7F7F7Fu;
-    if (O.blocks == FSDP_Q8_TILES) {
-        const int64_t at = kCol ? static_cast<int64_t>(kb) * O.pitch + (i >> 7)
-                                : static_cast<int64_t>(i >> 7) * O.pitch + kb;
-        return O.scales[at] * 0x01010101u;
-    }
-    return *reinterpret_cast<const uint32_t *>(O.scales + static_cast<int64_t>(kb) * O.pitch + i);
-}
-
 // Of 128 results' scales in LDS, byte x of the pair is that of this lane's row of
 // the x-th 16.
 __device__ __forceinline__ i32x2 spread_scales(lds_char *t, int lane) {
@@ -193,11 +193,25 @@ __device__ __forceinline__ void for_each(F &&f) {
     }
 }
 
+// The tile of this block.  Blocks go round-robin over the 8 XCDs; each XCD takes a
+// stretch of an order in which eight rows of tiles are worked off column by column,
+// so that what its blocks read at a time fits its L2.
+__device__ __forceinline__ void tile_of(int tiles_m, int tiles_n, int &ti, int &tj) {
+    constexpr int kRows = 8;
+    const int n = tiles_m * tiles_n, b = blockIdx.x, xcd = b & 7, per = n >> 3, rem = n & 7;
+    const int t = xcd * per + (xcd < rem ? xcd : rem) + (b >> 3);
+    const int group = t / (kRows * tiles_n), first = group * kRows;
+    const int rows = tiles_m - first < kRows ? tiles_m - first : kRows;
+    const int at = t - first * tiles_n;
+    ti = first + at % rows;
+    tj = at / rows;
+}
+
 // n neighbouring results of row i from column j.
 template <int n, typename F>
-__device__ __forceinline__ void store(const Out &o, float f, int i, int j, int M, int N, F &&get) {
+__device__ __forceinline__ void store(const Out &o, float f, int part, int i, int j, int M, int N, F &&get) {
     if (o.sums != nullptr) {
-        float *p = o.sums + (static_cast<int64_t>(blockIdx.z) * M + i) * N + j;
+        float *p = o.sums + (static_cast<int64_t>(part) * M + i) * N + j;
         const bool vec = j + n <= N && (N & 3) == 0;
 #pragma unroll
         for (int e = 0; e < n; e += 4) {
@@ -231,43 +245,65 @@ __device__ __forceinline__ void store(const Out &o, float f, int i, int j, int M
     }
 }
 
+// The scales of an operand's W results, four a lane and one dword a step: as they lie,
+// or a 128 x 128 block's one byte four times over.
+template <int W>
+struct ScaleLoader {
+    const uint8_t *base;
+    int64_t step;
+    uint32_t voff, select, add, bits;
+    __device__ __forceinline__ ScaleLoader(const Operand &O, bool col, int i0, int lane) {
+        int i = 4 * (lane % (W / 4));
+        i = i0 + i < O.n ? i : (O.n - 1 - i0) & ~3;
+        base = O.scales, step = 0, voff = 0, select = 0x0C0C0C0Cu, add = 0u, bits = 0u;
+        if (O.blocks == FSDP_Q8_TENSOR) {       // 2^0, whatever lies there
+            base = reinterpret_cast<const uint8_t *>(O.codes);
+            bits = 0x7F7F7F7Fu;
+        } else if (O.blocks == FSDP_Q8_TILES) {
+            base += col ? i0 >> 7 : static_cast<int64_t>(i0 >> 7) * O.pitch;
+            voff = static_cast<uint32_t>(i >> 7) * (col ? 1u : static_cast<uint32_t>(O.pitch));
+            step = col ? O.pitch : 1, select = 0u, add = 0x01010101u;
+        } else {
+            base += i0;
+            voff = i, step = O.pitch, select = 0x03020100u;
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void border() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// One BM x BN tile a block, WM x WN waves of FM x 4 results of 16 x 16 each.  Two
+// images in LDS.  A step's products are made in two halves of the wave's rows i.
+// During the first half the second half's rows are read, after which the step's
+// image is free; at the border in the middle every wave has them in registers
+// and the next step's image has landed; during the second half the next step's
+// first rows and, as their last products are made, its columns are read, and the
+// step after it starts on its way into the freed image.
 template <int BM, int BN, int WM, int WN, bool kColA, bool kColB, int FMTA>
-__global__ __launch_bounds__(64 * WM *WN) void q8_product_kernel(Operand A, Operand B, Out out,
-                                                                 int K) {
+__global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, Operand B, Out out,
+                                                                    int K) {
     constexpr int WAVES = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
-    constexpr int kScales = (BM < 128 ? 128 : BM) + (BN < 128 ? 128 : BN) + 128;
+    constexpr int HM = FM / 2;
     constexpr int kStage = (BM + BN) * kBK;
-    static_assert(FN % 4 == 0 && FM <= 8 && FN <= 8, "");
+    // scales in LDS: 128 bytes may be read past a wave's own
+    constexpr int kScalesB = BM + 128, kScales = kScalesB + BN + 128;
+    static_assert(FN == 4 && FM % 2 == 0 && FM <= 8, "");
     __shared__ __attribute__((aligned(1024))) char smem[2 * kStage + 2 * kScales];
     lds_char *lds = (lds_char *)smem;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN, g = lane >> 4;
-    const int i0 = blockIdx.x * BM, j0 = blockIdx.y * BN;
+    const int tiles_m = (A.n + BM - 1) / BM, tiles_n = (B.n + BN - 1) / BN;
+    int ti, tj;
+    tile_of(tiles_m, tiles_n, ti, tj);
+    const int i0 = ti * BM, j0 = tj * BN, part = blockIdx.y;
     const int all = (K + kBK - 1) / kBK;
-    const int from = static_cast<int>(static_cast<int64_t>(all) * blockIdx.z / out.split);
-    const int to = static_cast<int>(static_cast<int64_t>(all) * (blockIdx.z + 1) / out.split);
-
-    auto image = [&](int s) { return lds + (s & 1) * kStage; };
-    auto scales = [&](int s) { return lds + 2 * kStage + (s & 1) * kScales; };
-    constexpr int kScalesB = BM < 128 ? 128 : BM;
-    auto fill_step = [&](int s) {
-#pragma unroll
-        for (int u = 0; u < (BM / 8 + WAVES - 1) / WAVES; ++u)
-            if (u * WAVES + wave < BM / 8)
-                fill<kColA, BM, false>(image(s), A, i0, s * kBK, K, u * WAVES + wave, lane);
-#pragma unroll
-        for (int u = 0; u < (BN / 8 + WAVES - 1) / WAVES; ++u)
-            if (u * WAVES + wave < BN / 8)
-                fill<kColB, BN, !kColB>(image(s) + BM * kBK, B, j0, s * kBK, K, u * WAVES + wave,
-                                        lane);
-    };
-    const int tid = threadIdx.x;
-    auto step_scales = [&](int s) {
-        if (tid < BM / 4) return load_scales<kColA>(A, s, i0 + 4 * tid);
-        if (tid < BM / 4 + BN / 4) return load_scales<kColB>(B, s, j0 + 4 * (tid - BM / 4));
-        return 0u;
-    };
+    // at most 2^15 steps, in far fewer stretches than 2^16
+    const int from = static_cast<int>(static_cast<uint32_t>(all * part) / static_cast<uint32_t>(out.split));
+    const int to = static_cast<int>(static_cast<uint32_t>(all * (part + 1)) / static_cast<uint32_t>(out.split));
 
     f32x4 acc[FM][FN];
 #pragma unroll
@@ -275,55 +311,141 @@ __global__ __launch_bounds__(64 * WM *WN) void q8_product_kernel(Operand A, Oper
 #pragma unroll
         for (int y = 0; y < FN; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (from < to) fill_step(from);
-    uint32_t sc = from < to ? step_scales(from) : 0u;
-    for (int s = from; s < to; ++s) {
-        if (tid < BM / 4 + BN / 4)
-            *(lds_u32 *)(scales(s) + (tid < BM / 4 ? 4 * tid : kScalesB + 4 * (tid - BM / 4))) = sc;
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (s + 1 < to) {
-            fill_step(s + 1);
-            sc = step_scales(s + 1);
-        }
-        lds_char *ta = image(s), *tb = ta + BM * kBK;
-        if ((!kColA || !kColB) && s == all - 1 && (K & 15) != 0) {
-            // what follows the sum's last element in its 16 bytes is no part of it
+    if (from < to) {
+        const Filler<kColA, BM, false, WAVES> fa(A, i0, K, wave, lane);
+        const Filler<kColB, BN, !kColB, WAVES> fb(B, j0, K, wave, lane);
+        constexpr int kLA = decltype(fa)::kLoads, kLB = decltype(fb)::kLoads;
+        // even waves put a's scales into LDS, odd ones b's, all of them over and over:
+        // no branch
+        const bool of_a = (wave & 1) == 0;
+        const ScaleLoader<BM> la(A, kColA, i0, lane);
+        const ScaleLoader<BN> lb(B, kColB, j0, lane);
+        const uint8_t *sbase = of_a ? la.base : lb.base;
+        const int64_t sstep = of_a ? la.step : lb.step;
+        const uint32_t svoff = of_a ? la.voff : lb.voff, sselect = of_a ? la.select : lb.select,
+                       sadd = of_a ? la.add : lb.add, sbits = of_a ? la.bits : lb.bits;
+        const int sat = 2 * kStage + 4 * (of_a ? lane % (BM / 4) : kScalesB / 4 + lane % (BN / 4));
+        uint32_t sw, ssel;
+        auto load_scales = [&](int s) {
+            const uint8_t *p = sbase + s * sstep + svoff;
+            ssel = sselect + (lo32(p) & 3u) * sadd;
+            sw = *reinterpret_cast<const uint32_t *>(p - (lo32(p) & 3u));
+        };
+        auto put_scales = [&](int s) {
+            *(lds_u32 *)(lds + sat + (s & 1) * kScales) = __builtin_amdgcn_perm(sw, sw, ssel) | sbits;
+        };
+        auto image = [&](int s) { return lds + (s & 1) * kStage; };
+        auto read_p = [&](int s, int x) {
+            lds_char *t = image(s);
+            if constexpr (kColA) return read_cols<BM>(t, wm * WTM + 16 * x, lane);
+            else return read_rows(t, wm * WTM + 16 * x, lane);
+        };
+        auto read_q = [&](int s, int y) {
+            lds_char *t = image(s) + BM * kBK;
+            if constexpr (kColB) return read_cols<BN>(t, wn * WTN + 16 * y, lane);
+            else return read_rows(t, wn * WTN + 16 * y, lane);
+        };
+        auto read_sa = [&](int s) {
+            return spread_scales(lds + 2 * kStage + (s & 1) * kScales + wm * WTM, lane);
+        };
+        auto read_sb = [&](int s) {
+            lds_char *t = lds + 2 * kStage + (s & 1) * kScales + kScalesB + wn * WTN;
+            if constexpr (kColB) return spread_scales(t, lane).x;
+            else return static_cast<int>(*(const lds_u32 *)(t + 4 * (lane & 15)));
+        };
+        // what follows the sum's last element in its 16 bytes is no part of it
+        auto cut_tail = [&](int s) {
+            if ((kColA && kColB) || s != all - 1 || (K & 15) == 0) return;
             const int c = (K & 127) >> 4, keep = K & 15;
-            for (int r = tid; r < (kColA ? 0 : BM) + (kColB ? 0 : BN); r += 64 * WAVES) {
-                const int row = !kColA && r < BM ? r : r - (kColA ? 0 : BM);
-                lds_char *p = (!kColA && r < BM ? ta : tb) + row * 128 + (c ^ swz_row(row)) * 16;
+            constexpr int kRowsA = kColA ? 0 : BM, kRowsB = kColB ? 0 : BN;
+            for (int r = tid; r < kRowsA + kRowsB; r += 64 * WAVES) {
+                const bool of_a = r < kRowsA;
+                const int row = of_a ? r : r - kRowsA;
+                lds_char *p = image(s) + (of_a ? 0 : BM * kBK) + row * 128 + (c ^ swz_row(row)) * 16;
                 for (int b = keep; b < 16; ++b) p[b] = 0;
             }
-            __syncthreads();
-        }
+            border<0>();
+        };
+
+        load_scales(from);
+#pragma unroll
+        for (int t = 0; t < kLA; ++t) fa.load(image(from), from, t, wave);
+#pragma unroll
+        for (int t = 0; t < kLB; ++t) fb.load(image(from) + BM * kBK, from, t, wave);
+        put_scales(from);
+        border<0>();
+        cut_tail(from);
         i32x8 p[FM], q[FN];
-        const i32x2 sa = spread_scales(scales(s) + wm * WTM, lane);
-        int sb[2];
-        if constexpr (kColB) {
-            const i32x2 t = spread_scales(scales(s) + kScalesB + wn * WTN, lane);
-            sb[0] = t.x;
-            sb[1] = t.y;
-        } else {
+        i32x2 sa = read_sa(from);
+        int sb = read_sb(from);
 #pragma unroll
-            for (int h = 0; h < FN / 4; ++h)
-                sb[h] = *(const lds_u32 *)(scales(s) + kScalesB + wn * WTN + 64 * h + 4 * (lane & 15));
-        }
+        for (int x = 0; x < HM; ++x) p[x] = read_p(from, x);
 #pragma unroll
-        for (int x = 0; x < FM; ++x) {
-            if constexpr (kColA) p[x] = read_cols<BM>(ta, wm * WTM + 16 * x, lane);
-            else p[x] = read_rows(ta, wm * WTM + 16 * x, lane);
-        }
+        for (int y = 0; y < FN; ++y) q[y] = read_q(from, y);
+        if (from + 1 < to) {
+            load_scales(from + 1);
 #pragma unroll
-        for (int y = 0; y < FN; ++y) {
-            if constexpr (kColB) q[y] = read_cols<BN>(tb, wn * WTN + 16 * y, lane);
-            else q[y] = read_rows(tb, wn * WTN + 16 * y, lane);
+            for (int t = 0; t < kLA; ++t) fa.load(image(from + 1), from + 1, t, wave);
+#pragma unroll
+            for (int t = 0; t < kLB; ++t)
+                fb.load(image(from + 1) + BM * kBK, from + 1, t, wave);
         }
+
         auto mma = [&](auto xc, auto yc) {
             constexpr int x = decltype(xc)::value, y = decltype(yc)::value;
             acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                q[y], p[x], acc[x][y], 0, FMTA, y & 3, sb[y >> 2], x & 3, x < 4 ? sa.x : sa.y);
+                q[y], p[x], acc[x][y], 0, FMTA, y, sb, x & 3, x < 4 ? sa.x : sa.y);
         };
-        for_each<FM>([&](auto xc) { for_each<FN>([&](auto yc) { mma(xc, yc); }); });
+        // kMore: steps that follow, 2 for two and more
+        auto step = [&](int s, auto more) {
+            constexpr int kMore = decltype(more)::value;
+            // columns y outermost: the first products need the first columns alone
+            for_each<HM * FN>([&](auto nc) {
+                constexpr int n = decltype(nc)::value, y = n / HM, x = n % HM;
+                mma(Int<x>{}, Int<y>{});
+                // the second half's rows, one operand at a time, in the first products' time
+                if constexpr (n < HM) p[HM + n] = read_p(s, HM + n);
+                if constexpr (n == HM && kMore > 0) put_scales(s + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            i32x2 sa2 = sa;
+            int sb2 = sb;
+            if constexpr (kMore > 0) {
+                border<0>();
+                if constexpr (kMore == 1) cut_tail(s + 1);
+                sa2 = read_sa(s + 1);
+                sb2 = read_sb(s + 1);
+                if constexpr (kMore > 1) load_scales(s + 2);
+            }
+            for_each<HM * FN>([&](auto nc) {
+                constexpr int n = decltype(nc)::value, y = n / HM, x = n % HM;
+                mma(Int<HM + x>{}, Int<y>{});
+                if constexpr (kMore > 0) {
+                    if constexpr (n < HM) p[n] = read_p(s + 1, n);
+                    if constexpr (x == HM - 1) q[y] = read_q(s + 1, y);
+                }
+                if constexpr (kMore > 1) {
+                    // the loads, spread over the half
+                    constexpr int kL = kLA + kLB, lo = n * kL / (HM * FN),
+                                  hi = (n + 1) * kL / (HM * FN);
+                    for_each<hi - lo>([&](auto tc) {
+                        constexpr int t = lo + decltype(tc)::value;
+                        if constexpr (t < kLA) fa.load(image(s + 2), s + 2, t, wave);
+                        else fb.load(image(s + 2) + BM * kBK, s + 2, t - kLA, wave);
+                    });
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            sa = sa2;
+            sb = sb2;
+        };
+        int s = from;
+        for (; s + 2 < to; ++s) step(s, Int<2>{});
+        if (s + 1 < to) {
+            step(s, Int<1>{});
+            ++s;
+        }
+        step(s, Int<0>{});
     }
 
     // Row i of the results; this lane's columns: 16 neighbouring ones of every 64, or
@@ -336,15 +458,12 @@ __global__ __launch_bounds__(64 * WM *WN) void q8_product_kernel(Operand A, Oper
             if constexpr (kColB) {
                 for_each<FN>([&](auto yc) {
                     constexpr int y = decltype(yc)::value;
-                    store<4>(out, f, i, j0 + wn * WTN + 16 * y + 4 * g, A.n, B.n,
+                    store<4>(out, f, part, i, j0 + wn * WTN + 16 * y + 4 * g, A.n, B.n,
                              [&](int e) { return acc[x][y][e]; });
                 });
             } else {
-                for_each<FN / 4>([&](auto hc) {
-                    constexpr int h = decltype(hc)::value;
-                    store<16>(out, f, i, j0 + wn * WTN + 64 * h + 16 * g, A.n, B.n,
-                              [&](int e) { return acc[x][4 * h + (e & 3)][e >> 2]; });
-                });
+                store<16>(out, f, part, i, j0 + wn * WTN + 16 * g, A.n, B.n,
+                          [&](int e) { return acc[x][e & 3][e >> 2]; });
             }
         }
     });
@@ -387,19 +506,19 @@ unsigned blocks_for(int64_t n) {
 template <int BM, int BN, int WM, int WN>
 void launch(const Operand &A, bool ta, const Operand &B, bool tb, int format, const Out &out, int K,
             hipStream_t st) {
-    const dim3 grid((A.n + BM - 1) / BM, (B.n + BN - 1) / BN, out.split);
-    constexpr int kThreads = 64 * WM * WN;
-    auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, st>>>(A, B, out, K); };
+    const dim3 grid((A.n + BM - 1) / BM * ((B.n + BN - 1) / BN), out.split);
     const bool e4 = format == FSDP_Q8_E4M3;
+    void (*kernel)(Operand, Operand, Out, int) = nullptr;
     if (!ta && tb)
-        e4 ? go(q8_product_kernel<BM, BN, WM, WN, false, false, 0>)
-           : go(q8_product_kernel<BM, BN, WM, WN, false, false, 1>);
+        kernel = e4 ? q8_product_kernel<BM, BN, WM, WN, false, false, 0>
+                    : q8_product_kernel<BM, BN, WM, WN, false, false, 1>;
     else if (!ta)
-        e4 ? go(q8_product_kernel<BM, BN, WM, WN, false, true, 0>)
-           : go(q8_product_kernel<BM, BN, WM, WN, false, true, 1>);
+        kernel = e4 ? q8_product_kernel<BM, BN, WM, WN, false, true, 0>
+                    : q8_product_kernel<BM, BN, WM, WN, false, true, 1>;
     else
-        e4 ? go(q8_product_kernel<BM, BN, WM, WN, true, true, 0>)
-           : go(q8_product_kernel<BM, BN, WM, WN, true, true, 1>);
+        kernel = e4 ? q8_product_kernel<BM, BN, WM, WN, true, true, 0>
+                    : q8_product_kernel<BM, BN, WM, WN, true, true, 1>;
+    kernel<<<grid, 64 * WM * WN, 0, st>>>(A, B, out, K);
 }
 
 int64_t round16(int64_t x) { return (x + 15) & ~int64_t{15}; }
@@ -414,7 +533,7 @@ bool aligned(const Q8Mat &m) {
 Q8Cut q8_cut(const Q8Mat &a, bool ta, const Q8Mat &b, bool tb) {
     const int M = ta ? a.cols : a.rows, N = tb ? b.rows : b.cols;
     Q8Cut c{};
-    c.tile = M <= 64 || N <= 64 ? 1 : 0;
+    c.tile = M <= 64 || N <= 64 ? 2 : M <= 128 || N <= 128 ? 1 : 0;
     c.split = 1;
     c.bytes_a = aligned(a) ? 0 : round256(round16(a.cols) * a.rows);
     c.bytes_b = aligned(b) ? 0 : round256(round16(b.cols) * b.rows);
@@ -441,7 +560,8 @@ hipError_t launch_q8_product(const Q8Mat &a, bool ta, const Q8Mat &b, bool tb, u
     const Operand A = operand(a, cut.bytes_a, M), B = operand(b, cut.bytes_b, N);
     Out out{p, cut.split > 1 ? reinterpret_cast<float *>(at) : nullptr, a.divisor, b.divisor, ldo,
             cut.split};
-    if (cut.tile == 0) launch<128, 128, 2, 2>(A, ta, B, tb, a.format, out, K, st);
+    if (cut.tile == 0) launch<256, 256, 2, 4>(A, ta, B, tb, a.format, out, K, st);
+    else if (cut.tile == 1) launch<128, 128, 2, 2>(A, ta, B, tb, a.format, out, K, st);
     else launch<64, 64, 2, 1>(A, ta, B, tb, a.format, out, K, st);
     if (cut.split > 1)
         q8_join_kernel<<<blocks_for(static_cast<int64_t>(M) * N), kBlock, 0, st>>>(out, M, N);
