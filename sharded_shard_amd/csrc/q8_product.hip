@@ -247,32 +247,17 @@ __device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// n neighbouring results of row i from column j, one by one where they must be.
-template <int n, typename F>
-__device__ __forceinline__ void store(const Out &o, float f, int part, int i, int j, int M, int N,
-                                      F &&get) {
+// Four neighbouring fp32 sums of row i from column j.
+__device__ __forceinline__ void store_sums(const Out &o, int part, int i, int j, int M, int N,
+                                           const f32x4 &v) {
     if (i >= M) return;
-    if (o.sums != nullptr) {
-        float *p = o.sums + (static_cast<int64_t>(part) * M + i) * N + j;
-        const bool vec = j + n <= N && (N & 3) == 0;
+    float *p = o.sums + (static_cast<int64_t>(part) * M + i) * N + j;
+    if (j + 4 <= N && (N & 3) == 0) {
+        *reinterpret_cast<f32x4 *>(p) = v;
+    } else {
 #pragma unroll
-        for (int e = 0; e < n; e += 4) {
-            if (vec) {
-                *reinterpret_cast<f32x4 *>(p + e) = f32x4{get(e), get(e + 1), get(e + 2), get(e + 3)};
-            } else {
-#pragma unroll
-                for (int t = e; t < e + 4; ++t)
-                    if (j + t < N) p[t] = get(t);
-            }
-        }
-        return;
-    }
-    uint16_t *p = o.p + static_cast<int64_t>(i) * o.ld + j;
-#pragma unroll
-    for (int e = 0; e < n; e += 2) {
-        const uint32_t w = two_bf16(get(e) * f, get(e + 1) * f);
-        if (j + e < N) p[e] = static_cast<uint16_t>(w);
-        if (j + e + 1 < N) p[e + 1] = static_cast<uint16_t>(w >> 16);
+        for (int e = 0; e < 4; ++e)
+            if (j + e < N) p[e] = v[e];
     }
 }
 
@@ -424,7 +409,7 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
     constexpr int kYoung = 1 + 2 * kLP + kLQ;
     // Stores of a tile's results, at least: those that follow what the first border
     // after them waits for.
-    constexpr int kStores = 2 * HM * (kColB ? 4 : 2);
+    constexpr int kStores = 2 * HM * 2;
     static_assert(kYoung + kStores < 64, "the counter's range");
     i32x2 sa, sa2;
     int sb, sb2;
@@ -471,10 +456,26 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
         sb = sb2;
     };
     const float f = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(factor(out))));
-    // results of one row a vector store takes
-    constexpr int kVec = kColB ? 4 : 8;
-    const bool vec = out.sums == nullptr && (B.n & (kVec - 1)) == 0 && (out.ld & (kVec - 1)) == 0 &&
-                     (lo32(out.p) & (2 * kVec - 1)) == 0;
+    const bool vec = out.sums == nullptr && (B.n & 7) == 0 && (out.ld & 7) == 0 &&
+                     (lo32(out.p) & 15u) == 0;
+    // This lane's results of row x: twice eight neighbouring columns, from first(y).
+    auto first = [&](int y, int g) {
+        return wn * WTN + 32 * y + (kColB ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
+    };
+    auto eight = [&](auto xc, auto yc) {
+        constexpr int x = decltype(xc)::value, y = decltype(yc)::value;
+        const f32x4 &a = acc[x][2 * y], &b = acc[x][2 * y + 1];
+        auto two = [&](const f32x4 &c, int e) { return two_bf16(c[e] * f, c[e + 1] * f); };
+        u32x4 w{two(a, 0), two(a, 2), two(b, 0), two(b, 2)};
+        if constexpr (kColB) {
+            // Four columns of each 16 and lane: of two lanes 16 apart, one takes the eight of
+            // the first 16, the other those of the second.
+            const auto s = __builtin_amdgcn_permlane16_swap(w.x, w.z, false, false);
+            const auto t = __builtin_amdgcn_permlane16_swap(w.y, w.w, false, false);
+            w = u32x4{s[0], t[0], s[1], t[1]};
+        }
+        return w;
+    };
     auto results = [&](const Item &o) {
         const int i0 = o.ti * BM, j0 = o.tj * BN, l = anew(), g = l >> 4;
         if (vec) {
@@ -488,19 +489,10 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
             for_each<2 * HM>([&](auto xc) {
                 constexpr int x = decltype(xc)::value;
                 const uint32_t i = x / HM * HALF + (wm * HM + x % HM) * 16 + (l & 15);
-                for_each<kColB ? FN : FN / 2>([&](auto yc) {
-                    constexpr int y = decltype(yc)::value;
-                    const int j = wn * WTN + (kColB ? 16 * y + 4 * g : 32 * y + 8 * g);
+                for_each<2>([&](auto yc) {
+                    const int j = first(decltype(yc)::value, g);
                     const uint32_t at = j < cols ? i * ld + j * 2u : 0xFFFFFFF0u;
-                    auto two = [&](const f32x4 &a, int e) { return two_bf16(a[e] * f, a[e + 1] * f); };
-                    if constexpr (kColB) {
-                        const f32x4 &a = acc[x][y];
-                        __builtin_amdgcn_raw_buffer_store_b64(u32x2{two(a, 0), two(a, 2)}, r, at, 0, 0);
-                    } else {
-                        const f32x4 &a = acc[x][2 * y], &b = acc[x][2 * y + 1];
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            u32x4{two(a, 0), two(a, 2), two(b, 0), two(b, 2)}, r, at, 0, 0);
-                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(eight(xc, yc), r, at, 0, 0);
                 });
             });
             return;
@@ -508,14 +500,24 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
         for_each<2 * HM>([&](auto xc) {
             constexpr int x = decltype(xc)::value;
             const int i = i0 + x / HM * HALF + (wm * HM + x % HM) * 16 + (l & 15);
-            for_each<kColB ? FN : FN / 2>([&](auto yc) {
-                constexpr int y = decltype(yc)::value;
-                const int j = j0 + wn * WTN + (kColB ? 16 * y + 4 * g : 32 * y + 8 * g);
-                store<kVec>(out, f, o.part, i, j, A.n, B.n, [&](int e) {
-                    if constexpr (kColB) return acc[x][y][e];
-                    else return acc[x][2 * y + (e >> 2)][e & 3];
+            if (out.sums != nullptr) {
+                // fours of columns, as they come
+                for_each<FN>([&](auto yc) {
+                    constexpr int y = decltype(yc)::value;
+                    const int j = j0 + wn * WTN +
+                                  (kColB ? 16 * y + 4 * g : 32 * (y >> 1) + 8 * g + 4 * (y & 1));
+                    store_sums(out, o.part, i, j, A.n, B.n, acc[x][y]);
                 });
-            });
+            } else {
+                for_each<2>([&](auto yc) {
+                    const u32x4 w = eight(xc, yc);
+                    const int j = j0 + first(decltype(yc)::value, g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (i < A.n && j + e < B.n)
+                            out.p[i * out.ld + j + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+                });
+            }
         });
         // fewer stores than kStores perhaps
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
