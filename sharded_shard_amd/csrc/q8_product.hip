@@ -555,16 +555,133 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
     }
 }
 
-// The stretches' sums in order.
-__global__ __launch_bounds__(kBlock) void q8_join_kernel(Out out, int M, int N) {
-    const int64_t n = static_cast<int64_t>(M) * N;
+// ---------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------
+
+// Up to 16 FM rows by b transposed: b is read once, which bounds the time (58.7 MB for
+// one row by 14336 x 4096), and nothing in LDS would be read twice.  A block has 16 FN
+// columns, and each of its eight waves every eighth step of the sum, so that many
+// loads are under way however few columns there are; the waves' sums meet in LDS, in
+// their order.
+constexpr int kFewWaves = 8;
+
+// The scale of a row at step s, one byte.
+__device__ __forceinline__ int few_scale(const Operand &O, int i, int s) {
+    if (O.blocks == FSDP_Q8_TENSOR) return 127;
+    const int64_t at = O.blocks == FSDP_Q8_TILES ? (i >> 7) * O.pitch + s
+                                                 : static_cast<int64_t>(s) * O.pitch + i;
+    return O.scales[at];
+}
+
+template <int FM, int FN, int FMTA>
+__global__ __launch_bounds__(64 * kFewWaves) void q8_few_kernel(Operand A, Operand B, Out out, int K) {
+    __shared__ __attribute__((aligned(16))) f32x4 sums[kFewWaves][FM * FN][64];
+    const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int j0 = blockIdx.x * 16 * FN, steps = (K + kBK - 1) / kBK;
+    // rows past the matrix are read as its last one; what comes of them is dropped
+    const char *row_a[FM], *row_b[FN];
+    int ia[FM], ib[FN];
+#pragma unroll
+    for (int x = 0; x < FM; ++x) {
+        ia[x] = 16 * x + j < A.n ? 16 * x + j : A.n - 1;
+        row_a[x] = A.codes + ia[x] * A.ld;
+    }
+#pragma unroll
+    for (int y = 0; y < FN; ++y) {
+        ib[y] = j0 + 16 * y + j < B.n ? j0 + 16 * y + j : B.n - 1;
+        row_b[y] = B.codes + ib[y] * B.ld;
+    }
+    struct Step {
+        Frag a[FM], b[FN];
+        int sa[FM], sb[FN];
+    };
+    // chunks past the sum are zeros
+    auto load = [&](Step &t, int s) {
+        const int k = s * kBK + 16 * g;
+        const bool in0 = k < K, in1 = k + 64 < K;
+        const int k1 = in1 ? k + 64 : 0, kk = in0 ? k : 0;
+        auto one = [&](const char *row) {
+            Frag f;
+            f.h[0] = *reinterpret_cast<const i32x4 *>(row + kk);
+            f.h[1] = *reinterpret_cast<const i32x4 *>(row + k1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f.h[0][e] = in0 ? f.h[0][e] : 0;
+                f.h[1][e] = in1 ? f.h[1][e] : 0;
+            }
+            return f;
+        };
+#pragma unroll
+        for (int y = 0; y < FN; ++y) t.b[y] = one(row_b[y]), t.sb[y] = few_scale(B, ib[y], s);
+#pragma unroll
+        for (int x = 0; x < FM; ++x) t.a[x] = one(row_a[x]), t.sa[x] = few_scale(A, ia[x], s);
+    };
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int x = 0; x < FM; ++x)
+#pragma unroll
+        for (int y = 0; y < FN; ++y) acc[x][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // two steps' loads at a time
+    for (int s = wave; s < steps; s += 2 * kFewWaves) {
+        Step t[2];
+        const int s1 = s + kFewWaves < steps ? s + kFewWaves : s;
+        load(t[0], s);
+        load(t[1], s1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h == 1 && s1 == s) break;
+#pragma unroll
+            for (int x = 0; x < FM; ++x)
+#pragma unroll
+                for (int y = 0; y < FN; ++y)
+                    acc[x][y] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        t[h].b[y].v, t[h].a[x].v, acc[x][y], 0, FMTA, 0, t[h].sb[y], 0, t[h].sa[x]);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < FM; ++x)
+#pragma unroll
+        for (int y = 0; y < FN; ++y) sums[wave][x * FN + y][lane] = acc[x][y];
+    __syncthreads();
+    // Row 16 x + j of the results, columns 4 g .. + 4 of the y-th 16.
     const float f = factor(out);
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; i < n;
+    for (int u = tid; u < FM * FN * 64; u += 64 * kFewWaves) {
+        const int n = u >> 6, l = u & 63;
+        f32x4 v = sums[0][n][l];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) v += sums[w][n][l];
+        const int i = n / FN * 16 + (l & 15), c = j0 + n % FN * 16 + (l >> 4) * 4;
+        if (i >= A.n) continue;
+        uint16_t *p = out.p + i * out.ld + c;
+        const uint32_t lo = two_bf16(v[0] * f, v[1] * f), hi = two_bf16(v[2] * f, v[3] * f);
+        if (c + 4 <= B.n && (lo32(out.p) & 7u) == 0 && (out.ld & 3) == 0) {
+            *reinterpret_cast<u32x2 *>(p) = u32x2{lo, hi};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < B.n) p[e] = static_cast<uint16_t>((e < 2 ? lo : hi) >> (16 * (e & 1)));
+        }
+    }
+}
+
+// The stretches' sums in order, four neighbouring results a thread where rows are
+// whole fours.
+template <int n>
+__global__ __launch_bounds__(kBlock) void q8_join_kernel(Out out, int M, int N) {
+    typedef float vec __attribute__((ext_vector_type(n)));
+    const int64_t all = static_cast<int64_t>(M) * N / n;
+    const float f = factor(out);
+    const vec *sums = reinterpret_cast<const vec *>(out.sums);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x; i < all;
          i += static_cast<int64_t>(gridDim.x) * kBlock) {
-        float s = out.sums[i];
-        for (int k = 1; k < out.split; ++k) s += out.sums[k * n + i];
-        const int64_t row = i / N;
-        out.p[row * out.ld + (i - row * N)] = static_cast<uint16_t>(bf16_rne(s * f));
+        vec s = sums[i];
+        for (int k = 1; k < out.split; ++k) s += sums[k * all + i];
+        const int64_t row = i * n / N;
+        uint16_t *p = out.p + row * out.ld + (i * n - row * N);
+#pragma unroll
+        for (int e = 0; e < n; ++e) p[e] = static_cast<uint16_t>(two_bf16(s[e] * f, 0.0f));
     }
 }
 
@@ -622,6 +739,15 @@ void launch(const Operand &A, bool ta, const Operand &B, bool tb, int format, co
     kernel<<<grid, 64 * WM * WN, 0, st>>>(A, B, out, K);
 }
 
+template <int FM, int FN>
+void launch_few(const Operand &A, const Operand &B, int format, const Out &out, int K,
+                hipStream_t st) {
+    const int grid = (B.n + 16 * FN - 1) / (16 * FN);
+    void (*kernel)(Operand, Operand, Out, int) =
+        format == FSDP_Q8_E4M3 ? q8_few_kernel<FM, FN, 0> : q8_few_kernel<FM, FN, 1>;
+    kernel<<<grid, 64 * kFewWaves, 0, st>>>(A, B, out, K);
+}
+
 int64_t round16(int64_t x) { return (x + 15) & ~int64_t{15}; }
 int64_t round256(int64_t x) { return (x + 255) & ~int64_t{255}; }
 
@@ -631,11 +757,46 @@ bool aligned(const Q8Mat &m) {
 
 }  // namespace
 
+// Microseconds of a product by tiles of one size with its sum in `split` stretches, as
+// measured on MI355X: a step takes a block at least `alone`, and the blocks of a CU
+// together `each` a block; a launch 3 (with its first loads and its results); joined
+// stretches a second launch, and their fp32 sums written and read at 4 TB/s.
+struct TileCost {
+    int side, per_cu;
+    double alone, each;
+};
+constexpr TileCost kTiles[3] = {{256, 1, 1.25, 1.50}, {128, 2, 0.60, 0.52}, {64, 4, 0.38, 0.21}};
+
+static double cost(const TileCost &t, int64_t M, int64_t N, int steps, int split) {
+    const int64_t items = ((M + t.side - 1) / t.side) * ((N + t.side - 1) / t.side) * split;
+    const int64_t full = items / (256 * t.per_cu), rest = items - full * 256 * t.per_cu;
+    auto step = [&](int64_t blocks) {
+        const double together = t.each * static_cast<double>((blocks + 255) / 256);
+        return blocks == 0 ? 0.0 : together > t.alone ? together : t.alone;
+    };
+    const double each = (steps + split - 1) / split;
+    double us = 3.0 + each * (static_cast<double>(full) * step(256 * t.per_cu) + step(rest));
+    if (split > 1) us += 3.0 + 8e-6 * static_cast<double>(M) * static_cast<double>(N) * split / 4.0;
+    return us;
+}
+
 Q8Cut q8_cut(const Q8Mat &a, bool ta, const Q8Mat &b, bool tb) {
-    const int M = ta ? a.cols : a.rows, N = tb ? b.rows : b.cols;
+    const int64_t M = ta ? a.cols : a.rows, N = tb ? b.rows : b.cols, K = ta ? a.rows : a.cols;
+    const int steps = static_cast<int>((K + kBK - 1) / kBK);
     Q8Cut c{};
-    c.tile = M <= 64 || N <= 64 ? 2 : M <= 128 || N <= 128 ? 1 : 0;
     c.split = 1;
+    // (one row by 14336 x 4096: 15.2 us by tiles of 64; 32 rows 15.8)
+    if (!ta && tb && M <= 32) {
+        c.tile = 3;
+    } else {
+        double best = 0.0;
+        for (int t = 0; t < 3; ++t)
+            // stretches of two steps and more
+            for (int split = 1; split == 1 || (split <= 16 && split * 2 <= steps); split *= 2) {
+                const double us = cost(kTiles[t], M, N, steps, split);
+                if ((t == 0 && split == 1) || us < best) best = us, c.tile = t, c.split = split;
+            }
+    }
     // rows along the sum that end inside 16 bytes are copied too, with zeros after them
     c.bytes_a = aligned(a) && (ta || (a.cols & 15) == 0) ? 0 : round256(round16(a.cols) * a.rows);
     c.bytes_b = aligned(b) && (!tb || (b.cols & 15) == 0) ? 0 : round256(round16(b.cols) * b.rows);
@@ -667,11 +828,25 @@ hipError_t launch_q8_product(const Q8Mat &a, bool ta, const Q8Mat &b, bool tb, u
     const Operand A = operand(a, cut.bytes_a, M), B = operand(b, cut.bytes_b, N);
     Out out{p, cut.split > 1 ? reinterpret_cast<float *>(at) : nullptr, a.divisor, b.divisor, ldo,
             cut.split};
-    if (cut.tile == 0) launch<256, 256, 2, 4>(A, ta, B, tb, a.format, out, K, st);
-    else if (cut.tile == 1) launch<128, 128, 2, 2>(A, ta, B, tb, a.format, out, K, st);
-    else launch<64, 64, 2, 1>(A, ta, B, tb, a.format, out, K, st);
-    if (cut.split > 1)
-        q8_join_kernel<<<blocks_for(static_cast<int64_t>(M) * N), kBlock, 0, st>>>(out, M, N);
+    if (cut.tile == 0) {
+        launch<256, 256, 2, 4>(A, ta, B, tb, a.format, out, K, st);
+    } else if (cut.tile == 1) {
+        launch<128, 128, 2, 2>(A, ta, B, tb, a.format, out, K, st);
+    } else if (cut.tile == 2) {
+        launch<64, 64, 2, 1>(A, ta, B, tb, a.format, out, K, st);
+    } else {
+        // columns a block: enough blocks for every CU, or loads enough for one
+        const bool wide = N >= 32 * 256;
+        if (M <= 16) wide ? launch_few<1, 2>(A, B, a.format, out, K, st)
+                          : launch_few<1, 1>(A, B, a.format, out, K, st);
+        else wide ? launch_few<2, 2>(A, B, a.format, out, K, st)
+                  : launch_few<2, 1>(A, B, a.format, out, K, st);
+    }
+    if (cut.split > 1) {
+        const int64_t n = static_cast<int64_t>(M) * N;
+        if (N % 4 == 0) q8_join_kernel<4><<<blocks_for(n / 4), kBlock, 0, st>>>(out, M, N);
+        else q8_join_kernel<1><<<blocks_for(n), kBlock, 0, st>>>(out, M, N);
+    }
     return hipGetLastError();
 }
 
