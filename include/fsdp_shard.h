@@ -16,7 +16,8 @@
  *             fsdp_pack_allgather_fp8_groups, fsdp_step_group_set
  *             AdamW, amax and copy-ins of many groups, one launch each
  *   8 bits    fsdp_block_scales_shard, fsdp_pack_allgather_fp8_blocks,
- *             fsdp_q8_quantize, fsdp_q8_dequantize, fsdp_q8_product
+ *             fsdp_q8_quantize, fsdp_q8_dequantize, fsdp_q8_product,
+ *             fsdp_q8_linear_forward, fsdp_q8_linear_backward
  *             copy-in, activation checkpoints and products in 8-bit floating
  *             point with a scale for each block of 128
  *   Muon      fsdp_muon_momentum, fsdp_muon_reduce_momentum,
@@ -631,6 +632,29 @@ fsdp_status fsdp_q8_product_workspace(const fsdp_q8_t *a, int32_t trans_a, const
 fsdp_status fsdp_q8_product(const fsdp_q8_t *a, int32_t trans_a, const fsdp_q8_t *b,
                             int32_t trans_b, uint16_t *out, int64_t ldo, void *workspace,
                             int64_t workspace_bytes, void *stream);
+
+/* A linear layer's steps from native code, one call each: the products above with
+ * the quantising of their operands.  W is [out, in] in 8 bits (E4M3, in TILES or
+ * TENSOR), x and dy are bf16 or fp32, y, dx and dW bf16.
+ *   forward   y [tokens, out] = x W^T, x [tokens, in] quantised along rows; and
+ *             x along columns into `saved` (E4M3, COLS, [tokens, in]), the
+ *             checkpoint for the backward pass, unless it is NULL
+ *   backward  from dy [tokens, out] in `format`: dx [tokens, in] = dy W unless dx is
+ *             NULL, dy quantised along rows; dW [out, in] = dy^T x unless dW is
+ *             NULL, x from `saved` and dy quantised along columns
+ * Bit for bit fsdp_q8_quantize and fsdp_q8_product, one after the other.
+ *   workspace  as for fsdp_q8_product, fsdp_q8_linear_workspace's bytes (the larger
+ *              of the two steps')
+ * Outputs share memory with nothing else of the call.  Every argument is checked
+ * before anything is launched.  Errors: as the calls they make. */
+fsdp_status fsdp_q8_linear_workspace(const fsdp_q8_t *w, int64_t tokens, int64_t *bytes);
+fsdp_status fsdp_q8_linear_forward(const fsdp_q8_t *w, const void *x, int32_t dtype, int64_t ldx,
+                                   int64_t tokens, const fsdp_q8_t *saved, uint16_t *y, int64_t ldy,
+                                   void *workspace, int64_t workspace_bytes, void *stream);
+fsdp_status fsdp_q8_linear_backward(const fsdp_q8_t *w, const fsdp_q8_t *saved, const void *dy,
+                                    int32_t dtype, int64_t lddy, int32_t format, uint16_t *dx,
+                                    int64_t lddx, uint16_t *dw, int64_t lddw, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
 
 /* Where parameter i's scales lie in a plan's: `offset` bytes from the start,
  * line after line of its 128 x 128 blocks (pitch = ceil(cols / 128)); total:

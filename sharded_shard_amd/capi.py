@@ -181,6 +181,10 @@ _SIGS = {
     "fsdp_q8_dequantize": (_i32, [_Q8, _P, _i32, _i64, _P]),
     "fsdp_q8_product_workspace": (_i32, [_Q8, _i32, _Q8, _i32, ctypes.POINTER(_i64)]),
     "fsdp_q8_product": (_i32, [_Q8, _i32, _Q8, _i32, _P, _i64, _P, _i64, _P]),
+    "fsdp_q8_linear_workspace": (_i32, [_Q8, _i64, ctypes.POINTER(_i64)]),
+    "fsdp_q8_linear_forward": (_i32, [_Q8, _P, _i32, _i64, _i64, _Q8, _P, _i64, _P, _i64, _P]),
+    "fsdp_q8_linear_backward": (_i32, [_Q8, _Q8, _P, _i32, _i64, _i32, _P, _i64, _P, _i64, _P,
+                                       _i64, _P]),
     "fsdp_plan_block_scales": (_i32, [_P, _i32, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
     "fsdp_block_scales_shard": (_i32, [_P, _P, _P]),
     "fsdp_pack_allgather_fp8_blocks": (_i32, [_P, _P, _P, _P]),
@@ -787,6 +791,32 @@ def fsdp_q8_product(a: Q8Struct, trans_a: int, b: Q8Struct, trans_b: int, out, l
            "fsdp_q8_product")
 
 
+def fsdp_q8_linear_workspace(w: Q8Struct, tokens: int) -> int:
+    n = _i64()
+    _check(lib.fsdp_q8_linear_workspace(ctypes.byref(w), tokens, ctypes.byref(n)),
+           "fsdp_q8_linear_workspace")
+    return n.value
+
+
+def fsdp_q8_linear_forward(w: Q8Struct, x, dtype: int, ldx: int, tokens: int, saved, y, ldy: int,
+                           workspace, workspace_bytes: int, stream=None) -> None:
+    """saved: the checkpoint's Q8Struct, or None."""
+    _check(lib.fsdp_q8_linear_forward(ctypes.byref(w), addr(x), dtype, ldx, tokens,
+                                      ctypes.byref(saved) if saved is not None else None, addr(y),
+                                      ldy, addr(workspace), workspace_bytes, stream_handle(stream)),
+           "fsdp_q8_linear_forward")
+
+
+def fsdp_q8_linear_backward(w: Q8Struct, saved: Q8Struct, dy, dtype: int, lddy: int, format: int,
+                            dx, lddx: int, dw, lddw: int, workspace, workspace_bytes: int,
+                            stream=None) -> None:
+    """dx, dw: None for none."""
+    _check(lib.fsdp_q8_linear_backward(ctypes.byref(w), ctypes.byref(saved), addr(dy), dtype, lddy,
+                                       format, addr(dx), lddx, addr(dw), lddw, addr(workspace),
+                                       workspace_bytes, stream_handle(stream)),
+           "fsdp_q8_linear_backward")
+
+
 def fsdp_plan_block_scales(plan, i: int):
     """(offset, total): where parameter i's block scales start, and the bytes of all."""
     o, t = _i64(), _i64()
@@ -796,6 +826,8 @@ def fsdp_plan_block_scales(plan, i: int):
 
 
 def _scales_dev(plan, scales) -> int:
+    if isinstance(scales, int):
+        return scales
     ok = _dims(plan) is not None
     return _dev(scales, fsdp_plan_block_scales(plan, 0)[1], "scales") if ok else addr(scales)
 
@@ -806,7 +838,7 @@ def fsdp_block_scales_shard(plan, scales, stream=None) -> None:
 
 
 def fsdp_pack_allgather_fp8_blocks(plan, ag_in, scales, stream=None) -> None:
-    d = _dims(plan)
+    d = None if isinstance(ag_in, int) else _dims(plan)
     a = _dev(ag_in, d[1], "ag_in") if d else addr(ag_in)
     _check(lib.fsdp_pack_allgather_fp8_blocks(plan, a, _scales_dev(plan, scales),
                                               stream_handle(stream)),

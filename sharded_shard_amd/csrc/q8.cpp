@@ -160,6 +160,103 @@ fsdp_status check_product(const fsdp_q8_t *a, int32_t ta, const fsdp_q8_t *b, in
 
 int64_t bytes_of(const fsdp::Q8Cut &c) { return c.bytes_a + c.bytes_b + c.bytes_sums; }
 
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// The workspace of a linear layer's two steps: x, or dy both ways round, in 8 bits,
+// then what the products need.
+struct Linear {
+    Q8Mat w{}, x{}, dy{}, dyt{};
+    fsdp::Q8Cut forward{}, input{};
+    int64_t held = 0, sums = 0;
+    char *base = nullptr;
+    void *products = nullptr;
+
+    // A quantised [rows, cols] at `at`, which it moves on.
+    static Q8Mat matrix(char *&at, int64_t rows, int64_t cols, int32_t format, int32_t blocks) {
+        fsdp_q8_t q{};
+        q.rows = rows, q.cols = cols, q.ld = up(cols, 16), q.blocks = blocks;
+        const Lines l = scale_lines(q);
+        Q8Mat m{};
+        m.rows = static_cast<int32_t>(rows), m.cols = static_cast<int32_t>(cols);
+        m.format = format, m.blocks = blocks;
+        m.ld = q.ld, m.pitch = up(l.length, 16);
+        m.codes = reinterpret_cast<uint8_t *>(at);
+        at += up(rows * m.ld, 256);
+        m.scales = reinterpret_cast<uint8_t *>(at);
+        at += up(l.n * m.pitch, 256);
+        return m;
+    }
+
+    // Where everything lies from `from`; the products' memory is the largest that one of
+    // the three needs, whatever the alignment of what they are given.
+    void lay(char *from, int32_t format) {
+        char *at = from;
+        x = matrix(at, x.rows, w.cols, FSDP_Q8_E4M3, FSDP_Q8_ROWS);
+        const int64_t one = at - from;
+        at = from;
+        dy = matrix(at, x.rows, w.rows, format, FSDP_Q8_ROWS);
+        dyt = matrix(at, x.rows, w.rows, format, FSDP_Q8_COLS);
+        held = at - from > one ? at - from : one;
+        base = from;
+        products = from + held;
+    }
+
+    fsdp_status plan(const fsdp_q8_t *W, int64_t tokens, int32_t format, const char *call) {
+        fsdp_status s = check(W, call, "w", &w);
+        if (s != FSDP_OK) return s;
+        if (W->format != FSDP_Q8_E4M3 ||
+            (W->blocks != FSDP_Q8_TILES && W->blocks != FSDP_Q8_TENSOR))
+            return bad(FSDP_E_UNSUPPORTED, call, "w", "must be E4M3, in TILES or TENSOR");
+        if (format != FSDP_Q8_E4M3 && format != FSDP_Q8_E5M2)
+            return bad(FSDP_E_UNSUPPORTED, call, "format", "must be FSDP_Q8_E4M3 or FSDP_Q8_E5M2");
+        if (tokens < 0) return bad(FSDP_E_INVAL, call, "tokens", "negative");
+        if (tokens > kQ8MaxSide || up(w.rows, 16) > kQ8MaxSide || up(w.cols, 16) > kQ8MaxSide)
+            return bad(FSDP_E_UNSUPPORTED, call, "tokens", "above 2^22");
+        x.rows = static_cast<int32_t>(tokens);
+        lay(nullptr, format);
+        forward = fsdp::q8_cut(x, false, w, true);
+        input = fsdp::q8_cut(dy, false, w, false);
+        // a checkpoint at the worst alignment
+        Q8Mat odd = x;
+        odd.codes = reinterpret_cast<uint8_t *>(uintptr_t{1});
+        const int64_t a = bytes_of(forward), b = bytes_of(input),
+                      c = bytes_of(fsdp::q8_cut(dyt, true, odd, false));
+        sums = a > b ? a : b;
+        sums = sums > c ? sums : c;
+        fmt = format;
+        return FSDP_OK;
+    }
+    int32_t fmt = 0;
+
+    int64_t bytes() const { return held + sums; }
+    Span span() const { return {base, bytes(), "workspace"}; }
+
+    fsdp_status place(void *workspace, int64_t have, const char *call) {
+        if (bytes() > 0) {
+            if (workspace == nullptr || have < bytes())
+                return set_error(FSDP_E_INVAL, std::string(call) + ": the workspace needs " +
+                                                   std::to_string(bytes()) + " bytes");
+            if (misaligned(workspace, 256))
+                return set_error(FSDP_E_ALIGN,
+                                 std::string(call) + ": workspace not 256-byte aligned");
+        }
+        lay(static_cast<char *>(workspace), fmt);
+        return FSDP_OK;
+    }
+
+    fsdp_status check_saved(const fsdp_q8_t *saved, const char *call, Q8Mat *S) const {
+        const fsdp_status s = check(saved, call, "saved", S);
+        if (s != FSDP_OK) return s;
+        if (saved->format != FSDP_Q8_E4M3 || saved->blocks != FSDP_Q8_COLS)
+            return bad(FSDP_E_UNSUPPORTED, call, "saved", "must be E4M3, in COLS");
+        if (saved->rows != x.rows || saved->cols != w.cols)
+            return bad(FSDP_E_INVAL, call, "saved", "must be [tokens, in]");
+        if (saved->divisor != nullptr)
+            return bad(FSDP_E_INVAL, call, "saved", "a divisor is for reading only");
+        return FSDP_OK;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -268,6 +365,97 @@ fsdp_status fsdp_q8_product(const fsdp_q8_t *a, int32_t trans_a, const fsdp_q8_t
     if (e == hipSuccess)
         e = fsdp::launch_q8_product(A, trans_a != 0, B, trans_b != 0, out, ldo, cut, workspace,
                                     static_cast<hipStream_t>(stream));
+    return launched(e, call);
+} catch (...) {
+    return FSDP_E_NOMEM;
+}
+
+fsdp_status fsdp_q8_linear_workspace(const fsdp_q8_t *w, int64_t tokens, int64_t *bytes) try {
+    const char *call = "fsdp_q8_linear_workspace";
+    if (bytes == nullptr) return set_error(FSDP_E_INVAL, std::string(call) + ": null bytes");
+    Linear l;
+    const fsdp_status s = l.plan(w, tokens, FSDP_Q8_E4M3, call);
+    if (s == FSDP_OK) *bytes = l.bytes();
+    return s;
+} catch (...) {
+    return FSDP_E_NOMEM;
+}
+
+fsdp_status fsdp_q8_linear_forward(const fsdp_q8_t *w, const void *x, int32_t dtype, int64_t ldx,
+                                   int64_t tokens, const fsdp_q8_t *saved, uint16_t *y, int64_t ldy,
+                                   void *workspace, int64_t workspace_bytes, void *stream) try {
+    const char *call = "fsdp_q8_linear_forward";
+    Linear l;
+    Q8Mat S{};
+    Span X, Y;
+    fsdp_status s = l.plan(w, tokens, FSDP_Q8_E4M3, call);
+    if (s != FSDP_OK || (saved != nullptr && (s = l.check_saved(saved, call, &S)) != FSDP_OK) ||
+        (s = check_wide(x, dtype, tokens, w->cols, ldx, call, "x", &X)) != FSDP_OK ||
+        (s = check_wide(y, FSDP_DTYPE_BF16, tokens, w->rows, ldy, call, "y", &Y)) != FSDP_OK ||
+        (s = l.place(workspace, workspace_bytes, call)) != FSDP_OK)
+        return s;
+    const Span outs[4] = {Y, l.span(), saved ? codes_of(*saved, "saved's codes") : Span{},
+                          saved ? scales_of(*saved, "saved's scales") : Span{}};
+    const Span ins[4] = {X, codes_of(*w, "w's codes"), scales_of(*w, "w's scales"),
+                         {w->divisor, w->divisor ? 4 : 0, "w's divisor"}};
+    if ((s = check_apart(outs, ins, call)) != FSDP_OK) return s;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = fsdp::injected_fault();
+    if (e == hipSuccess)
+        e = fsdp::launch_q8_quantize(x, dtype == FSDP_DTYPE_F32, ldx, l.x, saved ? &S : nullptr, st);
+    if (e == hipSuccess) e = fsdp::injected_fault();
+    if (e == hipSuccess)
+        e = fsdp::launch_q8_product(l.x, false, l.w, true, y, ldy, l.forward, l.products, st);
+    return launched(e, call);
+} catch (...) {
+    return FSDP_E_NOMEM;
+}
+
+fsdp_status fsdp_q8_linear_backward(const fsdp_q8_t *w, const fsdp_q8_t *saved, const void *dy,
+                                    int32_t dtype, int64_t lddy, int32_t format, uint16_t *dx,
+                                    int64_t lddx, uint16_t *dw, int64_t lddw, void *workspace,
+                                    int64_t workspace_bytes, void *stream) try {
+    const char *call = "fsdp_q8_linear_backward";
+    if (saved == nullptr) return bad(FSDP_E_INVAL, call, "saved", "null");
+    Linear l;
+    Q8Mat S{};
+    Span DY, DX{}, DW{};
+    const int64_t tokens = saved->rows;
+    fsdp_status s = l.plan(w, tokens, format, call);
+    if (s != FSDP_OK || (s = l.check_saved(saved, call, &S)) != FSDP_OK ||
+        (s = check_wide(dy, dtype, tokens, w->rows, lddy, call, "dy", &DY)) != FSDP_OK ||
+        (dx != nullptr && (s = check_wide(dx, FSDP_DTYPE_BF16, tokens, w->cols, lddx, call, "dx",
+                                          &DX)) != FSDP_OK) ||
+        (dw != nullptr && (s = check_wide(dw, FSDP_DTYPE_BF16, w->rows, w->cols, lddw, call, "dW",
+                                          &DW)) != FSDP_OK) ||
+        (s = l.place(workspace, workspace_bytes, call)) != FSDP_OK)
+        return s;
+    const Span outs[3] = {DX, DW, l.span()};
+    const Span ins[6] = {DY,
+                         codes_of(*w, "w's codes"),
+                         scales_of(*w, "w's scales"),
+                         {w->divisor, w->divisor ? 4 : 0, "w's divisor"},
+                         codes_of(*saved, "saved's codes"),
+                         scales_of(*saved, "saved's scales")};
+    if ((s = check_apart(outs, ins, call)) != FSDP_OK) return s;
+    if (dx == nullptr && dw == nullptr) return FSDP_OK;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const Q8Mat &first = dx ? l.dy : l.dyt;
+    hipError_t e = fsdp::injected_fault();
+    if (e == hipSuccess)
+        e = fsdp::launch_q8_quantize(dy, dtype == FSDP_DTYPE_F32, lddy, first,
+                                     dx && dw ? &l.dyt : nullptr, st);
+    if (e == hipSuccess && dx != nullptr) {
+        e = fsdp::injected_fault();
+        if (e == hipSuccess)
+            e = fsdp::launch_q8_product(l.dy, false, l.w, false, dx, lddx, l.input, l.products, st);
+    }
+    if (e == hipSuccess && dw != nullptr) {
+        e = fsdp::injected_fault();
+        if (e == hipSuccess)
+            e = fsdp::launch_q8_product(l.dyt, true, S, false, dw, lddw,
+                                        fsdp::q8_cut(l.dyt, true, S, false), l.products, st);
+    }
     return launched(e, call);
 } catch (...) {
     return FSDP_E_NOMEM;

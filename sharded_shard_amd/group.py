@@ -279,10 +279,12 @@ class ShardedGroup:
     def block_scales(self, out, stream=None) -> None:
         """This rank's scale byte of every 128 x 128 block into ``out`` [n_block_scales]
         (uint8); the maximum over ranks is what ``pack_fp8_blocks`` takes."""
-        capi.fsdp_block_scales_shard(self.plan, out, stream)
+        capi.fsdp_block_scales_shard(self.plan, capi._dev(out, self.n_block_scales, "out"), stream)
 
     def pack_fp8_blocks(self, ag_in, scales, stream=None) -> None:
-        capi.fsdp_pack_allgather_fp8_blocks(self.plan, ag_in, scales, stream)
+        """FP8 copy-in into ``ag_in`` [S] bytes with a scale for each block."""
+        capi.fsdp_pack_allgather_fp8_blocks(self.plan, capi._dev(ag_in, self.S, "ag_in"),
+                                            capi._dev(scales, self.n_block_scales, "scales"), stream)
 
     def full_q8(self, i: int, scales):
         """Parameter i's gathered FP8 matrix with its blocks' ``scales`` [n_block_scales],

@@ -64,12 +64,15 @@ class Q8:
     the GPU by which values are divided (the FP8 copy-in's per-parameter scale).
     It is a view: it keeps the tensors, and reads them when it is used."""
 
+    __slots__ = ("rows", "cols", "blocks", "format", "divisor", "device", "c", "aligned", "_codes",
+                 "_scales", "_both", "_stream")
+
     def __init__(self, codes: torch.Tensor, scales: Optional[torch.Tensor], blocks: str,
                  format: str = "e4m3", divisor: Optional[torch.Tensor] = None):
         kind, fmt = _known(BLOCKS, blocks, "blocks"), _known(FORMATS, format, "format")
         ld = _rows_of(codes, "codes", _BYTES)
-        self.rows, self.cols = codes.shape
-        lines, length = scale_lines(self.rows, self.cols, blocks)
+        rows, cols = codes.shape
+        lines, length = scale_lines(rows, cols, blocks)
         pitch = 0
         if lines:
             if scales is None:
@@ -78,37 +81,63 @@ class Q8:
             if scales.shape[0] < lines or scales.shape[1] < length:
                 raise ValueError(f"scales must hold {lines} lines of {length} bytes, "
                                  f"not {tuple(scales.shape)}")
+            if blocks != "tiles" and pitch % 4:
+                if lines > 1:
+                    raise ValueError("lines of scales must lie a multiple of 4 bytes apart")
+                pitch = _up(pitch, 4)
         if divisor is not None:
             if divisor.dtype != torch.float32 or divisor.numel() != 1:
                 raise ValueError("divisor: one fp32 is needed")
             capi._dev(divisor, 4, "divisor")
-        self.codes, self.scales, self.divisor = codes, scales, divisor
-        self.blocks, self.format = blocks, format
-        self.device = codes.device
-        self.c = capi.Q8Struct(codes.data_ptr(), scales.data_ptr() if lines else 0,
-                               divisor.data_ptr() if divisor is not None else 0,
-                               self.rows, self.cols, ld, pitch, fmt, kind)
+        self._codes, self._scales, self._both = codes, scales, None
+        self._set(rows, cols, blocks, format, codes.device, codes.data_ptr(),
+                  scales.data_ptr() if lines else 0, divisor, ld, pitch, fmt, kind)
+
+    def _set(self, rows, cols, blocks, format, device, codes, scales, divisor, ld, pitch, fmt, kind):
+        self.rows, self.cols, self.blocks, self.format = rows, cols, blocks, format
+        self.divisor, self.device = divisor, device
+        self.aligned = (codes | ld) & 15 == 0
+        self._stream = None
+        self.c = capi.Q8Struct(codes, scales, divisor.data_ptr() if divisor is not None else 0, rows,
+                               cols, ld, pitch, fmt, kind)
 
     @classmethod
     def empty(cls, shape, blocks: str, format: str = "e4m3", device="cuda") -> "Q8":
         """Memory for a matrix of this shape, laid out so that products read it in
         place."""
         rows, cols = shape
-        _known(BLOCKS, blocks, "blocks")
-        if blocks == "tensor":
+        kind, fmt = _known(BLOCKS, blocks, "blocks"), _known(FORMATS, format, "format")
+        if kind == capi.FSDP_Q8_TENSOR:
             raise ValueError("blocks must have scales")
-        ld = _up(cols, 16)
+        ld = (cols + 15) & ~15
         lines, length = scale_lines(rows, cols, blocks)
-        pitch = _up(length, 16)
+        pitch = (length + 15) & ~15
+        q = cls.__new__(cls)
         # one piece of memory: the codes, then the scales
-        both = torch.empty(rows * ld + lines * pitch, dtype=torch.uint8, device=device)
-        codes = both[:rows * ld].view(rows, ld)[:, :cols]
-        return cls(codes, both[rows * ld:].view(lines, pitch)[:, :length] if lines else both[:0].view(0, 0),
-                   blocks, format)
+        q._both = torch.empty(rows * ld + lines * pitch, dtype=torch.uint8, device=device)
+        q._codes = q._scales = None
+        at = q._both.data_ptr()
+        q._set(rows, cols, blocks, format, q._both.device, at, at + rows * ld, None, ld, pitch, fmt,
+               kind)
+        return q
 
     @property
     def shape(self):
         return self.rows, self.cols
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = self._both.as_strided((self.rows, self.cols), (self.c.ld, 1))
+        return self._codes
+
+    @property
+    def scales(self) -> Optional[torch.Tensor]:
+        if self._scales is None and self._both is not None:
+            lines, length = scale_lines(self.rows, self.cols, self.blocks)
+            self._scales = self._both.as_strided((lines, length), (self.c.pitch, 1),
+                                                 self.rows * self.c.ld)
+        return self._scales
 
     def codes_view(self) -> torch.Tensor:
         """The codes, uint8 [rows, cols]."""
@@ -117,6 +146,8 @@ class Q8:
     def scales_view(self) -> torch.Tensor:
         """The scales' bytes: [columns / 128, rows], [rows / 128, columns] or, of
         tiles, [rows / 128, columns / 128], rounded up."""
+        if self._both is not None:
+            return self.scales
         lines, length = scale_lines(self.rows, self.cols, self.blocks)
         return self.scales[:lines, :length]
 
@@ -132,12 +163,19 @@ def _here(*qs: Q8) -> None:
                              f"cuda:{torch.cuda.current_device()}")
 
 
-def _on(stream):
-    """The context in which memory is taken for work on `stream`: torch hands it out
-    again in the order of the stream that it was taken on."""
+def _handle(stream) -> int:
+    return stream if isinstance(stream, int) else capi.stream_handle(stream)
+
+
+def _take(make, stream):
+    """make() where its memory is for work on `stream`: torch hands memory out again in
+    the order of the stream that it was taken on."""
+    if stream is None:
+        return make()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return make()
 
 
 def quantize(x: torch.Tensor, blocks: str = "rows", format: str = "e4m3", out=None, stream=None):
@@ -150,12 +188,9 @@ def quantize(x: torch.Tensor, blocks: str = "rows", format: str = "e4m3", out=No
     _known(FORMATS, format, "format")
     ldx = _rows_of(x, "x", _DTYPES)
     if out is None:
+        shape, dev = x.shape, x.device
         kinds = ("rows", "cols") if pair else (blocks,)
-        if stream is None:
-            out = [Q8.empty(x.shape, k, format, x.device) for k in kinds]
-        else:
-            with _on(stream):
-                out = [Q8.empty(x.shape, k, format, x.device) for k in kinds]
+        out = _take(lambda: [Q8.empty(shape, k, format, dev) for k in kinds], stream)
     else:
         out = list(out) if pair else [out]
         _here(*out)
@@ -169,11 +204,8 @@ def quantize(x: torch.Tensor, blocks: str = "rows", format: str = "e4m3", out=No
 
 def _result(shape, dtype, device, out, stream, dtypes):
     if out is None:
-        if stream is None:
-            out = torch.empty(shape, dtype=dtype, device=device)
-        else:
-            with _on(stream):
-                out = torch.empty(shape, dtype=dtype, device=device)
+        out = _take(lambda: torch.empty(shape, dtype=dtype, device=device), stream)
+        return out, shape[1]
     elif tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must be {tuple(shape)}, not {tuple(out.shape)}")
     return out, _rows_of(out, "out", dtypes)
@@ -196,17 +228,22 @@ def product(a: Q8, b: Q8, trans_a: bool = False, trans_b: bool = False, out=None
     that share one must follow each other."""
     _here(a, b)
     ta, tb = int(trans_a), int(trans_b)
-    need = capi.fsdp_q8_product_workspace(a.c, ta, b.c, tb)
+    # what the bytes of workspace follow from
+    key = (ta, tb, a.rows, a.cols, a.aligned, a.blocks, b.rows, b.cols, b.aligned, b.blocks, b.format)
+    need = _needs.get(key)
+    if need is None:
+        if len(_needs) >= 4096:
+            _needs.clear()
+        need = _needs[key] = capi.fsdp_q8_product_workspace(a.c, ta, b.c, tb)
     shape = a.cols if trans_a else a.rows, b.rows if trans_b else b.cols
     out, ldo = _result(shape, torch.bfloat16, a.device, out, stream, _HALF)
     if need and workspace is None:
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
-        else:
-            with _on(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+        workspace = _take(lambda: torch.empty(need, dtype=torch.uint8, device=a.device), stream)
     capi.fsdp_q8_product(a.c, ta, b.c, tb, out.data_ptr(), ldo, workspace, 0, stream)
     return out
+
+
+_needs: dict = {}
 
 
 class Linear8:
@@ -226,32 +263,60 @@ class Linear8:
         _known(FORMATS, grad_format, "grad_format")
         self.weight, self.grad_format = weight, grad_format
         self.saved = []
+        self._bytes = {}
+
+    def _workspace(self, tokens: int, stream):
+        n = self._bytes.get(tokens)
+        if n is None:
+            n = self._bytes[tokens] = capi.fsdp_q8_linear_workspace(self.weight.c, tokens)
+        dev = self.weight.device
+        return _take(lambda: torch.empty(n, dtype=torch.uint8, device=dev), stream), n
 
     def forward(self, x: torch.Tensor, out=None, save: bool = True, stream=None) -> torch.Tensor:
         """``x`` [tokens, in] bf16 or fp32 -> [tokens, out] bf16.  save: keep the 8-bit
         checkpoint (not for evaluation)."""
-        if x.dim() != 2 or x.shape[1] != self.weight.cols:
-            raise ValueError(f"x must be [tokens, {self.weight.cols}], not {tuple(x.shape)}")
+        w = self.weight
+        _here(w)
+        ldx = _rows_of(x, "x", _DTYPES)
+        tokens, cols = x.shape
+        if cols != w.cols:
+            raise ValueError(f"x must be [tokens, {w.cols}], not {tuple(x.shape)}")
+        y, ldy = _result((tokens, w.rows), torch.bfloat16, w.device, out, stream, _HALF)
+        q = _take(lambda: Q8.empty((tokens, cols), "cols", "e4m3", w.device), stream) if save else None
+        ws, n = self._workspace(tokens, stream)
+        capi.fsdp_q8_linear_forward(w.c, x.data_ptr(), _DTYPES[x.dtype], ldx, tokens,
+                                    q.c if save else None, y.data_ptr(), ldy, ws.data_ptr(), n, stream)
         if save:
-            rows, cols = quantize(x, "both", stream=stream)
-        else:
-            rows, cols = quantize(x, "rows", stream=stream), None
-        y = product(rows, self.weight, trans_b=True, out=out, stream=stream)
-        if save:
-            self.saved.append(cols)
+            q._stream = _handle(stream)
+            self.saved.append(q)
         return y
 
-    def backward(self, dy: torch.Tensor, dweight: torch.Tensor, out=None,
-                 stream=None) -> torch.Tensor:
-        """``dy`` [tokens, out] -> dx [tokens, in] bf16; ``dweight`` [out, in] bf16 (the
-        group's full gradient) is written."""
+    def backward(self, dy: torch.Tensor, dweight: Optional[torch.Tensor], out=None,
+                 need_input: bool = True, stream=None) -> Optional[torch.Tensor]:
+        """``dy`` [tokens, out] bf16 or fp32 -> dx [tokens, in] bf16 (None without
+        need_input); ``dweight`` [out, in] bf16 (the group's full gradient) is written
+        (None: a frozen weight)."""
         if not self.saved:
             raise RuntimeError("backward without a saved forward")
-        x = self.saved[0]
-        if tuple(dy.shape) != (x.rows, self.weight.rows):
-            raise ValueError(f"dy must be {(x.rows, self.weight.rows)}, not {tuple(dy.shape)}")
-        rows, cols = quantize(dy, "both", self.grad_format, stream=stream)
-        dx = product(rows, self.weight, out=out, stream=stream)
-        product(cols, x, trans_a=True, out=dweight, stream=stream)
+        w, x = self.weight, self.saved[0]
+        _here(w)
+        lddy = _rows_of(dy, "dy", _DTYPES)
+        if tuple(dy.shape) != (x.rows, w.rows):
+            raise ValueError(f"dy must be {(x.rows, w.rows)}, not {tuple(dy.shape)}")
+        dx, lddx = None, 0
+        if need_input:
+            dx, lddx = _result(x.shape, torch.bfloat16, w.device, out, stream, _HALF)
+        lddw = 0
+        if dweight is not None:
+            dweight, lddw = _result(w.shape, torch.bfloat16, w.device, dweight, stream, _HALF)
+        ws, n = self._workspace(x.rows, stream)
+        capi.fsdp_q8_linear_backward(w.c, x.c, dy.data_ptr(), _DTYPES[dy.dtype], lddy,
+                                     FORMATS[self.grad_format], dx.data_ptr() if need_input else 0,
+                                     lddx, dweight.data_ptr() if dweight is not None else 0, lddw,
+                                     ws.data_ptr(), n, stream)
+        if _handle(stream) != x._stream:
+            # its memory is another stream's: not to be handed out before this one is done
+            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            x._both.record_stream(torch.cuda.current_stream() if s is None else s)
         self.saved.pop(0)
         return dx
