@@ -50,29 +50,58 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
     return __uint_as_float(byte == 255u ? 0x7FC00000u : byte == 0u ? 0x400000u : byte << 23);
 }
 
-// Four codes, by the converter (to nearest even).  Finite values that would
-// round past fmax, which only a caller's scales can leave, are clamped to it;
-// the comparisons keep NaN.
-template <int FMT>
-__device__ __forceinline__ float clamped(float x) {
-    constexpr float kMax = FMT == FSDP_Q8_E4M3 ? 448.0f : 57344.0f;
-    // an infinity is no value that a code could stand in for: NaN for E4M3
-    if constexpr (FMT == FSDP_Q8_E4M3) x = fabsf(x) == __builtin_inff() ? __builtin_nanf("") : x;
-    else if (fabsf(x) == __builtin_inff()) return x;
-    return x > kMax ? kMax : (x < -kMax ? -kMax : x);
+// Four codes, by the converter (to nearest even), of values that a caller's scales may
+// leave past fmax: clamped to it; the comparisons keep NaN.  An infinity is no value
+// that a code could stand in for: the converter makes it NaN.
+__device__ __forceinline__ float clamp448(float x) {
+    if (fabsf(x) == __builtin_inff()) return x;
+    return x > 448.0f ? 448.0f : (x < -448.0f ? -448.0f : x);
 }
 
+__device__ __forceinline__ uint32_t four_clamped(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(a), clamp448(b), 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(c), clamp448(d), w, true);
+    return static_cast<uint32_t>(w);
+}
+
+// Four codes of values that fit.
 template <int FMT>
 __device__ __forceinline__ uint32_t four_codes(float a, float b, float c, float d) {
     int w;
     if constexpr (FMT == FSDP_Q8_E4M3) {
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(clamped<FMT>(a), clamped<FMT>(b), 0, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(clamped<FMT>(c), clamped<FMT>(d), w, true);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
     } else {
-        w = __builtin_amdgcn_cvt_pk_bf8_f32(clamped<FMT>(a), clamped<FMT>(b), 0, false);
-        w = __builtin_amdgcn_cvt_pk_bf8_f32(clamped<FMT>(c), clamped<FMT>(d), w, true);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
     }
     return static_cast<uint32_t>(w);
+}
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Four codes of four bf16 over a power of two, one instruction for two (equal to the
+// converter of fp32 on the quotient for every bf16 that fits and every scale).
+template <int FMT>
+__device__ __forceinline__ uint32_t four_scaled(uint32_t lo, uint32_t hi, float s) {
+    s16x2 w{0, 0};
+    const bf16x2 a = __builtin_bit_cast(bf16x2, lo), b = __builtin_bit_cast(bf16x2, hi);
+    if constexpr (FMT == FSDP_Q8_E4M3) {
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, a, s, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, b, s, true);
+    } else {
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(w, a, s, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(w, b, s, true);
+    }
+    return __builtin_bit_cast(uint32_t, w);
+}
+
+// Both halves' maxima.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
 }
 
 // ---------------------------------------------------------------------------
@@ -125,6 +154,26 @@ __device__ __forceinline__ uint32_t lane_max(uint32_t v, int from, int to) {
     return v;
 }
 
+// The maximum over 16 neighbouring lanes, in each of them, by rotating them.
+template <bool kHalves>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+    auto step = [&](uint32_t o) { v = kHalves ? max2(v, o) : umax(v, o); };
+    step(__builtin_amdgcn_update_dpp(0u, v, 0x128, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0u, v, 0x124, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0u, v, 0x122, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0u, v, 0x121, 0xF, 0xF, false));
+    return v;
+}
+
+// The maximum over the wave's four lanes 16 apart, in each of them.
+template <bool kHalves>
+__device__ __forceinline__ uint32_t column_max(uint32_t v) {
+    auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = kHalves ? max2(a[0], a[1]) : umax(a[0], a[1]);
+    a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return kHalves ? max2(a[0], a[1]) : umax(a[0], a[1]);
+}
+
 // n of eight codes at p; vec: one store of all eight
 __device__ __forceinline__ void store_eight(uint8_t *p, uint32_t lo, uint32_t hi, int n, bool vec) {
     if (vec && n == 8) {
@@ -138,94 +187,203 @@ __device__ __forceinline__ void store_eight(uint8_t *p, uint32_t lo, uint32_t hi
 
 enum { kWriteRows = 1, kWriteCols = 2, kWriteTiles = 4 };
 
-// One 128 x 128 block a workgroup, held in registers from the loads to the
-// stores: thread (r, c) of 16 x 16 has the eight columns from 8 c of the rows r,
-// r + 16, ...  A row's maximum is taken over its 16 neighbouring lanes, a
-// column's over the wave's four rows and, through LDS, over the waves.
-template <int FMT, bool kF32, int WHAT>
-__global__ __launch_bounds__(kBlock) void q8_quantize_kernel(const void *__restrict__ x,
-                                                             int64_t ldx, Q8Mat A, Q8Mat B) {
-    __shared__ uint32_t part[4][128];
+// One 128 x 128 block a workgroup, held in registers from the loads to the stores:
+// thread (r, c) of 128 / P x 16 has the eight columns from 8 c of P rows.  A row's
+// maximum is taken over its 16 neighbouring lanes, a column's over the wave's four
+// rows and, through LDS, over the waves.
+//
+// Of bf16 the magnitudes are compared two at a time as 16-bit numbers, and one
+// instruction divides two by their scale and rounds them.  The scales of two
+// neighbouring columns differ, but are powers of two: their exponents, less that of a
+// common scale 2^(kLow - 127), are taken from the values', two at a time, and what
+// is left is over the common one.  A value that this leaves under 2^-126 is under
+// 2^-22 of its scale, no code's worth, and may come out as anything as small.
+// (8192 x 4096 both ways: 39 us with a product and a conversion from fp32 for each
+// value.)
+constexpr uint32_t kLow = 24;
+
+template <int FMT, bool kF32, int WHAT, int P>
+__global__ __launch_bounds__(2048 / P) void q8_quantize_kernel(const void *__restrict__ x,
+                                                               int64_t ldx, Q8Mat A, Q8Mat B) {
+    constexpr int kWaves = 32 / P, kRows = 128 / P, kWords = kF32 ? 8 : 4;
+    __shared__ __attribute__((aligned(16))) uint32_t part[kWaves][16][kWords];
     __shared__ __attribute__((aligned(16))) uint8_t bytes[2][128];
-    const int tid = threadIdx.x, r = tid >> 4, c = (tid & 15) * 8, wave = tid >> 6;
+    const int tid = threadIdx.x, r = tid >> 4, t16 = tid & 15, c = t16 * 8, wave = tid >> 6;
     const int row0 = blockIdx.y * 128, col0 = blockIdx.x * 128;
     const int rows = A.rows - row0 < 128 ? A.rows - row0 : 128;
     const int cols = A.cols - col0 < 128 ? A.cols - col0 : 128;
     const int n = cols - c < 0 ? 0 : (cols - c < 8 ? cols - c : 8);
     const bool vec = (lo32(x) & 15u) == 0 && (ldx & (kF32 ? 3 : 7)) == 0;
     const Q8Mat &rm = A, &cm = (WHAT & kWriteRows) && (WHAT & kWriteCols) ? B : A;
-    Eight<kF32> v[8];
+    Eight<kF32> v[P];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const int row = r + 16 * p;
+    for (int p = 0; p < P; ++p) {
+        const int row = r + kRows * p;
         const int64_t o = static_cast<int64_t>(row0 + row) * ldx + col0 + c;
         v[p] = load_eight<kF32>(x, o, row < rows ? n : 0, vec);
     }
+    // magnitudes, two in a word of bf16; what is not finite has none
+    uint32_t mag[P][kWords];
+    bool odd = false;
+    if constexpr (kF32) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mag[p][e] = finite_mag(v[p].get(e));
+    } else {
+        uint32_t most = 0;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mag[p][e] = v[p].w[0][e] & 0x7FFF7FFFu;
+                most = max2(most, mag[p][e]);
+            }
+        odd = __any((most & 0xFFFFu) >= 0x7F80u || (most >> 16) >= 0x7F80u);
+        if (odd) {
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t m = mag[p][e];
+                    mag[p][e] = ((m & 0xFFFFu) < 0x7F80u ? m & 0xFFFFu : 0u) |
+                                (m < 0x7F800000u ? m & 0xFFFF0000u : 0u);
+                }
+        }
+    }
+    auto codes_at = [&](const Q8Mat &m, int row) {
+        return m.codes + static_cast<int64_t>(row0 + row) * m.ld + col0 + c;
+    };
+    // row p over one scale for all its values
+    auto put_row = [&](const Q8Mat &m, bool wide, int p, uint32_t byte) {
+        const int row = r + kRows * p;
+        uint32_t lo, hi;
+        if constexpr (kF32) {
+            const float s = inverse_scale(byte);
+            lo = four_codes<FMT>(v[p].get(0) * s, v[p].get(1) * s, v[p].get(2) * s, v[p].get(3) * s);
+            hi = four_codes<FMT>(v[p].get(4) * s, v[p].get(5) * s, v[p].get(6) * s, v[p].get(7) * s);
+        } else {
+            const float s = scale_of(byte);
+            lo = four_scaled<FMT>(v[p].w[0].x, v[p].w[0].y, s);
+            hi = four_scaled<FMT>(v[p].w[0].z, v[p].w[0].w, s);
+        }
+        if (row < rows) store_eight(codes_at(m, row), lo, hi, n, wide);
+    };
     if constexpr (WHAT & kWriteRows) {
         const bool wide = (lo32(rm.codes) & 7u) == 0 && (rm.ld & 7) == 0;
+        auto put = [&](int p, uint32_t m) {
+            const uint32_t b = scale_byte<FMT>(m);
+            if (t16 == 0) bytes[0][r + kRows * p] = static_cast<uint8_t>(b);
+            put_row(rm, wide, p, b);
+        };
+        if constexpr (kF32) {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            uint32_t m = 0;
+            for (int p = 0; p < P; ++p) {
+                uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = umax(m, finite_mag(v[p].get(e)));
-            const uint32_t b = scale_byte<FMT>(lane_max(m, 1, 16));
-            const float s = inverse_scale(b);
-            const int row = r + 16 * p;
-            if ((tid & 15) == 0) bytes[0][row] = static_cast<uint8_t>(b);
-            if (row < rows)
-                store_eight(rm.codes + static_cast<int64_t>(row0 + row) * rm.ld + col0 + c,
-                            four_codes<FMT>(v[p].get(0) * s, v[p].get(1) * s, v[p].get(2) * s,
-                                            v[p].get(3) * s),
-                            four_codes<FMT>(v[p].get(4) * s, v[p].get(5) * s, v[p].get(6) * s,
-                                            v[p].get(7) * s),
-                            n, wide);
+                for (int e = 0; e < 8; ++e) m = umax(m, mag[p][e]);
+                put(p, row_max<false>(m));
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < P; p += 2) {
+                auto four = [&](int k) {
+                    return max2(max2(mag[k][0], mag[k][1]), max2(mag[k][2], mag[k][3]));
+                };
+                // two rows' maxima in the halves of a word
+                const uint32_t a = four(p), b = four(p + 1);
+                const uint32_t m = row_max<true>(max2(__builtin_amdgcn_perm(b, a, 0x05040100u),
+                                                      __builtin_amdgcn_perm(b, a, 0x07060302u)));
+                put(p, m << 16);
+                put(p + 1, m & 0xFFFF0000u);
+            }
         }
     }
     if constexpr (WHAT & (kWriteCols | kWriteTiles)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kWords; ++e) {
             uint32_t m = 0;
 #pragma unroll
-            for (int p = 0; p < 8; ++p) m = umax(m, finite_mag(v[p].get(e)));
-            m = lane_max(m, 16, 64);
-            if ((tid & 48) == 0) part[wave][c + e] = m;
+            for (int p = 0; p < P; ++p) m = kF32 ? umax(m, mag[p][e]) : max2(m, mag[p][e]);
+            m = column_max<!kF32>(m);
+            if ((tid & 48) == 0) part[wave][t16][e] = m;
         }
     }
     __syncthreads();
     if constexpr (WHAT & (kWriteCols | kWriteTiles)) {
         const bool wide = (lo32(cm.codes) & 7u) == 0 && (cm.ld & 7) == 0;
-        float s[8];
-        uint32_t all = 0;
+        uint32_t m[kWords];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t m = umax(umax(part[0][c + e], part[1][c + e]),
-                                    umax(part[2][c + e], part[3][c + e]));
-            const uint32_t b = scale_byte<FMT>(m);
-            all = umax(all, m);
-            s[e] = inverse_scale(b);
-            if constexpr (WHAT & kWriteCols)
-                if (r == 0) bytes[1][c + e] = static_cast<uint8_t>(b);
-        }
+        for (int e = 0; e < kWords; ++e) m[e] = part[0][t16][e];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+            for (int e = 0; e < kWords; ++e)
+                m[e] = kF32 ? umax(m[e], part[w][t16][e]) : max2(m[e], part[w][t16][e]);
         if constexpr (WHAT & kWriteTiles) {
-            const uint32_t b = scale_byte<FMT>(lane_max(all, 1, 16));
+            uint32_t all = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = inverse_scale(b);
+            for (int e = 0; e < kWords; ++e) all = kF32 ? umax(all, m[e]) : max2(all, m[e]);
+            all = row_max<!kF32>(all);
+            if constexpr (!kF32) all = umax(all << 16, all & 0xFFFF0000u);
+            const uint32_t b = scale_byte<FMT>(all);
             if (tid == 0)
                 cm.scales[static_cast<int64_t>(blockIdx.y) * cm.pitch + blockIdx.x] =
                     static_cast<uint8_t>(b);
-        }
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const int row = r + 16 * p;
-            if (row < rows)
-                store_eight(cm.codes + static_cast<int64_t>(row0 + row) * cm.ld + col0 + c,
-                            four_codes<FMT>(v[p].get(0) * s[0], v[p].get(1) * s[1],
-                                            v[p].get(2) * s[2], v[p].get(3) * s[3]),
-                            four_codes<FMT>(v[p].get(4) * s[4], v[p].get(5) * s[5],
-                                            v[p].get(6) * s[6], v[p].get(7) * s[7]),
-                            n, wide);
+            for (int p = 0; p < P; ++p) put_row(cm, wide, p, b);
+        } else {
+            uint32_t b[8];
+            bool low = odd;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t k = kF32 ? m[e] : e & 1 ? m[e >> 1] & 0xFFFF0000u : m[e >> 1] << 16;
+                b[e] = scale_byte<FMT>(k);
+                low |= k != 0 && b[e] < kLow;
+                if (r == 0) bytes[1][c + e] = static_cast<uint8_t>(b[e]);
+            }
+            if (kF32 || __any(low)) {
+                float s[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = inverse_scale(b[e]);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int row = r + kRows * p;
+                    if (row < rows)
+                        store_eight(codes_at(cm, row),
+                                    four_codes<FMT>(v[p].get(0) * s[0], v[p].get(1) * s[1],
+                                                    v[p].get(2) * s[2], v[p].get(3) * s[3]),
+                                    four_codes<FMT>(v[p].get(4) * s[4], v[p].get(5) * s[5],
+                                                    v[p].get(6) * s[6], v[p].get(7) * s[7]),
+                                    n, wide);
+                }
+            } else {
+                // an empty column's zeros stay zeros
+                uint32_t less[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = b[2 * e] < kLow ? 0u : b[2 * e] - kLow;
+                    const uint32_t hi = b[2 * e + 1] < kLow ? 0u : b[2 * e + 1] - kLow;
+                    less[e] = lo << 7 | hi << 23;
+                }
+                const float s = scale_of(kLow);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int row = r + kRows * p;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const u16x2 d = __builtin_elementwise_sub_sat(
+                            __builtin_bit_cast(u16x2, mag[p][e]), __builtin_bit_cast(u16x2, less[e]));
+                        w[e] = (v[p].w[0][e] & 0x80008000u) | __builtin_bit_cast(uint32_t, d);
+                    }
+                    if (row < rows)
+                        store_eight(codes_at(cm, row), four_scaled<FMT>(w[0], w[1], s),
+                                    four_scaled<FMT>(w[2], w[3], s), n, wide);
+                }
+            }
+            __syncthreads();
         }
-        if constexpr (WHAT & kWriteCols) __syncthreads();
     }
     // The blocks' scales: neighbouring rows, or columns, are neighbouring bytes.
     if constexpr (WHAT & kWriteRows) {
@@ -270,11 +428,18 @@ __device__ __forceinline__ void code_values(uint32_t lo, uint32_t hi, float (&x)
     }
 }
 
+// Two as bf16, to nearest even, by the instruction.
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // The same blocks and threads.  A code times its power of two is exact in
 // fp32; a divisor, where there is one, rounds once more.
-template <int FMT, bool kF32>
-__global__ __launch_bounds__(kBlock) void q8_dequantize_kernel(Q8Mat Q, void *__restrict__ out,
-                                                               int64_t ldo) {
+template <int FMT, bool kF32, int P>
+__global__ __launch_bounds__(2048 / P) void q8_dequantize_kernel(Q8Mat Q, void *__restrict__ out,
+                                                                 int64_t ldo) {
+    constexpr int kRows = 128 / P;
     const int tid = threadIdx.x, r = tid >> 4, c = (tid & 15) * 8;
     const int row0 = blockIdx.y * 128, col0 = blockIdx.x * 128;
     const int rows = Q.rows - row0 < 128 ? Q.rows - row0 : 128;
@@ -284,36 +449,65 @@ __global__ __launch_bounds__(kBlock) void q8_dequantize_kernel(Q8Mat Q, void *__
     const bool vec = n == 8 && (lo32(Q.codes) & 7u) == 0 && (Q.ld & 7) == 0;
     const bool wide = n == 8 && (lo32(out) & 15u) == 0 && (ldo & (kF32 ? 3 : 7)) == 0;
     const float div = Q.divisor ? *Q.divisor : 1.0f;
-    float s[8];
-    const uint8_t *sb = Q.scales + (Q.blocks == FSDP_Q8_ROWS
-                                        ? static_cast<int64_t>(blockIdx.x) * Q.pitch
-                                        : static_cast<int64_t>(blockIdx.y) * Q.pitch);
+    // All loads leave before the first is waited for: rows past the matrix read its first
+    // again.
+    uint32_t w[P][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        s[e] = Q.blocks == FSDP_Q8_COLS    ? scale_of(sb[col0 + c + (e < n ? e : 0)])
-               : Q.blocks == FSDP_Q8_TILES ? scale_of(sb[blockIdx.x])
-                                           : 1.0f;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const int row = r + 16 * p;
-        if (row >= rows) continue;
+    for (int p = 0; p < P; ++p) {
+        const int row = r + kRows * p < rows ? r + kRows * p : 0;
         const uint8_t *from = Q.codes + static_cast<int64_t>(row0 + row) * Q.ld + col0 + c;
-        uint32_t w[2] = {0u, 0u};
         if (vec) {
             const u32x2 t = *reinterpret_cast<const u32x2 *>(from);
-            w[0] = t.x;
-            w[1] = t.y;
+            w[p][0] = t.x;
+            w[p][1] = t.y;
         } else {
+            w[p][0] = w[p][1] = 0u;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (e < n) w[e >> 2] |= static_cast<uint32_t>(from[e]) << (8 * (e & 3));
+                if (e < n) w[p][e >> 2] |= static_cast<uint32_t>(from[e]) << (8 * (e & 3));
         }
-        const float sr = Q.blocks == FSDP_Q8_ROWS ? scale_of(sb[row0 + row]) : 1.0f;
+    }
+    uint32_t by_row[P], by_col[8];
+    const uint8_t *sb = Q.scales + static_cast<int64_t>(Q.blocks == FSDP_Q8_ROWS ? blockIdx.x
+                                                                                : blockIdx.y) *
+                                       Q.pitch;
+#pragma unroll
+    for (int p = 0; p < P; ++p) by_row[p] = 127u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) by_col[e] = 127u;
+    if (Q.blocks == FSDP_Q8_ROWS) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) by_row[p] = sb[row0 + (r + kRows * p < rows ? r + kRows * p : 0)];
+    } else if (Q.blocks == FSDP_Q8_COLS) {
+        if (n == 8) {
+            // a line starts at a multiple of four bytes
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(sb + col0 + c);
+            const uint32_t lo = q[0], hi = q[1];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) by_col[e] = (e < 4 ? lo : hi) >> (8 * (e & 3)) & 255u;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) by_col[e] = sb[col0 + c + (e < n ? e : 0)];
+        }
+    } else if (Q.blocks == FSDP_Q8_TILES) {
+        const uint32_t b = sb[blockIdx.x];
+#pragma unroll
+        for (int p = 0; p < P; ++p) by_row[p] = b;
+    }
+    float s[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = scale_of(by_col[e]);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int row = r + kRows * p;
+        if (row >= rows) continue;
+        const float sr = scale_of(by_row[p]);
         float y[8];
-        code_values<FMT>(w[0], w[1], y);
+        code_values<FMT>(w[p][0], w[p][1], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            y[e] *= Q.blocks == FSDP_Q8_ROWS ? sr : s[e];
+            // one of the two is 1
+            y[e] *= Q.blocks == FSDP_Q8_COLS ? s[e] : sr;
             if (Q.divisor) y[e] /= div;
         }
         const int64_t o = static_cast<int64_t>(row0 + row) * ldo + col0 + c;
@@ -329,7 +523,9 @@ __global__ __launch_bounds__(kBlock) void q8_dequantize_kernel(Q8Mat Q, void *__
             }
         } else {
             uint16_t *to = static_cast<uint16_t *>(out) + o;
-            const u32x4 h = pack8(y);
+            u32x4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = two_bf16(y[2 * e], y[2 * e + 1]);
             if (wide) {
                 *reinterpret_cast<u32x4 *>(to) = h;
             } else {
@@ -431,7 +627,7 @@ __global__ __launch_bounds__(kBlock) void pack_fp8_blocks_kernel(
         const int groups = (valid - head) >> 4, done = head + groups * 16;
         auto one = [&](int i) {
             const float v = src[i] * scale_at(place_after(row0, col0, i, be.cols));
-            dst[i] = static_cast<uint8_t>(four_codes<FSDP_Q8_E4M3>(v, v, v, v));
+            dst[i] = static_cast<uint8_t>(four_clamped(v, v, v, v));
         };
         const int tid = threadIdx.x;
         if (tid < head) one(tid);
@@ -453,7 +649,7 @@ __global__ __launch_bounds__(kBlock) void pack_fp8_blocks_kernel(
                 const float s = scale_at(at);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    w[k] = four_codes<FSDP_Q8_E4M3>(v[k].x * s, v[k].y * s, v[k].z * s, v[k].w * s);
+                    w[k] = four_clamped(v[k].x * s, v[k].y * s, v[k].z * s, v[k].w * s);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -463,7 +659,7 @@ __global__ __launch_bounds__(kBlock) void pack_fp8_blocks_kernel(
                         y[e] = v[k][e] * scale_at(at);
                         if (++at.col == be.cols) at = {at.row + 1, 0};
                     }
-                    w[k] = four_codes<FSDP_Q8_E4M3>(y[0], y[1], y[2], y[3]);
+                    w[k] = four_clamped(y[0], y[1], y[2], y[3]);
                 }
             }
             *reinterpret_cast<u32x4 *>(dst + o) = w;
@@ -472,23 +668,41 @@ __global__ __launch_bounds__(kBlock) void pack_fp8_blocks_kernel(
     }
 }
 
-template <int FMT, bool kF32>
+dim3 blocks_of(const Q8Mat &m) { return dim3((m.cols + 127) / 128, (m.rows + 127) / 128); }
+
+// Rows a thread: two, 16 waves a block, where the blocks are few and a thread's own time
+// counts; eight where there are enough to fill the CUs.
+bool few(const dim3 &grid) { return grid.x * grid.y < 1024u; }
+
+template <int FMT, bool kF32, int P>
 void quantize(const void *x, int64_t ldx, const Q8Mat &a, const Q8Mat *b, dim3 grid,
               hipStream_t st) {
     const Q8Mat none{};
-    const Q8Mat &second = b ? *b : none;
+    constexpr int kThreads = 2048 / P;
     if (b != nullptr)
-        q8_quantize_kernel<FMT, kF32, kWriteRows | kWriteCols>
-            <<<grid, kBlock, 0, st>>>(x, ldx, a, second);
+        q8_quantize_kernel<FMT, kF32, kWriteRows | kWriteCols, P>
+            <<<grid, kThreads, 0, st>>>(x, ldx, a, *b);
     else if (a.blocks == FSDP_Q8_ROWS)
-        q8_quantize_kernel<FMT, kF32, kWriteRows><<<grid, kBlock, 0, st>>>(x, ldx, a, second);
+        q8_quantize_kernel<FMT, kF32, kWriteRows, P><<<grid, kThreads, 0, st>>>(x, ldx, a, none);
     else if (a.blocks == FSDP_Q8_COLS)
-        q8_quantize_kernel<FMT, kF32, kWriteCols><<<grid, kBlock, 0, st>>>(x, ldx, a, second);
+        q8_quantize_kernel<FMT, kF32, kWriteCols, P><<<grid, kThreads, 0, st>>>(x, ldx, a, none);
     else
-        q8_quantize_kernel<FMT, kF32, kWriteTiles><<<grid, kBlock, 0, st>>>(x, ldx, a, second);
+        q8_quantize_kernel<FMT, kF32, kWriteTiles, P><<<grid, kThreads, 0, st>>>(x, ldx, a, none);
 }
 
-dim3 blocks_of(const Q8Mat &m) { return dim3((m.cols + 127) / 128, (m.rows + 127) / 128); }
+template <int FMT, bool kF32>
+void quantize(const void *x, int64_t ldx, const Q8Mat &a, const Q8Mat *b, hipStream_t st) {
+    const dim3 grid = blocks_of(a);
+    if (few(grid)) quantize<FMT, kF32, 2>(x, ldx, a, b, grid, st);
+    else quantize<FMT, kF32, 8>(x, ldx, a, b, grid, st);
+}
+
+template <int FMT, bool kF32>
+void dequantize(const Q8Mat &q, void *out, int64_t ldo, hipStream_t st) {
+    const dim3 grid = blocks_of(q);
+    if (few(grid)) q8_dequantize_kernel<FMT, kF32, 2><<<grid, 1024, 0, st>>>(q, out, ldo);
+    else q8_dequantize_kernel<FMT, kF32, 8><<<grid, 256, 0, st>>>(q, out, ldo);
+}
 
 }  // namespace
 
@@ -497,25 +711,23 @@ hipError_t launch_q8_quantize(const void *x, bool f32, int64_t ldx, const Q8Mat 
     if (a.rows == 0 || a.cols == 0) return hipSuccess;
     const Q8Mat &rows = b && a.blocks == FSDP_Q8_COLS ? *b : a;
     const Q8Mat *cols = b && a.blocks == FSDP_Q8_COLS ? &a : b;
-    const dim3 grid = blocks_of(a);
     if (a.format == FSDP_Q8_E4M3)
-        f32 ? quantize<FSDP_Q8_E4M3, true>(x, ldx, rows, cols, grid, st)
-            : quantize<FSDP_Q8_E4M3, false>(x, ldx, rows, cols, grid, st);
+        f32 ? quantize<FSDP_Q8_E4M3, true>(x, ldx, rows, cols, st)
+            : quantize<FSDP_Q8_E4M3, false>(x, ldx, rows, cols, st);
     else
-        f32 ? quantize<FSDP_Q8_E5M2, true>(x, ldx, rows, cols, grid, st)
-            : quantize<FSDP_Q8_E5M2, false>(x, ldx, rows, cols, grid, st);
+        f32 ? quantize<FSDP_Q8_E5M2, true>(x, ldx, rows, cols, st)
+            : quantize<FSDP_Q8_E5M2, false>(x, ldx, rows, cols, st);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_dequantize(const Q8Mat &q, void *out, bool f32, int64_t ldo, hipStream_t st) {
     if (q.rows == 0 || q.cols == 0) return hipSuccess;
-    const dim3 grid = blocks_of(q);
     if (q.format == FSDP_Q8_E4M3)
-        f32 ? q8_dequantize_kernel<FSDP_Q8_E4M3, true><<<grid, kBlock, 0, st>>>(q, out, ldo)
-            : q8_dequantize_kernel<FSDP_Q8_E4M3, false><<<grid, kBlock, 0, st>>>(q, out, ldo);
+        f32 ? dequantize<FSDP_Q8_E4M3, true>(q, out, ldo, st)
+            : dequantize<FSDP_Q8_E4M3, false>(q, out, ldo, st);
     else
-        f32 ? q8_dequantize_kernel<FSDP_Q8_E5M2, true><<<grid, kBlock, 0, st>>>(q, out, ldo)
-            : q8_dequantize_kernel<FSDP_Q8_E5M2, false><<<grid, kBlock, 0, st>>>(q, out, ldo);
+        f32 ? dequantize<FSDP_Q8_E5M2, true>(q, out, ldo, st)
+            : dequantize<FSDP_Q8_E5M2, false>(q, out, ldo, st);
     return hipGetLastError();
 }
 
