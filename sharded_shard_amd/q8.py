@@ -48,13 +48,17 @@ def _rows_of(t: torch.Tensor, what: str, dtypes) -> int:
     if t.dim() != 2 or t.dtype not in dtypes:
         raise ValueError(f"{what}: a matrix of {' or '.join(str(d) for d in dtypes)} is needed, "
                          f"not {tuple(t.shape)} of {t.dtype}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{what} is on {t.device}, not on the current GPU")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    down, across = t.stride()
+    if across != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must follow each other")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{what}: rows overlap")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if down < cols:
+        if rows > 1:
+            raise ValueError(f"{what}: rows overlap")
+        return cols
+    return down
 
 
 class Q8:
@@ -64,7 +68,7 @@ class Q8:
     the GPU by which values are divided (the FP8 copy-in's per-parameter scale).
     It is a view: it keeps the tensors, and reads them when it is used."""
 
-    __slots__ = ("rows", "cols", "blocks", "format", "divisor", "device", "c", "aligned", "_codes",
+    __slots__ = ("rows", "cols", "blocks", "format", "divisor", "device", "index", "c", "aligned", "_codes",
                  "_scales", "_both", "_stream")
 
     def __init__(self, codes: torch.Tensor, scales: Optional[torch.Tensor], blocks: str,
@@ -96,7 +100,7 @@ class Q8:
     def _set(self, rows, cols, blocks, format, device, codes, scales, divisor, ld, pitch, fmt, kind):
         self.rows, self.cols, self.blocks, self.format = rows, cols, blocks, format
         self.divisor, self.device = divisor, device
-        self.aligned = (codes | ld) & 15 == 0
+        self.aligned, self.index = (codes | ld) & 15 == 0, device.index
         self._stream = None
         self.c = capi.Q8Struct(codes, scales, divisor.data_ptr() if divisor is not None else 0, rows,
                                cols, ld, pitch, fmt, kind)
@@ -157,10 +161,10 @@ class Q8:
 
 
 def _here(*qs: Q8) -> None:
+    now = torch.cuda.current_device()
     for q in qs:
-        if q.device.index != torch.cuda.current_device():
-            raise ValueError(f"the 8-bit matrix is on {q.device}, not on the current device "
-                             f"cuda:{torch.cuda.current_device()}")
+        if q.index != now:
+            raise ValueError(f"the 8-bit matrix is on {q.device}, not on the current device cuda:{now}")
 
 
 def _handle(stream) -> int:
