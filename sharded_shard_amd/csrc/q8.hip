@@ -50,18 +50,12 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
     return __uint_as_float(byte == 255u ? 0x7FC00000u : byte == 0u ? 0x400000u : byte << 23);
 }
 
-// Four codes, by the converter (to nearest even), of values that a caller's scales may
-// leave past fmax: clamped to it; the comparisons keep NaN.  An infinity is no value
-// that a code could stand in for: the converter makes it NaN.
-__device__ __forceinline__ float clamp448(float x) {
-    if (fabsf(x) == __builtin_inff()) return x;
-    return x > 448.0f ? 448.0f : (x < -448.0f ? -448.0f : x);
-}
-
-__device__ __forceinline__ uint32_t four_clamped(float a, float b, float c, float d) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(a), clamp448(b), 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(c), clamp448(d), w, true);
-    return static_cast<uint32_t>(w);
+// x over a caller's scale, which may leave it past fmax, or past fp32: clamped there;
+// the comparisons keep NaN.  x - x is 0, or NaN where x is not finite: an infinity is
+// no value that a code could stand in for.
+__device__ __forceinline__ float clamped(float x, float inverse) {
+    const float y = x * inverse;
+    return (y > 448.0f ? 448.0f : (y < -448.0f ? -448.0f : y)) + (x - x);
 }
 
 // Four codes of values that fit.
@@ -627,8 +621,8 @@ __global__ __launch_bounds__(kBlock) void pack_fp8_blocks_kernel(
         head = head < valid ? head : valid;
         const int groups = (valid - head) >> 4, done = head + groups * 16;
         auto one = [&](int i) {
-            const float v = src[i] * scale_at(place_after(row0, col0, i, be.cols));
-            dst[i] = static_cast<uint8_t>(four_clamped(v, v, v, v));
+            const float v = clamped(src[i], scale_at(place_after(row0, col0, i, be.cols)));
+            dst[i] = static_cast<uint8_t>(four_codes<FSDP_Q8_E4M3>(v, v, v, v));
         };
         const int tid = threadIdx.x;
         if (tid < head) one(tid);
@@ -650,17 +644,18 @@ __global__ __launch_bounds__(kBlock) void pack_fp8_blocks_kernel(
                 const float s = scale_at(at);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    w[k] = four_clamped(v[k].x * s, v[k].y * s, v[k].z * s, v[k].w * s);
+                    w[k] = four_codes<FSDP_Q8_E4M3>(clamped(v[k].x, s), clamped(v[k].y, s),
+                                                    clamped(v[k].z, s), clamped(v[k].w, s));
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float y[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        y[e] = v[k][e] * scale_at(at);
+                        y[e] = clamped(v[k][e], scale_at(at));
                         if (++at.col == be.cols) at = {at.row + 1, 0};
                     }
-                    w[k] = four_clamped(y[0], y[1], y[2], y[3]);
+                    w[k] = four_codes<FSDP_Q8_E4M3>(y[0], y[1], y[2], y[3]);
                 }
             }
             *reinterpret_cast<u32x4 *>(dst + o) = w;

@@ -51,6 +51,8 @@ def _rows_of(t: torch.Tensor, what: str, dtypes) -> int:
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{what} is on {t.device}, not on the current GPU")
     rows, cols = t.shape
+    if rows == 0 or cols == 0:
+        return cols
     down, across = t.stride()
     if across != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must follow each other")
