@@ -8,10 +8,10 @@
 // has neighbouring j of one i.
 //
 // Inside the instruction eight neighbouring products at a time are aligned to
-// the largest of them and what lies 2^-14 below its power of two is dropped
-// (measured); the eights and the accumulator add in fp32.  A sum is so within
-// 7 2^-13 of its largest products, 1.5e-5 of the result for normal data and
-// below the 2^-9 of the rounding to bf16 that follows.
+// the largest of them and keep their bits down to 2^-13 of its power of two
+// (measured); the eights and the accumulator add in fp32.  An eight is so within
+// 7 2^-13 of its largest product, a sum within 1.5e-5 of its size for normal data,
+// far below the 2^-9 of the rounding to bf16 that follows.
 #include "q8.hpp"
 
 #include "device.hpp"
@@ -407,10 +407,7 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
     };
     // scales and all parts of a step: the loads younger than what a border waits for
     constexpr int kYoung = 1 + 2 * kLP + kLQ;
-    // Stores of a tile's results, at least: those that follow what the first border
-    // after them waits for.
-    constexpr int kStores = 2 * HM * 2;
-    static_assert(kYoung + kStores < 64, "the counter's range");
+    static_assert(kYoung < 64, "the counter's range");
     i32x2 sa, sa2;
     int sb, sb2;
     auto mma = [&](auto hc, auto xc, auto yc) {
@@ -419,9 +416,8 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
             q[y], p[h][x], acc[h * HM + x][y], 0, FMTA, y, sb, x, h ? sa.y : sa.x);
     };
     // Step v.  Step s of the item that is aimed at starts on its way into the images.
-    // kPast: stores between the loads that the borders wait for and those.
-    auto step = [&](int v, int s, auto past) {
-        constexpr int N = HM * FN, kPast = decltype(past)::value;
+    auto step = [&](int v, int s) {
+        constexpr int N = HM * FN;
         int l = anew();
         load_scales(s);
         // columns outermost: the first products need the first columns alone
@@ -437,7 +433,7 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
             });
             __builtin_amdgcn_sched_barrier(0);
         });
-        border<kYoung + kPast>();
+        border<kYoung>();
         l = anew();
         sa2 = read_sa(v + 1);
         sb2 = read_sb(v + 1);
@@ -451,7 +447,7 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
             if constexpr (n == N - 1) put_scales(v + 2);
             __builtin_amdgcn_sched_barrier(0);
         });
-        border<kYoung + kPast>();
+        border<kYoung>();
         sa = sa2;
         sb = sb2;
     };
@@ -479,8 +475,8 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
     auto results = [&](const Item &o) {
         const int i0 = o.ti * BM, j0 = o.tj * BN, l = anew(), g = l >> 4;
         if (vec) {
-            // rows past the matrix lie past the range; stores there and of columns past
-            // it are dropped, but counted
+            // rows past the matrix lie past the range, where stores are dropped, and columns
+            // past it are sent there
             const int rows = A.n - i0 < BM ? A.n - i0 : BM, cols = B.n - j0 < BN ? B.n - j0 : BN;
             const uint32_t ld = static_cast<uint32_t>(out.ld) * 2u;
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
@@ -519,8 +515,6 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
                 });
             }
         });
-        // fewer stores than kStores perhaps
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     };
 
     // Loads for steps that no item has read nothing, and are counted.
@@ -542,12 +536,12 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
     int v = 0;
     for (int b = blockIdx.x;;) {
         int s = now.from;
-        for (; s + 2 < now.to; ++s, ++v) step(v, s + 2, Int<0>{});
+        for (; s + 2 < now.to; ++s, ++v) step(v, s + 2);
         b += gridDim.x;
         if (b < items) ahead = item_of(b, tiles_m, tiles_n, out.split, all);
         else ahead.from = all;
         aim();
-        for (int i = 0; s < now.to; ++s, ++v, ++i) step(v, ahead.from + i, Int<0>{});
+        for (int i = 0; s < now.to; ++s, ++v, ++i) step(v, ahead.from + i);
         results(now);
         if (b >= items) break;
         clear();
