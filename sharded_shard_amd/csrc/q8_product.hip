@@ -300,9 +300,15 @@ __device__ __forceinline__ void border() {
 // is read, and its Q as the last products of the present columns are made, and P1
 // of the step after next starts.  At the border after a turn every wave has the
 // operands of the next turn in registers and the parts that are read in it have
-// landed, two to three turns after their loads left.  (One border a step, with all
-// loads in the second turn: 531 us instead of 430 for 8192 x 14336 x 4096, b as it
-// is; 424 and 418 with b transposed.)
+// landed, two to three turns after their loads left.  (Tried before the rest stood:
+// one border a step, with all loads in the second turn, took 531 us for 430 of 8192 x
+// 14336 x 4096, b as it is, and 424 for 418 with b transposed.  Four waves of 128 x
+// 128 in place of eight of 128 x 64 read a third less from LDS, but nothing runs
+// while one of them makes addresses or waits: 465 for 400.)
+//
+// Eight waves keep the matrix cores busy 62% of the time, and on normal data the clock
+// falls to 1.9 GHz for the card's power: 395 us, 2.4 PFLOP/s, where zeros take 315.
+// Loads that all hit the caches would give 388.
 //
 // A block goes from tile to tile without a pause: the last two steps of one load
 // the first two of the next, and its results are stored, without a wait, before
@@ -418,12 +424,18 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
     // Step v.  Step s of the item that is aimed at starts on its way into the images.
     auto step = [&](int v, int s) {
         constexpr int N = HM * FN;
-        int l = anew();
-        load_scales(s);
-        // columns outermost: the first products need the first columns alone
+        int l = 0;
+        // Columns outermost: the first products need the first columns alone.  Behind each
+        // product what else is due, so that addresses are made while it runs (the reads'
+        // ahead of a turn's first product: 411 us for 403 of 8192 x 14336 x 4096).
         for_each<N>([&](auto nc) {
             constexpr int n = decltype(nc)::value, y = n / HM, x = n % HM;
             mma(Int<0>{}, Int<x>{}, Int<y>{});
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (n == 0) {
+                l = anew();
+                load_scales(s);
+            }
             if constexpr (n < HM) read_p(v, 1, n, l);
             constexpr int lo = n * (kLP + kLQ) / N, hi = (n + 1) * (kLP + kLQ) / N;
             for_each<hi - lo>([&](auto tc) {
@@ -431,21 +443,22 @@ __global__ __launch_bounds__(64 * WM *WN, 2) void q8_product_kernel(Operand A, O
                 if constexpr (t < kLP) load_p(v + 2, s, 0, t);
                 else load_q(v + 2, s, t - kLP);
             });
-            __builtin_amdgcn_sched_barrier(0);
         });
         border<kYoung>();
-        l = anew();
-        sa2 = read_sa(v + 1);
-        sb2 = read_sb(v + 1);
         for_each<N>([&](auto nc) {
             constexpr int n = decltype(nc)::value, y = n / HM, x = n % HM;
             mma(Int<1>{}, Int<x>{}, Int<y>{});
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (n == 0) l = anew();
             if constexpr (n < HM) read_p(v + 1, 0, n, l);
             if constexpr (x == HM - 1) read_q(v + 1, y, l);
+            if constexpr (n == N / 2) {
+                sa2 = read_sa(v + 1);
+                sb2 = read_sb(v + 1);
+            }
             constexpr int lo = n * kLP / N, hi = (n + 1) * kLP / N;
             for_each<hi - lo>([&](auto tc) { load_p(v + 2, s, 1, lo + decltype(tc)::value); });
             if constexpr (n == N - 1) put_scales(v + 2);
-            __builtin_amdgcn_sched_barrier(0);
         });
         border<kYoung>();
         sa = sa2;
@@ -779,7 +792,7 @@ Q8Cut q8_cut(const Q8Mat &a, bool ta, const Q8Mat &b, bool tb) {
     const int steps = static_cast<int>((K + kBK - 1) / kBK);
     Q8Cut c{};
     c.split = 1;
-    // (one row by 14336 x 4096: 15.2 us by tiles of 64; 32 rows 15.8)
+    // (one row by 14336 x 4096: 12.5 us for 15.2 by tiles of 64; 32 rows 15.8 either way)
     if (!ta && tb && M <= 32) {
         c.tile = 3;
     } else {
