@@ -537,45 +537,46 @@ __global__ __launch_bounds__(2048 / P) void q8_dequantize_kernel(Q8Mat Q, void *
 
 // One block's part on this rank a workgroup: 32 lanes take a row's 128 columns,
 // four each, without keeping them in the caches (a decoder block's shards on 8 ranks,
-// 122 MB: 27 -> 22 us; the copy-in after it, which reads them again, 24 -> 28).  Cells of entry -1 are blocks that other ranks hold alone: zeros.
+// 122 MB: 27 -> 22 us; the copy-in after it, which reads them again, 24 -> 28).  Cells
+// of entry -1 are blocks that other ranks hold alone: zeros.
 __global__ __launch_bounds__(kBlock) void block_scales_kernel(
     const BlockCell *__restrict__ cells, int64_t n_cells, const BlockEntry *__restrict__ blocks,
     const DevEntry *__restrict__ ents, uint8_t *__restrict__ scales) {
-  __shared__ uint32_t part[4];
-  for (int64_t k = blockIdx.x; k < n_cells; k += gridDim.x) {
-    const BlockCell cell = cells[k];
-    const int tid = threadIdx.x;
-    if (cell.entry < 0) {
-        for (int i = tid; i < cell.rows; i += kBlock) scales[cell.at + i] = 0;
-        continue;
-    }
-    const int64_t width = blocks[cell.entry].cols;
-    const float *p = ents[cell.entry].master + cell.row * width + cell.col;
-    const int64_t left = width - cell.col;
-    const int c = (tid & 31) * 4, n = left - c < 0 ? 0 : (left - c < 4 ? static_cast<int>(left - c) : 4);
-    const bool vec = n == 4 && (lo32(p) & 15u) == 0 && (width & 3) == 0;
-    uint32_t m = 0;
-    if (vec) {
-#pragma unroll 4
-        for (int r = tid >> 5; r < cell.rows; r += 8) {
-            const f32x4 v = ldp<1>(reinterpret_cast<const f32x4 *>(p + r * width + c));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m = umax(m, finite_mag(v[e]));
+    __shared__ uint32_t part[4];
+    for (int64_t k = blockIdx.x; k < n_cells; k += gridDim.x) {
+        const BlockCell cell = cells[k];
+        const int tid = threadIdx.x;
+        if (cell.entry < 0) {
+            for (int i = tid; i < cell.rows; i += kBlock) scales[cell.at + i] = 0;
+            continue;
         }
-    } else {
-        for (int r = tid >> 5; r < cell.rows; r += 8)
+        const int64_t width = blocks[cell.entry].cols;
+        const float *p = ents[cell.entry].master + cell.row * width + cell.col;
+        const int64_t left = width - cell.col;
+        const int c = (tid & 31) * 4, n = left - c < 0 ? 0 : (left - c < 4 ? static_cast<int>(left - c) : 4);
+        const bool vec = n == 4 && (lo32(p) & 15u) == 0 && (width & 3) == 0;
+        uint32_t m = 0;
+        if (vec) {
+#pragma unroll 4
+            for (int r = tid >> 5; r < cell.rows; r += 8) {
+                const f32x4 v = ldp<1>(reinterpret_cast<const f32x4 *>(p + r * width + c));
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < n) m = umax(m, finite_mag(p[r * width + c + e]));
+                for (int e = 0; e < 4; ++e) m = umax(m, finite_mag(v[e]));
+            }
+        } else {
+            for (int r = tid >> 5; r < cell.rows; r += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < n) m = umax(m, finite_mag(p[r * width + c + e]));
+        }
+        m = lane_max(m, 1, 64);
+        __syncthreads();            // the cell before is done with `part`
+        if ((tid & 63) == 0) part[tid >> 6] = m;
+        __syncthreads();
+        if (tid == 0)
+            scales[cell.at] = static_cast<uint8_t>(
+                scale_byte<FSDP_Q8_E4M3>(umax(umax(part[0], part[1]), umax(part[2], part[3]))));
     }
-    m = lane_max(m, 1, 64);
-    __syncthreads();            // the cell before is done with `part`
-    if ((tid & 63) == 0) part[tid >> 6] = m;
-    __syncthreads();
-    if (tid == 0)
-        scales[cell.at] = static_cast<uint8_t>(
-            scale_byte<FSDP_Q8_E4M3>(umax(umax(part[0], part[1]), umax(part[2], part[3]))));
-  }
 }
 
 // Row and column that lie d elements after column `col` of row `row`.
