@@ -22,7 +22,8 @@ BLOCKS = {"tensor": capi.FSDP_Q8_TENSOR, "rows": capi.FSDP_Q8_ROWS, "cols": capi
           "tiles": capi.FSDP_Q8_TILES}
 _DTYPES = {torch.bfloat16: capi.FSDP_DTYPE_BF16, torch.float32: capi.FSDP_DTYPE_F32}
 _HALF = (torch.bfloat16, torch.int16)      # the groups hold bf16 bits as int16
-_BYTES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+_FLOAT8 = {torch.float8_e4m3fn: "e4m3", torch.float8_e5m2: "e5m2"}
+_BYTES = (torch.uint8, *_FLOAT8)
 
 
 def _up(n: int, to: int) -> int:
@@ -64,8 +65,8 @@ def _rows_of(t: torch.Tensor, what: str, dtypes) -> int:
 
 
 class Q8:
-    """A matrix in 8 bits.  ``codes`` [rows, cols] of uint8 (or a float8 dtype),
-    rows contiguous; ``scales`` uint8, one line for each 128 of the matrix as
+    """A matrix in 8 bits.  ``codes`` [rows, cols] of uint8 (or the float8 dtype of
+    ``format``), rows contiguous; ``scales`` uint8, one line for each 128 of the matrix as
     ``scale_lines`` says, or None with blocks "tensor"; ``divisor``: one fp32 on
     the GPU by which values are divided (the FP8 copy-in's per-parameter scale).
     It is a view: it keeps the tensors, and reads them when it is used."""
@@ -76,6 +77,8 @@ class Q8:
     def __init__(self, codes: torch.Tensor, scales: Optional[torch.Tensor], blocks: str,
                  format: str = "e4m3", divisor: Optional[torch.Tensor] = None):
         kind, fmt = _known(BLOCKS, blocks, "blocks"), _known(FORMATS, format, "format")
+        if _FLOAT8.get(codes.dtype, format) != format:
+            raise ValueError(f"{codes.dtype} codes are not {format}")
         ld = _rows_of(codes, "codes", _BYTES)
         rows, cols = codes.shape
         lines, length = scale_lines(rows, cols, blocks)
