@@ -265,18 +265,29 @@ class Linear8:
     "e4m3" or "e5m2" (more range, one bit less) for dy."""
 
     def __init__(self, weight: Q8, grad_format: str = "e4m3"):
+        _known(FORMATS, grad_format, "grad_format")
+        self.weight, self.grad_format = weight, grad_format
+        self.saved = []
+
+    @property
+    def weight(self) -> Q8:
+        """It may be replaced between steps, by one of another place or size too."""
+        return self._weight
+
+    @weight.setter
+    def weight(self, weight: Q8) -> None:
         if weight.blocks not in ("tiles", "tensor"):
             raise ValueError("the weight must be in blocks of 128 x 128, or in none")
         if weight.format != "e4m3":
             raise ValueError("the weight must be E4M3")
-        _known(FORMATS, grad_format, "grad_format")
-        self.weight, self.grad_format = weight, grad_format
-        self.saved = []
-        self._bytes = {}
+        self._weight = weight
+        self._bytes = {}            # by tokens: they follow from the weight's sides and place too
 
     def _workspace(self, tokens: int, stream):
         n = self._bytes.get(tokens)
         if n is None:
+            if len(self._bytes) >= 4096:
+                self._bytes.clear()
             n = self._bytes[tokens] = capi.fsdp_q8_linear_workspace(self.weight.c, tokens)
         dev = self.weight.device
         return _take(lambda: torch.empty(n, dtype=torch.uint8, device=dev), stream), n

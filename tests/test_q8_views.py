@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-pytest.importorskip("sharded_shard_amd.capi")
+capi = pytest.importorskip("sharded_shard_amd.capi")
 from sharded_shard_amd import q8  # noqa: E402
 
 
@@ -17,3 +17,41 @@ def test_a_float8_type_is_its_format(dtype, named, blocks):
     if named == "e4m3":
         with pytest.raises(ValueError, match="float8.* codes are not e4m3"):
             q8.Q8(t.view(dtype), scales, blocks)
+
+
+def empty(rows, cols, blocks="tiles", format="e4m3"):
+    return q8.Q8.empty((rows, cols), blocks, format, device="cpu")
+
+
+def odd(rows, cols):
+    """A weight whose codes lie at an odd address: products copy it into their workspace."""
+    q = empty(rows, cols)
+    c = capi.Q8Struct.from_buffer_copy(q.c)
+    c.codes, c.ld = c.codes + 1, c.ld + 1
+    q.c, q.aligned = c, False
+    return q
+
+
+def test_another_weight_has_its_own_workspace():
+    """What a layer keeps about its weight goes when the weight does."""
+    layer = q8.Linear8(empty(256, 512))
+    ws, n = layer._workspace(64, None)
+    assert n == ws.numel() == capi.fsdp_q8_linear_workspace(layer.weight.c, 64)
+    for w in (odd(256, 512), empty(1024, 512), empty(256, 512)):
+        layer.weight = w
+        ws, n = layer._workspace(64, None)
+        assert n == ws.numel() == capi.fsdp_q8_linear_workspace(w.c, 64)
+    assert layer.weight is w
+    # the constructor's checks
+    with pytest.raises(ValueError, match="blocks"):
+        layer.weight = empty(256, 512, "rows")
+    with pytest.raises(ValueError, match="E4M3"):
+        layer.weight = empty(256, 512, "tiles", "e5m2")
+    assert layer.weight is w
+
+
+def test_what_a_layer_keeps_does_not_grow_without_end():
+    layer = q8.Linear8(empty(1, 16))
+    for tokens in range(1, 5000):
+        layer._workspace(tokens, None)
+    assert len(layer._bytes) <= 4096
