@@ -52,10 +52,11 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
 
 // x over a caller's scale, which may leave it past fmax, or past fp32: clamped there;
 // the comparisons keep NaN.  x - x is 0, or NaN where x is not finite: an infinity is
-// no value that a code could stand in for.
+// no value that a code could stand in for.  It is subtracted, since -0 - 0 is -0 (-0 + 0
+// is not).
 __device__ __forceinline__ float clamped(float x, float inverse) {
     const float y = x * inverse;
-    return (y > 448.0f ? 448.0f : (y < -448.0f ? -448.0f : y)) + (x - x);
+    return (y > 448.0f ? 448.0f : (y < -448.0f ? -448.0f : y)) - (x - x);
 }
 
 // Four codes of values that fit.

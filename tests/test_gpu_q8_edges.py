@@ -1,0 +1,63 @@
+"""8-bit matrices on the GPU, at the edges: signs of zero, single rows far apart,
+checkpoints at odd addresses."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import q8 as Q
+
+pytestmark = pytest.mark.gpu
+
+capi = pytest.importorskip("sharded_shard_amd.capi")
+from sharded_shard_amd import q8  # noqa: E402
+from sharded_shard_amd.group import ShardedGroup  # noqa: E402
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+def zeros_of_both_signs(rows, cols):
+    """Every third element a zero, of either sign; also values that round to one."""
+    g = np.random.default_rng([rows, cols])
+    x = g.standard_normal((rows, cols)).astype(np.float32)
+    pick = g.integers(0, 6, (rows, cols))
+    x[pick == 0], x[pick == 1] = 0.0, -0.0
+    x[pick == 2] *= np.float32(2.0 ** -40)
+    return x
+
+
+@pytest.mark.parametrize("shape", [(130, 40), (256, 384), (33, 129)], ids=str)
+def test_copy_in_keeps_the_sign_of_zero(shape):
+    """The codes themselves, as the quantiser makes them."""
+    x = zeros_of_both_signs(*shape)
+    g = ShardedGroup([shape], 1, 0)
+    g.shard_view(g.master_flat, 0).copy_(torch.from_numpy(x.reshape(-1)))
+    scales = torch.empty(g.n_block_scales, dtype=torch.uint8, device=DEV)
+    seg = torch.empty(g.S, dtype=torch.uint8, device=DEV)
+    g.block_scales(scales)
+    g.pack_fp8_blocks(seg, scales)
+    codes, _ = Q.quantize(x, "tiles", "e4m3")
+    assert np.array_equal(codes & 128, np.signbit(x) * 128)
+    assert np.array_equal(seg.cpu().numpy()[:x.size].reshape(shape), codes)
+    g.close()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(130, 40), (256, 384), (33, 129)], ids=str)
+def test_the_quantiser_keeps_the_sign_of_zero(shape, dtype, fmt):
+    x = torch.from_numpy(zeros_of_both_signs(*shape)).to(DEV, dtype)
+    h = x.double().cpu().numpy()
+    for blocks in ("rows", "cols", "tiles"):
+        codes, _ = Q.quantize(h, blocks, fmt)
+        assert np.array_equal(codes & 128, np.signbit(h) * 128)
+        assert np.array_equal(q8.quantize(x, blocks, fmt).codes_view().cpu().numpy(), codes)
+    for q, blocks in zip(q8.quantize(x, "both", fmt), ("rows", "cols")):
+        assert np.array_equal(q.codes_view().cpu().numpy(), Q.quantize(h, blocks, fmt)[0])
