@@ -109,7 +109,8 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     const size_t n = p->L.entries.size();
     std::vector<int64_t> own;
     for (const fsdp_shard_entry_t &t : p->L.entries) own.push_back(t.row_begin * t.cols);
-    const fsdp::Blocks blocks = fsdp::blocks_of(p->L);
+    // (a bind after the first upload sends the entries alone: it makes no blocks)
+    const fsdp::Blocks blocks = p->tiles_uploaded ? fsdp::Blocks{} : fsdp::blocks_of(p->L);
     struct Table {
         void **dst;
         const void *src;
@@ -165,9 +166,11 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     }
     e = hipStreamSynchronize(st);
     if (e != hipSuccess) return hip_fail(e, (c + ": upload").c_str());
-    p->tiles_uploaded = true;
-    p->n_cells = static_cast<int64_t>(blocks.cells.size());
-    p->n_block_scales = blocks.total;
+    if (!p->tiles_uploaded) {
+        p->n_cells = static_cast<int64_t>(blocks.cells.size());
+        p->n_block_scales = blocks.total;
+        p->tiles_uploaded = true;
+    }
     p->host_entries = std::move(ents);
     p->bound = prev | roles;
     return FSDP_OK;
