@@ -462,7 +462,7 @@ fsdp_status fsdp_q8_linear_backward(const fsdp_q8_t *w, const fsdp_q8_t *saved, 
 }
 
 fsdp_status fsdp_plan_block_scales(const fsdp_plan *p, int32_t i, int64_t *offset,
-                                   int64_t *total) {
+                                   int64_t *total) try {
     const char *call = "fsdp_plan_block_scales";
     if (p == nullptr || offset == nullptr || total == nullptr)
         return set_error(FSDP_E_INVAL, std::string(call) + ": null argument");
@@ -476,6 +476,8 @@ fsdp_status fsdp_plan_block_scales(const fsdp_plan *p, int32_t i, int64_t *offse
         *total += down(p->L.entries[k].rows) * down(p->L.entries[k].cols);
     }
     return FSDP_OK;
+} catch (...) {
+    return FSDP_E_NOMEM;
 }
 
 }  // extern "C"

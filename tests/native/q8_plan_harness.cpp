@@ -11,9 +11,11 @@
 
 namespace {
 size_t g_allocated = 0;     // bytes asked for since it was last set to 0
+bool g_none_left = false;   // every allocation fails
 }
 void *operator new(size_t n) {
     g_allocated += n;
+    if (g_none_left) throw std::bad_alloc();
     if (void *p = std::malloc(n > 0 ? n : 1)) return p;
     throw std::bad_alloc();
 }
@@ -55,10 +57,39 @@ void bind_again() {
     for (float *p : master) std::free(p);
 }
 
+// No exception leaves a C entry, not even where there is no memory for its message.
+void out_of_memory() {
+    const int64_t rows[1] = {130}, cols[1] = {70};
+    fsdp_plan *plan = nullptr;
+    must(fsdp_plan_create(rows, cols, 1, 1, 0, 1, &plan) == FSDP_OK, "plan");
+    int64_t at = 0, total = 0;
+    fsdp_q8_t q{};
+    q.rows = -1;
+    g_none_left = true;
+    const fsdp_status got[] = {
+        fsdp_plan_block_scales(plan, 7, &at, &total),
+        fsdp_plan_block_scales(nullptr, 0, &at, &total),
+        fsdp_q8_quantize(&q, FSDP_DTYPE_BF16, 0, &q, nullptr, nullptr),
+        fsdp_q8_dequantize(&q, &q, FSDP_DTYPE_BF16, 0, nullptr),
+        fsdp_q8_product_workspace(&q, 0, &q, 0, &at),
+        fsdp_q8_product(&q, 0, &q, 0, nullptr, 0, nullptr, 0, nullptr),
+        fsdp_q8_linear_workspace(&q, 1, &at),
+        fsdp_q8_linear_forward(&q, &q, 0, 0, 1, nullptr, nullptr, 0, nullptr, 0, nullptr),
+        fsdp_q8_linear_backward(&q, &q, &q, 0, 0, 0, nullptr, 0, nullptr, 0, nullptr, 0, nullptr),
+        fsdp_block_scales_shard(plan, nullptr, nullptr),
+        fsdp_pack_allgather_fp8_blocks(plan, nullptr, nullptr, nullptr),
+    };
+    g_none_left = false;
+    for (fsdp_status s : got) must(s == FSDP_E_NOMEM, "no memory");
+    must(fsdp_plan_block_scales(plan, 0, &at, &total) == FSDP_OK && total == 2, "after");
+    fsdp_plan_destroy(plan);
+}
+
 }  // namespace
 
 int main() {
     bind_again();
+    out_of_memory();
     std::printf("ALL OK\n");
     return 0;
 }
