@@ -99,7 +99,7 @@ fsdp_status need_roles(const fsdp_plan *p, int32_t roles, const char *call) {
 // tables; the device block is allocated the first time) on `st`, then record
 // the newly bound roles.
 fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32_t roles,
-                           hipStream_t st, const char *call) {
+                           hipStream_t st, const char *call) try {
     const std::string c(call);
     int dev = -1;
     hipError_t e = hipGetDevice(&dev);
@@ -174,6 +174,8 @@ fsdp_status commit_entries(fsdp_plan *p, std::vector<fsdp::DevEntry> ents, int32
     p->host_entries = std::move(ents);
     p->bound = prev | roles;
     return FSDP_OK;
+} catch (const std::bad_alloc &) {
+    return FSDP_E_NOMEM;    // (the blocks of a one-column parameter are many)
 }
 
 }  // namespace

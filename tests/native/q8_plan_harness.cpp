@@ -11,11 +11,11 @@
 
 namespace {
 size_t g_allocated = 0;     // bytes asked for since it was last set to 0
-bool g_none_left = false;   // every allocation fails
+size_t g_most = SIZE_MAX;   // an allocation of more fails
 }
 void *operator new(size_t n) {
     g_allocated += n;
-    if (g_none_left) throw std::bad_alloc();
+    if (n > g_most) throw std::bad_alloc();
     if (void *p = std::malloc(n > 0 ? n : 1)) return p;
     throw std::bad_alloc();
 }
@@ -43,6 +43,12 @@ void bind_again() {
     must(fsdp_plan_block_scales(plan, 0, &at, &total) == FSDP_OK, "block scales");
     must(total == 8192 + 1024, "blocks");
     std::vector<uint8_t> scales(total);
+    // no memory for the blocks: the plan stays as it was
+    g_most = static_cast<size_t>(total);
+    must(fsdp_bind(plan, master.data(), nullptr, nullptr, nullptr, nullptr, nullptr) == FSDP_E_NOMEM,
+         "no memory for the blocks");
+    g_most = SIZE_MAX;
+    must(fsdp_block_scales_shard(plan, scales.data(), nullptr) == FSDP_E_STATE, "not bound");
     for (int turn = 0; turn < 3; ++turn) {
         g_allocated = 0;
         must(fsdp_bind(plan, master.data(), nullptr, nullptr, nullptr, nullptr, nullptr) == FSDP_OK,
@@ -65,7 +71,7 @@ void out_of_memory() {
     int64_t at = 0, total = 0;
     fsdp_q8_t q{};
     q.rows = -1;
-    g_none_left = true;
+    g_most = 0;
     const fsdp_status got[] = {
         fsdp_plan_block_scales(plan, 7, &at, &total),
         fsdp_plan_block_scales(nullptr, 0, &at, &total),
@@ -79,7 +85,7 @@ void out_of_memory() {
         fsdp_block_scales_shard(plan, nullptr, nullptr),
         fsdp_pack_allgather_fp8_blocks(plan, nullptr, nullptr, nullptr),
     };
-    g_none_left = false;
+    g_most = SIZE_MAX;
     for (fsdp_status s : got) must(s == FSDP_E_NOMEM, "no memory");
     must(fsdp_plan_block_scales(plan, 0, &at, &total) == FSDP_OK && total == 2, "after");
     fsdp_plan_destroy(plan);
