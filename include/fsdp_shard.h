@@ -610,6 +610,13 @@ fsdp_status fsdp_q8_dequantize(const fsdp_q8_t *q, void *out, int32_t dtype, int
 fsdp_status fsdp_q8_product_workspace(const fsdp_q8_t *a, int32_t trans_a, const fsdp_q8_t *b,
                                       int32_t trans_b, int64_t *bytes);
 
+/* How the product is cut up (host only): `tile`, the side of the square of results a
+ * block makes (256, 128 or 64; 0: the path for up to 32 rows of x W^T), and
+ * `split`, the stretches of the sum that are added in a second launch (1: none).
+ * For tests and measurements; it follows from sizes, not from contents. */
+fsdp_status fsdp_q8_product_cut(const fsdp_q8_t *a, int32_t trans_a, const fsdp_q8_t *b,
+                                int32_t trans_b, int32_t *tile, int32_t *split);
+
 /* out [M, N] bf16, a row ldo elements after the other, = op(a) op(b): op turns a
  * matrix over where trans is 1.  y = x W^T: trans_b; dx = dy W: neither; dW =
  * dy^T x: trans_a.  A matrix that the sum runs along the rows of is in blocks

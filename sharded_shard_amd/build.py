@@ -35,6 +35,7 @@ SOURCES = [
     ("muon.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
     ("ortho.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
     ("q8.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
+    ("q8_cut.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I" + os.path.join(ROCM, "include")]),
     ("copy.hip", ["-x", "hip"] + DEVICE),
     ("pack.hip", ["-x", "hip"] + DEVICE),
     ("reduce.hip", ["-x", "hip"] + DEVICE),

@@ -180,6 +180,7 @@ _SIGS = {
     "fsdp_q8_quantize": (_i32, [_P, _i32, _i64, _Q8, _Q8, _P]),
     "fsdp_q8_dequantize": (_i32, [_Q8, _P, _i32, _i64, _P]),
     "fsdp_q8_product_workspace": (_i32, [_Q8, _i32, _Q8, _i32, ctypes.POINTER(_i64)]),
+    "fsdp_q8_product_cut": (_i32, [_Q8, _i32, _Q8, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]),
     "fsdp_q8_product": (_i32, [_Q8, _i32, _Q8, _i32, _P, _i64, _P, _i64, _P]),
     "fsdp_q8_linear_workspace": (_i32, [_Q8, _i64, ctypes.POINTER(_i64)]),
     "fsdp_q8_linear_forward": (_i32, [_Q8, _P, _i32, _i64, _i64, _Q8, _P, _i64, _P, _i64, _P]),
@@ -778,6 +779,14 @@ def fsdp_q8_product_workspace(a: Q8Struct, trans_a: int, b: Q8Struct, trans_b: i
     _check(lib.fsdp_q8_product_workspace(ctypes.byref(a), trans_a, ctypes.byref(b), trans_b,
                                          ctypes.byref(n)), "fsdp_q8_product_workspace")
     return n.value
+
+
+def fsdp_q8_product_cut(a: Q8Struct, trans_a: int, b: Q8Struct, trans_b: int):
+    """(tile, split): how the product is cut up."""
+    t, n = _i32(), _i32()
+    _check(lib.fsdp_q8_product_cut(ctypes.byref(a), trans_a, ctypes.byref(b), trans_b,
+                                   ctypes.byref(t), ctypes.byref(n)), "fsdp_q8_product_cut")
+    return t.value, n.value
 
 
 def fsdp_q8_product(a: Q8Struct, trans_a: int, b: Q8Struct, trans_b: int, out, ldo: int,

@@ -334,6 +334,22 @@ fsdp_status fsdp_q8_product_workspace(const fsdp_q8_t *a, int32_t trans_a, const
     return FSDP_E_NOMEM;
 }
 
+fsdp_status fsdp_q8_product_cut(const fsdp_q8_t *a, int32_t trans_a, const fsdp_q8_t *b,
+                                int32_t trans_b, int32_t *tile, int32_t *split) try {
+    const char *call = "fsdp_q8_product_cut";
+    Q8Mat A{}, B{};
+    fsdp_status s = check_product(a, trans_a, b, trans_b, call, &A, &B);
+    if (s != FSDP_OK) return s;
+    if (tile == nullptr || split == nullptr)
+        return set_error(FSDP_E_INVAL, std::string(call) + ": null tile or split");
+    const fsdp::Q8Cut cut = fsdp::q8_cut(A, trans_a != 0, B, trans_b != 0);
+    *tile = fsdp::kQ8TileSide[cut.tile];
+    *split = cut.split;
+    return FSDP_OK;
+} catch (...) {
+    return FSDP_E_NOMEM;
+}
+
 fsdp_status fsdp_q8_product(const fsdp_q8_t *a, int32_t trans_a, const fsdp_q8_t *b,
                             int32_t trans_b, uint16_t *out, int64_t ldo, void *workspace,
                             int64_t workspace_bytes, void *stream) try {

@@ -91,9 +91,98 @@ void out_of_memory() {
     fsdp_plan_destroy(plan);
 }
 
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t down(int64_t n) { return (n + 127) / 128; }
+
+// A matrix whose codes end with their memory, `at` bytes past a multiple of 256 and rows
+// `more` past a multiple of 16 bytes apart.
+struct Mat {
+    fsdp_q8_t q{};
+    std::vector<void *> held;
+    Mat(int64_t r, int64_t c, int blocks, int64_t at, int64_t more) {
+        q.rows = r, q.cols = c, q.ld = up(c, 16) + more, q.blocks = blocks;
+        const int64_t lines = blocks == FSDP_Q8_ROWS ? down(c) : down(r);
+        const int64_t length = blocks == FSDP_Q8_ROWS ? r : blocks == FSDP_Q8_COLS ? c : down(c);
+        q.pitch = up(length, 4);
+        q.codes = get(at + (r > 0 ? (r - 1) * q.ld + c : 0)) + at;
+        q.scales = get(lines > 0 ? (lines - 1) * q.pitch + length : 0);
+    }
+    uint8_t *get(int64_t n) {
+        void *p = nullptr;
+        if (posix_memalign(&p, 256, n > 0 ? n : 1) != 0) std::abort();
+        held.push_back(p);
+        return static_cast<uint8_t *>(p);
+    }
+    ~Mat() {
+        for (void *p : held) std::free(p);
+    }
+    Mat(const Mat &) = delete;
+};
+
+// The linear steps in exactly the memory that they ask for, with the weight and the
+// checkpoint at every alignment: the copies of operands, the quantised ones and the
+// stretches' sums of each product lie inside it.
+void linear(int64_t tokens, int64_t out, int64_t in, int32_t format) {
+    for (int where = 0; where < 9; ++where) {
+        const int64_t at[3] = {0, 1, 16}, more[3] = {0, 5, 16};
+        Mat w(out, in, FSDP_Q8_TILES, at[where / 3], more[where / 3]);
+        Mat saved(tokens, in, FSDP_Q8_COLS, at[where % 3], more[where % 3]);
+        int64_t need = 0;
+        must(fsdp_q8_linear_workspace(&w.q, tokens, &need) == FSDP_OK, "workspace");
+        uint8_t *ws = w.get(need);
+        std::vector<uint16_t> x(tokens * in + 1), y(tokens * out + 1), dy(tokens * out + 1),
+            dx(tokens * in + 1), dw(out * in + 1);
+        must(fsdp_q8_linear_forward(&w.q, x.data(), FSDP_DTYPE_BF16, in, tokens, &saved.q, y.data(),
+                                    out, ws, need, nullptr) == FSDP_OK,
+             "forward");
+        for (int which = 1; which < 4; ++which)
+            must(fsdp_q8_linear_backward(&w.q, &saved.q, dy.data(), FSDP_DTYPE_BF16, out, format,
+                                         which & 1 ? dx.data() : nullptr, in,
+                                         which & 2 ? dw.data() : nullptr, in, ws, need,
+                                         nullptr) == FSDP_OK,
+                 "backward");
+    }
+}
+
+// One product in exactly its memory; the tile and the stretches it is cut into.
+void product(int64_t m, int64_t n, int64_t k, int ta, int tb, int64_t at, int64_t more) {
+    Mat a(ta ? k : m, ta ? m : k, ta ? FSDP_Q8_COLS : FSDP_Q8_ROWS, at, more);
+    Mat b(tb ? n : k, tb ? k : n, FSDP_Q8_TILES, at, more);
+    int64_t need = 0;
+    int32_t tile = -1, split = 0;
+    must(fsdp_q8_product_workspace(&a.q, ta, &b.q, tb, &need) == FSDP_OK, "workspace");
+    must(fsdp_q8_product_cut(&a.q, ta, &b.q, tb, &tile, &split) == FSDP_OK, "cut");
+    must(tile == 256 || tile == 128 || tile == 64 || (tile == 0 && m <= 32 && !ta && tb), "tile");
+    must(split >= 1 && split <= 16 && (split == 1 || 2 * split * 128 <= up(k, 128)), "split");
+    const int64_t copies = up(up(a.q.cols, 16) * a.q.rows, 256) + up(up(b.q.cols, 16) * b.q.rows, 256);
+    must(need >= (split > 1 ? 4 * m * n * split : 0), "the stretches' sums");
+    must(need <= (split > 1 ? 4 * m * n * split : 0) + copies, "no more");
+    if (at == 1) must(need >= copies, "the copies of both operands");
+    std::vector<uint16_t> out(m * n + 1);
+    must(fsdp_q8_product(&a.q, ta, &b.q, tb, out.data(), n, a.get(need), need, nullptr) == FSDP_OK,
+         "product");
+}
+
 }  // namespace
 
 int main() {
+    for (int32_t f : {FSDP_Q8_E4M3, FSDP_Q8_E5M2}) {
+        linear(70, 260, 515, f);
+        linear(1, 1, 1, f);
+        linear(300, 128, 256, f);
+        linear(0, 40, 50, f);
+        linear(1100, 100, 36, f);
+        linear(3000, 64, 48, f);
+    }
+    for (int form = 0; form < 3; ++form)
+        for (int odd = 0; odd < 2; ++odd) {
+            product(1, 1, 1, form == 2, form == 0, odd, 5 * odd);
+            product(32, 500, 300, form == 2, form == 0, odd, 5 * odd);
+            product(33, 500, 3000, form == 2, form == 0, odd, 5 * odd);
+            product(256, 250, 9000, form == 2, form == 0, odd, 5 * odd);
+            product(2000, 1030, 260, form == 2, form == 0, odd, 5 * odd);
+            product(3520, 5824, 130, form == 2, form == 0, odd, 5 * odd);
+        }
     bind_again();
     out_of_memory();
     std::printf("ALL OK\n");

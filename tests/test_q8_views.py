@@ -1,4 +1,6 @@
 """8-bit matrices as Python holds them: what a view is taken for (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -55,3 +57,22 @@ def test_what_a_layer_keeps_does_not_grow_without_end():
     for tokens in range(1, 5000):
         layer._workspace(tokens, None)
     assert len(layer._bytes) <= 4096
+
+
+def test_how_a_product_is_cut_up():
+    """The sizes whose tiles the GPU tests rely on; refusals as the product's."""
+    cut = lambda m, n, k, ta, tb: capi.fsdp_q8_product_cut(
+        empty(*((k, m) if ta else (m, k)), "cols" if ta else "rows").c, int(ta),
+        empty(*((n, k) if tb else (k, n)), "tiles").c, int(tb))
+    assert cut(1, 14336, 4096, False, True) == cut(32, 64, 128, False, True) == (0, 1)
+    for ta, tb in ((False, True), (False, False), (True, False)):
+        assert cut(8192, 4096, 4096, ta, tb) == (256, 1)
+        assert cut(3520, 5824, 384, ta, tb) == (256, 1)
+        assert cut(64, 64, 256, ta, tb)[0] == 64
+        assert cut(256, 256, 8200, ta, tb)[1] > 1
+    with pytest.raises(capi.FsdpError):
+        capi.fsdp_q8_product_cut(empty(4, 16, "rows").c, 1, empty(4, 16).c, 1)
+    lib, n = capi.lib, ctypes.c_int32()
+    a, b = empty(4, 16, "rows").c, empty(4, 16).c
+    assert lib.fsdp_q8_product_cut(a, 0, b, 1, None, ctypes.byref(n)) == capi.FSDP_E_INVAL
+    assert lib.fsdp_q8_product_cut(None, 0, b, 1, ctypes.byref(n), ctypes.byref(n)) == capi.FSDP_E_INVAL
