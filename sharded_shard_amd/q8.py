@@ -24,6 +24,7 @@ _DTYPES = {torch.bfloat16: capi.FSDP_DTYPE_BF16, torch.float32: capi.FSDP_DTYPE_
 _HALF = (torch.bfloat16, torch.int16)      # the groups hold bf16 bits as int16
 _FLOAT8 = {torch.float8_e4m3fn: "e4m3", torch.float8_e5m2: "e5m2"}
 _BYTES = (torch.uint8, *_FLOAT8)
+_MOST = 1 << 22             # rows, columns and leading dimensions
 
 
 def _up(n: int, to: int) -> int:
@@ -61,6 +62,8 @@ def _rows_of(t: torch.Tensor, what: str, dtypes) -> int:
         if rows > 1:
             raise ValueError(f"{what}: rows overlap")
         return cols
+    if rows == 1 and down > _MOST:      # the last of a long sequence: no row follows
+        return _up(cols, 16)
     return down
 
 

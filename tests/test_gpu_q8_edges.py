@@ -61,3 +61,34 @@ def test_the_quantiser_keeps_the_sign_of_zero(shape, dtype, fmt):
         assert np.array_equal(q8.quantize(x, blocks, fmt).codes_view().cpu().numpy(), codes)
     for q, blocks in zip(q8.quantize(x, "both", fmt), ("rows", "cols")):
         assert np.array_equal(q.codes_view().cpu().numpy(), Q.quantize(h, blocks, fmt)[0])
+
+
+@pytest.mark.parametrize("stride", [1100 * 4096, 1100 * 4096 + 1])
+def test_one_row_however_far_the_next_would_be(stride):
+    """The last token of a long sequence, [1, tokens, width][:, -1]: its stride is the sequence's."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    flat = torch.randn(stride + 4096, generator=g, device=DEV).bfloat16()
+    row = flat.as_strided((1, 4096), (stride, 1), 8)
+    same = row.clone()
+    w = q8.quantize(torch.randn(300, 4096, generator=g, device=DEV).bfloat16(), "tiles")
+    for blocks in ("rows", "cols", "tiles"):
+        a, b = q8.quantize(row, blocks), q8.quantize(same, blocks)
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+        out = torch.zeros_like(flat).as_strided((1, 4096), (stride, 1), 3)
+        assert torch.equal(q8.dequantize(a, out=out), q8.dequantize(b))
+    codes = torch.zeros(stride + 4096, dtype=torch.uint8, device=DEV).as_strided((1, 4096), (stride, 1), 0)
+    a = q8.quantize(same, "rows")
+    codes.copy_(a.codes)
+    far = q8.Q8(codes, a.scales, "rows")
+    want = q8.product(a, w, trans_b=True)
+    assert torch.equal(q8.product(far, w, trans_b=True), want)
+    assert torch.equal(q8.dequantize(far), q8.dequantize(a))
+    out = torch.zeros(stride, dtype=torch.bfloat16, device=DEV).as_strided((1, 300), (stride, 1), 0)
+    assert torch.equal(q8.product(a, w, trans_b=True, out=out), want)
+    one, two = q8.Linear8(w), q8.Linear8(w)
+    assert torch.equal(one.forward(row, out=out), two.forward(same))
+    dy = torch.randn(stride, generator=g, device=DEV).bfloat16().as_strided((1, 300), (stride, 1), 0)
+    dw = [torch.empty(300, 4096, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    dx = torch.zeros(stride, dtype=torch.bfloat16, device=DEV).as_strided((1, 4096), (stride, 1), 0)
+    assert torch.equal(one.backward(dy, dw[0], out=dx), two.backward(dy.clone(), dw[1]))
+    assert torch.equal(*dw)
