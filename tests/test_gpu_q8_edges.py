@@ -92,3 +92,31 @@ def test_one_row_however_far_the_next_would_be(stride):
     dx = torch.zeros(stride, dtype=torch.bfloat16, device=DEV).as_strided((1, 4096), (stride, 1), 0)
     assert torch.equal(one.backward(dy, dw[0], out=dx), two.backward(dy.clone(), dw[1]))
     assert torch.equal(*dw)
+
+
+@pytest.mark.parametrize("at,more", [(1, 0), (3, 5), (16, 1), (8, 16)])
+@pytest.mark.parametrize("tokens", [40, 333, 1500])
+def test_backward_of_a_checkpoint_at_any_address(tokens, at, more):
+    """The native step with a caller's own checkpoint, in exactly its workspace: the bits of the
+    separate calls on one that lies as Linear8 lays it."""
+    n, k = 260, 515
+    g = torch.Generator(device=DEV).manual_seed(tokens)
+    x, dy = (torch.randn(tokens, c, generator=g, device=DEV).bfloat16() for c in (k, n))
+    w = q8.quantize(torch.randn(n, k, generator=g, device=DEV).bfloat16(), "tiles")
+    saved = q8.quantize(x, "cols")
+    ld = -(-k // 16) * 16 + more
+    codes = torch.full((at + tokens * ld,), 0x7F, dtype=torch.uint8, device=DEV)
+    codes = codes[at:].view(tokens, ld)[:, :k]
+    codes.copy_(saved.codes)
+    far = q8.Q8(codes, saved.scales, "cols")
+    need = capi.fsdp_q8_linear_workspace(w.c, tokens)
+    buf = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device=DEV)
+    ws = buf[256:256 + need]
+    dx = torch.empty(tokens, k, dtype=torch.bfloat16, device=DEV)
+    dw = torch.empty(n, k, dtype=torch.bfloat16, device=DEV)
+    capi.fsdp_q8_linear_backward(w.c, far.c, dy.data_ptr(), capi.FSDP_DTYPE_BF16, n, capi.FSDP_Q8_E4M3,
+                                 dx.data_ptr(), k, dw.data_ptr(), k, ws.data_ptr(), need)
+    dr, dc = q8.quantize(dy, "both")
+    assert torch.equal(dx, q8.product(dr, w))
+    assert torch.equal(dw, q8.product(dc, saved, trans_a=True))
+    assert (buf[:256] == 0x5A).all() and (buf[256 + need:] == 0x5A).all()
