@@ -575,7 +575,9 @@ enum { FSDP_Q8_TENSOR = 0, FSDP_Q8_ROWS = 1, FSDP_Q8_COLS = 2, FSDP_Q8_TILES = 3
  * codes at any address (16-byte aligned with ld a multiple of 16: no copy
  * before a product); for ROWS and COLS scales 4-byte aligned and pitch a
  * multiple of 4; divisor one fp32 on the device, or NULL for 1.  Bytes between
- * cols and ld, and between a line's last block and pitch, are not written. */
+ * cols and ld, and between a line's last block and pitch, are not written.
+ * Outputs share no memory with a call's other arguments; matrices side by side in
+ * the same rows (equal distances from row to row) share none. */
 typedef struct fsdp_q8_t {
     uint8_t *codes;
     uint8_t *scales;

@@ -19,17 +19,24 @@ bool misaligned(const void *p, uintptr_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
 }
 
-// A stretch of memory.
+// A stretch of memory: all of its bytes, or rows of `width` of them, `pitch` apart.
 struct Span {
     const void *p;
     int64_t bytes;
     const char *name;
+    int64_t width = 0, pitch = 0;
 };
 
 bool overlap(const Span &a, const Span &b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.bytes > 0 && b.bytes > 0 && x < y + static_cast<uintptr_t>(b.bytes) &&
-           y < x + static_cast<uintptr_t>(a.bytes);
+    if (a.bytes <= 0 || b.bytes <= 0 || x >= y + static_cast<uintptr_t>(b.bytes) ||
+        y >= x + static_cast<uintptr_t>(a.bytes))
+        return false;
+    if (a.pitch == 0 || a.pitch != b.pitch) return true;
+    // side by side in the same rows: b starts after a's part of a row and ends with it
+    const uintptr_t pitch = static_cast<uintptr_t>(a.pitch);
+    const uintptr_t from = y >= x ? (y - x) % pitch : (pitch - (x - y) % pitch) % pitch;
+    return from < static_cast<uintptr_t>(a.width) || from + static_cast<uintptr_t>(b.width) > pitch;
 }
 
 int64_t down(int64_t n) { return (n + kQ8Block - 1) / kQ8Block; }
@@ -53,11 +60,11 @@ Lines scale_lines(const fsdp_q8_t &q) {
 }
 
 Span codes_of(const fsdp_q8_t &q, const char *name) {
-    return {q.codes, extent(q.rows, q.cols, q.ld, 1), name};
+    return {q.codes, extent(q.rows, q.cols, q.ld, 1), name, q.cols, q.ld};
 }
 Span scales_of(const fsdp_q8_t &q, const char *name) {
     const Lines l = scale_lines(q);
-    return {q.scales, extent(l.n, l.length, q.pitch, 1), name};
+    return {q.scales, extent(l.n, l.length, q.pitch, 1), name, l.length, q.pitch};
 }
 
 fsdp_status bad(fsdp_status s, const char *call, const char *name, const char *what) {
@@ -106,7 +113,7 @@ fsdp_status check_wide(const void *p, int32_t dtype, int64_t rows, int64_t cols,
     const int64_t elem = dtype == FSDP_DTYPE_F32 ? 4 : 2;
     if (ld < cols) return bad(FSDP_E_INVAL, call, name, "leading dimension below the row's length");
     if (ld > kQ8MaxSide) return bad(FSDP_E_UNSUPPORTED, call, name, "leading dimension above 2^22");
-    *span = {p, extent(rows, cols, ld, elem), name};
+    *span = {p, extent(rows, cols, ld, elem), name, cols * elem, ld * elem};
     if (span->bytes > 0 && p == nullptr) return bad(FSDP_E_INVAL, call, name, "null");
     if (misaligned(p, static_cast<uintptr_t>(elem)))
         return bad(FSDP_E_ALIGN, call, name, "not aligned to its element");

@@ -163,9 +163,45 @@ void product(int64_t m, int64_t n, int64_t k, int ta, int tb, int64_t at, int64_
          "product");
 }
 
+// Matrices side by side in the same rows share no byte; those that do are refused.
+void side_by_side() {
+    const int64_t rows = 50, cols = 64, ld = 160;
+    std::vector<uint16_t> wide(rows * ld + 64);
+    const uint16_t *x = wide.data();
+    uint16_t *right = wide.data() + 64;
+    Mat q(rows, cols, FSDP_Q8_ROWS, 0, 0), s(rows, cols, FSDP_Q8_COLS, 0, 0);
+    Mat w(96, cols, FSDP_Q8_TILES, 0, 0), v(cols, cols, FSDP_Q8_TILES, 0, 0);
+    int64_t need = 0;
+    must(fsdp_q8_linear_workspace(&w.q, rows, &need) == FSDP_OK, "workspace");
+    uint8_t *ws = w.get(need);
+    must(fsdp_q8_linear_forward(&w.q, x, FSDP_DTYPE_BF16, ld, rows, &s.q, right, ld, ws, need,
+                                nullptr) == FSDP_OK,
+         "y to the right of x");
+    must(fsdp_q8_linear_backward(&w.q, &s.q, right, FSDP_DTYPE_BF16, ld, FSDP_Q8_E4M3, wide.data(), ld,
+                                 nullptr, 0, ws, need, nullptr) == FSDP_OK,
+         "dx to the left of dy");
+    must(fsdp_q8_linear_forward(&w.q, x, FSDP_DTYPE_BF16, ld, rows, nullptr, right - 1, ld, ws, need,
+                                nullptr) == FSDP_E_INVAL,
+         "one element shared");
+    must(fsdp_q8_linear_forward(&w.q, x, FSDP_DTYPE_BF16, ld, rows, nullptr, right + 1, ld, ws, need,
+                                nullptr) == FSDP_E_INVAL,
+         "one element of the next row shared");
+    must(fsdp_q8_linear_forward(&w.q, x, FSDP_DTYPE_BF16, ld, rows, nullptr, right, ld + 1, ws, need,
+                                nullptr) == FSDP_E_INVAL,
+         "rows of other lengths");
+    // codes of two matrices in the same rows, and of one in the columns it is read from
+    Mat two(rows, 2 * cols, FSDP_Q8_ROWS, 0, 0);
+    q.q.codes = two.q.codes, s.q.codes = two.q.codes + cols;
+    q.q.ld = s.q.ld = two.q.ld;
+    must(fsdp_q8_quantize(x, FSDP_DTYPE_BF16, ld, &q.q, &s.q, nullptr) == FSDP_OK, "codes side by side");
+    s.q.codes -= 1;
+    must(fsdp_q8_quantize(x, FSDP_DTYPE_BF16, ld, &q.q, &s.q, nullptr) == FSDP_E_INVAL, "codes shared");
+}
+
 }  // namespace
 
 int main() {
+    side_by_side();
     for (int32_t f : {FSDP_Q8_E4M3, FSDP_Q8_E5M2}) {
         linear(70, 260, 515, f);
         linear(1, 1, 1, f);

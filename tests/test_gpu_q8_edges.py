@@ -120,3 +120,22 @@ def test_backward_of_a_checkpoint_at_any_address(tokens, at, more):
     assert torch.equal(dx, q8.product(dr, w))
     assert torch.equal(dw, q8.product(dc, saved, trans_a=True))
     assert (buf[:256] == 0x5A).all() and (buf[256 + need:] == 0x5A).all()
+
+
+def test_results_beside_their_operands():
+    """x, y, dy and dx as columns of one buffer: each written without a byte of the others."""
+    t, n, k = 130, 96, 72
+    g = torch.Generator(device=DEV).manual_seed(3)
+    buf = torch.randn(t, k + n + n + k, generator=g, device=DEV).bfloat16()
+    x, y, dy, dx = buf.split((k, n, n, k), 1)
+    was = buf.clone()
+    w = q8.quantize(torch.randn(n, k, generator=g, device=DEV).bfloat16(), "tiles")
+    layer, alone = q8.Linear8(w), q8.Linear8(w)
+    dw = [torch.empty(n, k, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    want_y = alone.forward(x.clone())
+    want_dx = alone.backward(dy.clone(), dw[1])
+    assert torch.equal(layer.forward(x, out=y), want_y)
+    assert torch.equal(layer.backward(dy, dw[0], out=dx), want_dx) and torch.equal(*dw)
+    assert torch.equal(buf[:, :k], was[:, :k]) and torch.equal(dy, was[:, k + n:k + 2 * n])
+    with pytest.raises(capi.FsdpError):
+        layer.forward(x, out=buf[:, k - 1:k - 1 + n])
