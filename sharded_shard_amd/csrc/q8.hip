@@ -668,37 +668,46 @@ __global__ __launch_bounds__(kBlock) void pack_fp8_blocks_kernel(
 
 dim3 blocks_of(const Q8Mat &m) { return dim3((m.cols + 127) / 128, (m.rows + 127) / 128); }
 
-// Rows a thread: two, 16 waves a block, where the blocks are few and a thread's own time
-// counts; eight where there are enough to fill the CUs.
-bool few(const dim3 &grid) { return grid.x * grid.y < 1024u; }
+// Rows a thread: two, 16 waves a block, where there are fewer than `kTwo` blocks and a
+// thread's own time counts; eight, four waves, where there are more.  Along rows 16 waves
+// are faster until the CUs are full (256 blocks of bf16 3.6 us for 4.5, 512 4.8 for 5.3,
+// 1024 10.1 for 9.4; fp32 alike).  Down columns, the waves' maxima meet in LDS, where 16
+// cost four times what four do, and a second block no longer fits beside a first: both ways
+// 32 blocks 5.1 for 5.8, 256 6.3 for 6.7, 288 9.5 for 7.2; columns alone 4.5 for 4.4, 5.2
+// for 4.9, 7.9 for 5.5.  Of fp32 1,024 threads have not the registers for it as well (both
+// ways 32 blocks 14.7 for 6.2, 512 33.0 for 11.4), and eight rows are right throughout.
+template <bool kF32, int WHAT>
+constexpr unsigned kTwo = WHAT == kWriteRows             ? 1024u
+                          : kF32 || WHAT == kWriteCols ? 0u
+                                                         : 257u;
 
-template <int FMT, bool kF32, int P>
-void quantize(const void *x, int64_t ldx, const Q8Mat &a, const Q8Mat *b, dim3 grid,
-              hipStream_t st) {
-    const Q8Mat none{};
-    constexpr int kThreads = 2048 / P;
-    if (b != nullptr)
-        q8_quantize_kernel<FMT, kF32, kWriteRows | kWriteCols, P>
-            <<<grid, kThreads, 0, st>>>(x, ldx, a, *b);
-    else if (a.blocks == FSDP_Q8_ROWS)
-        q8_quantize_kernel<FMT, kF32, kWriteRows, P><<<grid, kThreads, 0, st>>>(x, ldx, a, none);
-    else if (a.blocks == FSDP_Q8_COLS)
-        q8_quantize_kernel<FMT, kF32, kWriteCols, P><<<grid, kThreads, 0, st>>>(x, ldx, a, none);
-    else
-        q8_quantize_kernel<FMT, kF32, kWriteTiles, P><<<grid, kThreads, 0, st>>>(x, ldx, a, none);
+template <int FMT, bool kF32, int WHAT>
+void quantize(const void *x, int64_t ldx, const Q8Mat &a, const Q8Mat &b, hipStream_t st) {
+    const dim3 grid = blocks_of(a);
+    if constexpr (kTwo<kF32, WHAT> > 0) {
+        if (grid.x * grid.y < kTwo<kF32, WHAT>) {
+            q8_quantize_kernel<FMT, kF32, WHAT, 2><<<grid, 1024, 0, st>>>(x, ldx, a, b);
+            return;
+        }
+    }
+    q8_quantize_kernel<FMT, kF32, WHAT, 8><<<grid, 256, 0, st>>>(x, ldx, a, b);
 }
 
 template <int FMT, bool kF32>
 void quantize(const void *x, int64_t ldx, const Q8Mat &a, const Q8Mat *b, hipStream_t st) {
-    const dim3 grid = blocks_of(a);
-    if (few(grid)) quantize<FMT, kF32, 2>(x, ldx, a, b, grid, st);
-    else quantize<FMT, kF32, 8>(x, ldx, a, b, grid, st);
+    const Q8Mat none{};
+    if (b != nullptr) quantize<FMT, kF32, kWriteRows | kWriteCols>(x, ldx, a, *b, st);
+    else if (a.blocks == FSDP_Q8_ROWS) quantize<FMT, kF32, kWriteRows>(x, ldx, a, none, st);
+    else if (a.blocks == FSDP_Q8_COLS) quantize<FMT, kF32, kWriteCols>(x, ldx, a, none, st);
+    else quantize<FMT, kF32, kWriteTiles>(x, ldx, a, none, st);
 }
 
 template <int FMT, bool kF32, bool kDiv>
 void dequantize(const Q8Mat &q, void *out, int64_t ldo, hipStream_t st) {
     const dim3 grid = blocks_of(q);
-    if (few(grid)) q8_dequantize_kernel<FMT, kF32, 2, kDiv><<<grid, 1024, 0, st>>>(q, out, ldo);
+    // as above, along rows (512 blocks of bf16 6.9 us either way, 256 5.0 for 5.4, 1024 11.6
+    // for 10.8)
+    if (grid.x * grid.y < 1024u) q8_dequantize_kernel<FMT, kF32, 2, kDiv><<<grid, 1024, 0, st>>>(q, out, ldo);
     else q8_dequantize_kernel<FMT, kF32, 8, kDiv><<<grid, 256, 0, st>>>(q, out, ldo);
 }
 
