@@ -537,9 +537,11 @@ __global__ __launch_bounds__(2048 / P) void q8_dequantize_kernel(Q8Mat Q, void *
 // ---------------------------------------------------------------------------
 
 // One block's part on this rank a workgroup: 32 lanes take a row's 128 columns,
-// four each, without keeping them in the caches (a decoder block's shards on 8 ranks,
-// 122 MB: 27 -> 22 us; the copy-in after it, which reads them again, 24 -> 28).  Cells
-// of entry -1 are blocks that other ranks hold alone: zeros.
+// four each, without keeping them in the caches.  Of a decoder block's shards on 8 ranks,
+// 122 MB, that takes 22 us for 24, and with the copy-in right after it, which then reads
+// them from memory, 55 for 54; with 512 MB of other work's writes between the two, as a
+// step has its collective there, 68 for 88.  Cells of entry -1 are blocks that other ranks
+// hold alone: zeros.
 __global__ __launch_bounds__(kBlock) void block_scales_kernel(
     const BlockCell *__restrict__ cells, int64_t n_cells, const BlockEntry *__restrict__ blocks,
     const DevEntry *__restrict__ ents, uint8_t *__restrict__ scales) {
@@ -705,8 +707,8 @@ void quantize(const void *x, int64_t ldx, const Q8Mat &a, const Q8Mat *b, hipStr
 template <int FMT, bool kF32, bool kDiv>
 void dequantize(const Q8Mat &q, void *out, int64_t ldo, hipStream_t st) {
     const dim3 grid = blocks_of(q);
-    // as above, along rows (512 blocks of bf16 6.9 us either way, 256 5.0 for 5.4, 1024 11.6
-    // for 10.8)
+    // as above, nothing meeting in LDS (by columns to bf16, 64 blocks 3.4 us for 4.1, 512 6.3
+    // for 6.4, 1024 11.0 for 10.6, 2048 18.4 for 16.9; other blocks and fp32 alike)
     if (grid.x * grid.y < 1024u) q8_dequantize_kernel<FMT, kF32, 2, kDiv><<<grid, 1024, 0, st>>>(q, out, ldo);
     else q8_dequantize_kernel<FMT, kF32, 8, kDiv><<<grid, 256, 0, st>>>(q, out, ldo);
 }

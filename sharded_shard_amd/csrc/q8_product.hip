@@ -790,8 +790,12 @@ hipError_t launch_q8_product(const Q8Mat &a, bool ta, const Q8Mat &b, bool tb, u
     } else if (cut.tile == 2) {
         launch<64, 64, 2, 1>(A, ta, B, tb, a.format, out, K, st);
     } else {
-        // columns a block: enough blocks for every CU, or loads enough for one
-        const bool wide = N >= 32 * 256;
+        // Columns a block: 16 while every CU has at most one such block, then 32 (K = 4096, one
+        // row and 32: 4096 columns 4.9 us for 6.8 and 7.9 for 9.9 with 32, 4112 6.8 either way
+        // and 10.3 for 13.3 with 16, 8192 7.0 for 7.4 and 10.4 for 14.0, 14336 12.9 for 13.8 and
+        // 18.3 for 25.2; of one row by 8193 to 12288, three turns for two, 16 would take 9.5
+        // to 10.0 for 10.9).
+        const bool wide = N > 16 * 256;
         if (M <= 16) wide ? launch_few<1, 2>(A, B, a.format, out, K, st)
                           : launch_few<1, 1>(A, B, a.format, out, K, st);
         else wide ? launch_few<2, 2>(A, B, a.format, out, K, st)
