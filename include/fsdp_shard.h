@@ -613,7 +613,7 @@ fsdp_status fsdp_q8_product_workspace(const fsdp_q8_t *a, int32_t trans_a, const
                                       int32_t trans_b, int64_t *bytes);
 
 /* How the product is cut up (host only): `tile`, the side of the square of results a
- * block makes (256, 128 or 64; 0: the path for up to 32 rows of x W^T), and
+ * block makes (256, 128 or 64; 0: the path for few rows, up to 32 of x W^T), and
  * `split`, the stretches of the sum that are added in a second launch (1: none).
  * For tests and measurements; it follows from sizes, not from contents. */
 fsdp_status fsdp_q8_product_cut(const fsdp_q8_t *a, int32_t trans_a, const fsdp_q8_t *b,

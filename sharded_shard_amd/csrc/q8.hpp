@@ -98,8 +98,8 @@ hipError_t launch_pack_fp8_blocks(const PackTile *tiles, int64_t n, const BlockE
                                   const DevEntry *ents, uint8_t *ag_in, const uint8_t *scales,
                                   hipStream_t st);
 
-// Sides of the results a block makes, by Q8Cut::tile; the last has up to 32 rows of them
-// and takes the sum in eight stretches of its own.
+// Sides of the results a block makes, by Q8Cut::tile; the last is for up to 32 rows of x W^T,
+// whose sums eight waves of a block share.
 constexpr int32_t kQ8TileSide[4] = {256, 128, 64, 0};
 
 // How a product is cut up, by its sizes, alignment and strides alone (q8_cut.cpp).

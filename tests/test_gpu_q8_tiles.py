@@ -119,12 +119,22 @@ def test_long_sums_of_whole_numbers_are_exact(mnk, want, ta, tb):
     check_whole(*mnk, ta, tb, "e4m3", "tiles", 2, 2, want)
 
 
-@pytest.mark.parametrize("mnk", [(1, 64, 128), (5, 33, 47), (16, 1000, 256), (17, 9000, 130),
-                                 (32, 129, 1024), (20, 8200, 4100)], ids=str)
+@pytest.mark.parametrize("mnk", [(1, 64, 128), (5, 33, 47), (16, 1000, 256), (1, 5000, 4100),
+                                 (16, 6001, 900), (32, 129, 1024), (17, 4096, 1299), (32, 6000, 1024),
+                                 (20, 8190, 2100)], ids=str)
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_few_rows_of_whole_numbers_are_exact(mnk, fmt):
     for blocks_b in ("rows", "tiles"):
         check_whole(*mnk, False, True, fmt, blocks_b, 4, 4, (0, False, False))
+
+
+# (1 x 28000 is 438 tiles in four stretches, 1752 for the 1024 blocks that fit at once)
+@pytest.mark.parametrize("mnk,want", [((32, 256, 8192), (64, True, False)), ((17, 9000, 130), (64, False, False)),
+                                      ((20, 8200, 4100), (64, True, False)),
+                                      ((1, 28000, 8192), (64, True, True))], ids=str)
+def test_few_rows_by_tiles_of_whole_numbers_are_exact(mnk, want):
+    """Where tiles are faster: long sums, many columns."""
+    check_whole(*mnk, False, True, "e4m3", "tiles", 4, 4, want)
 
 
 # ---- what the instruction keeps ------------------------------------------------------

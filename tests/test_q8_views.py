@@ -65,6 +65,7 @@ def test_how_a_product_is_cut_up():
         empty(*((k, m) if ta else (m, k)), "cols" if ta else "rows").c, int(ta),
         empty(*((n, k) if tb else (k, n)), "tiles").c, int(tb))
     assert cut(1, 14336, 4096, False, True) == cut(32, 64, 128, False, True) == (0, 1)
+    assert cut(32, 28672, 8192, False, True)[0] == 64       # tiles read as many weights faster
     for ta, tb in ((False, True), (False, False), (True, False)):
         assert cut(8192, 4096, 4096, ta, tb) == (256, 1)
         assert cut(3520, 5824, 384, ta, tb) == (256, 1)
