@@ -12,6 +12,7 @@
 #include "q8.hpp"
 
 #include "device.hpp"
+#include "q8_device.hpp"
 
 namespace fsdp {
 
@@ -75,7 +76,6 @@ __device__ __forceinline__ uint32_t four_codes(float a, float b, float c, float 
 
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Four codes of four bf16 over a power of two, one instruction for two (equal to the
 // converter of fp32 on the quotient for every bf16 that fits and every scale).
@@ -421,12 +421,6 @@ __device__ __forceinline__ void code_values(uint32_t lo, uint32_t hi, float (&x)
             x[4 * h + 3] = __builtin_amdgcn_cvt_f32_bf8(w, 3);
         }
     }
-}
-
-// Two as bf16, to nearest even, by the instruction.
-__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // The same blocks and threads.  A code times its power of two is exact in

@@ -10,11 +10,15 @@
 // Inside the instruction eight neighbouring products at a time are aligned to
 // the largest of them and keep their bits down to 2^-13 of its power of two
 // (measured); the eights and the accumulator add in fp32.  An eight is so within
-// 7 2^-13 of its largest product, a sum within 1.5e-5 of its size for normal data,
-// far below the 2^-9 of the rounding to bf16 that follows.
+// 7 2^-13 of its largest product.  A sum is off by 1.5e-5 of its size on normal data
+// and 4.5e-5 where one channel in a hundred is twenty times the others (root mean
+// squares of fp32 sums of 8192), against up to 2^-8 in the rounding to bf16 that
+// follows; where products cancel, by up to 2^-10 of the sum of their magnitudes.  That
+// is the choice of 8-bit instructions: fp16 ones, exact here, run at half the rate.
 #include "q8.hpp"
 
 #include "device.hpp"
+#include "q8_device.hpp"
 
 namespace fsdp {
 
@@ -238,13 +242,6 @@ __device__ __forceinline__ Item item_of(int b, int tiles_m, int tiles_n, int spl
     o.from = static_cast<int>(static_cast<uint32_t>(steps * o.part) / static_cast<uint32_t>(split));
     o.to = static_cast<int>(static_cast<uint32_t>(steps * (o.part + 1)) / static_cast<uint32_t>(split));
     return o;
-}
-
-// Two results as bf16, to nearest even, by the instruction.
-__device__ __forceinline__ uint32_t two_bf16(float lo, float hi) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // Four neighbouring fp32 sums of row i from column j.
