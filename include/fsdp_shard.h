@@ -601,9 +601,9 @@ typedef struct fsdp_q8_t {
 fsdp_status fsdp_q8_quantize(const void *x, int32_t dtype, int64_t ldx, const fsdp_q8_t *a,
                              const fsdp_q8_t *b, void *stream);
 
-/* What q stands for, as bf16 or fp32, a row ldo elements after the other.  Exact
- * in fp32 (code times a power of two) but for results under 2^-149 and the
- * division by a divisor; bf16 is rounded once more, to nearest even.
+/* What q stands for, as bf16 or fp32, a row ldo elements after the other.  In fp32
+ * a code times a power of two is exact (infinite past 2^128), and rounded once
+ * where there is a divisor; bf16 is rounded once more, to nearest even.
  * Errors: as fsdp_q8_quantize. */
 fsdp_status fsdp_q8_dequantize(const fsdp_q8_t *q, void *out, int32_t dtype, int64_t ldo,
                                void *stream);
@@ -626,8 +626,12 @@ fsdp_status fsdp_q8_product_cut(const fsdp_q8_t *a, int32_t trans_a, const fsdp_
  * either is TENSOR.  `a` may be E5M2 (gradients), `b` is E4M3.
  *   Sums are fp32 of exact products, but that the matrix instruction drops, of
  * eight neighbouring products, what lies 2^-14 below the power of two of the
- * largest: a sum is off by at most 2^-10 of the sum of the products'
- * magnitudes, 1.5e-5 of the result for normal data.  It is rounded once to bf16.
+ * largest.  With the fp32 additions a sum of K is off by at most 7 2^-13 +
+ * (K/8 + K/128 + 24) 2^-24 of the sum of the products' magnitudes (2^-10 of it
+ * up to K = 15,000); on normal data by 1.5e-5 of the results' size, and by
+ * 4.5e-5 where one channel in a hundred is twenty times the others (root mean
+ * squares).  It is divided by the divisors as fp32 (a product with their rounded
+ * reciprocals) and rounded once to bf16, 2^-8.
  * The same call gives the same bits every time.
  *   workspace  device memory, 256-byte aligned, of at least
  *              fsdp_q8_product_workspace's bytes (NULL where that is 0).

@@ -37,7 +37,8 @@ double cost(const TileCost &t, int64_t side, int64_t M, int64_t N, int steps, in
 // Where there are many turns of the CUs, or waves have many steps, tiles with the sum in
 // stretches are faster: they read b at 6.2 TB/s, this path at 4.7.  A launch of tiles
 // counts 5 here.  Over 435 products (64 to 57344 columns, sums of 128 to 28672) the choice
-// takes 1.8% more than the better of the two on average, where this path for all took 12%:
+// takes 1.8% more than the better of the two on average, where this path for all takes 12%
+// (4% and 14% in a run after the one that gave the constants):
 // one row by 4096 x 4096 5.4 us and 9.6 by tiles, 32 rows 8.8 and 10.7; one row by 14336 x
 // 4096 13.4 and 15.8, 32 rows 19.5 and 17.1; by 28672 x 8192 46 and 38, 32 rows 64 and 38.
 double few_cost(int64_t M, int64_t N, int64_t K, int steps) {
